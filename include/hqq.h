@@ -387,6 +387,136 @@ int hqq_gemm_dx(const void* packed, const void* delta_fp16, const void* zero_fp1
 int hqq_gemv(const void* packed, const void* delta_fp16, const void* zero_fp16, int64_t N, int64_t K, int nbits,
              int group_size, int axis, const void* x_fp16, int64_t batch, void* y, int y_dtype, void* stream);
 
+/*
+ * Quantised key/value cache and the attention that reads it: the other half of a decode step's
+ * memory traffic next to the fused products above ("从压缩文件到一次前向"; the affine group format of
+ * "量化公式", its start only: a cache entry is written once, in microseconds, so there are no
+ * proximal rounds).  Not part of the page's method.
+ *
+ * Cache of one layer: num_pages pages of hqq_kv_page_bytes(...) bytes; a page holds page_size
+ * tokens of every KV head, one block per head.  Token slots are numbered page * page_size + offset
+ * (int64).  A group of group_size channels of one token and head keeps nbits-bit codes, a step and a
+ * floor (fp16), made in fp32 from the values x (NaN taken as 0, the rest held to +-65504, so every
+ * written entry is finite):
+ *   floor = fp16(min x), step = fp16(max(max x - floor, 0) * (1 / (2^nbits - 1))),
+ *   code = clip(rint((x - floor) * (1 / step)), 0, 2^nbits - 1)  (0 where step = 0),
+ * and stands for floor + code * step.
+ * Block layout (D = head_dim, b = nbits; in order, without gaps):
+ *   K codes     [page_size][h: 4][i: D/32][j: 8]: channel 32 i + 8 h + j of the token; for b = 4
+ *               the nibbles 0..7 of the 32-bit word (h, i) hold j = 0, 2, 4, 6, 1, 3, 5, 7
+ *   V codes     [page_size/4][r: 16][t: 4][j: D/16]: channel r D/16 + j of token 4 * index + t, j from the
+ *               low bits up
+ *   K metadata  [D/group_size][page_size] 32-bit words: step in the low half, floor in the high half
+ *   V metadata  the same
+ * Formats: head_dim 64 or 128, nbits 4 or 8, group_size 32, 64 or 128 (at most head_dim), page_size
+ * 16, 32, 64, 128 or 256; others return HQQ_ERR_UNSUPPORTED.
+ * Pages may start out with any contents: no call reads a token that has not been written, except
+ * where it is masked out, whatever its memory holds.
+ */
+typedef struct hqq_kv_cache {
+  void* pages; /* num_pages * hqq_kv_page_bytes(...) bytes, 16-byte aligned */
+  int64_t num_pages;
+  int num_kv_heads, head_dim, nbits, group_size, page_size;
+} hqq_kv_cache;
+
+/* Types of keys, values, queries and outputs. */
+#define HQQ_KV_F16 0
+#define HQQ_KV_BF16 1
+
+/* Bytes of one page, or 0 when the format is not supported. */
+size_t hqq_kv_page_bytes(int num_kv_heads, int head_dim, int nbits, int group_size, int page_size);
+
+/*
+ * Quantises the keys and values of n tokens into their slots.
+ *   k, v       in  [n, num_kv_heads, head_dim] of dtype, channels contiguous, token and head strides
+ *              in elements (multiples of 8; 16-byte aligned pointers), e.g. slices of a fused projection.
+ *   slots      in  int64 [n], distinct; a slot outside the cache (negative, say) is skipped.
+ *   k_echo, v_echo  out (both or neither) [n, num_kv_heads, head_dim] contiguous of dtype: the values
+ *              the cache stands for (also of skipped tokens), rounded once: what a prompt's own attention
+ *              takes to see the keys that later steps will see.
+ * n = 0 does nothing.
+ */
+typedef struct hqq_kv_write_args {
+  hqq_kv_cache cache;
+  int dtype;
+  const void* k;
+  const void* v;
+  int64_t n, k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+  const int64_t* slots;
+  void* k_echo;
+  void* v_echo;
+  void* stream;
+} hqq_kv_write_args;
+int hqq_kv_write(const hqq_kv_write_args* args);
+
+/*
+ * Reads slots back: k, v out [n, num_kv_heads, head_dim] contiguous of dtype, floor + code * step in
+ * fp32 rounded once; zeros for a slot outside the cache.  slots may repeat.
+ */
+typedef struct hqq_kv_read_args {
+  hqq_kv_cache cache;
+  int dtype;
+  int64_t n;
+  const int64_t* slots;
+  void* k;
+  void* v;
+  void* stream;
+} hqq_kv_read_args;
+int hqq_kv_read(const hqq_kv_read_args* args);
+
+/*
+ * Attention of query tokens over their sequences' cached keys and values:
+ *   o[i, h] = sum_j p_j v[j, h'] / sum_j p_j,  p_j = exp(scale * q[i, h] . k[j, h']),  h' = h / (num_q_heads / num_kv_heads),
+ * with k and v what the cache stands for.
+ *   q          in  [total_q, num_q_heads, head_dim] of dtype, channels contiguous, strides as for k
+ *              above; num_q_heads a multiple of num_kv_heads.
+ *   cu_q       in  int32 [num_seqs + 1] (device): sequence b has the query tokens cu_q[b] .. cu_q[b+1]-1, at
+ *              most max_q of them; NULL: total_q / num_seqs tokens each (which must divide).  Tokens
+ *              of no sequence, or of one whose range leaves the tensor or exceeds max_q, have undefined outputs.
+ *   page_table in  int32 [num_seqs, table_cols] (device), rows table_stride apart: a sequence's pages in order.
+ *              Tokens on a page outside the cache (-1, say) are masked out.
+ *   seq_lens   in  int32 [num_seqs] (device): cached tokens of each sequence, its query tokens included;
+ *              0 for none.  Limited to max_len (host; a bound the caller knows) and to the table.
+ *   causal     1: query token t of T stands at position seq_len - T + t and sees the keys up to it; 0: all.
+ *   scale      finite, > 0.
+ *   out        out [total_q, num_q_heads, head_dim] contiguous of dtype.  A row that sees no key is 0.
+ *   lse        out (nullable) float [total_q, num_q_heads]: log of the sum of exp(scale * q.k); -inf for no key.
+ *   workspace  at least hqq_kv_attention_workspace_bytes(args) bytes (may be 0), 16-byte aligned.
+ * Scores, maximum, sums and the join of key ranges are fp32; a code enters its product exactly
+ * (streamed rows) or as fp16(floor + code * step) (tiles of many rows); the softmax weights enter the
+ * value product in fp16.  Deterministic.
+ * prefix_table and prefix_len are 0 here; hqq_kv_attention_shared puts the first prefix_len (host) keys, on the
+ * int32 pages prefix_table (device), in front of every sequence's own keys: all query rows see all of
+ * them, and their own keys (seq_lens: own cached tokens) under the causal rule.  The prefix is
+ * read once for the rows of all sequences together.  prefix_len = 0 is allowed.
+ */
+typedef struct hqq_kv_attention_args {
+  hqq_kv_cache cache;
+  int dtype;
+  const void* q;
+  int64_t total_q, q_token_stride, q_head_stride;
+  int num_q_heads;
+  int64_t num_seqs;
+  const int32_t* cu_q;
+  int64_t max_q;
+  const int32_t* page_table;
+  int64_t table_stride, table_cols;
+  const int32_t* seq_lens;
+  int64_t max_len;
+  int causal;
+  float scale;
+  const int32_t* prefix_table;
+  int64_t prefix_len;
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+} hqq_kv_attention_args;
+size_t hqq_kv_attention_workspace_bytes(const hqq_kv_attention_args* args);
+int hqq_kv_attention(const hqq_kv_attention_args* args);
+int hqq_kv_attention_shared(const hqq_kv_attention_args* args);
+
 /* Static description of a status code. */
 const char* hqq_status_string(int status);
 

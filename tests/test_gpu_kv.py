@@ -1,0 +1,414 @@
+"""The quantised key/value cache and its attention against the plain implementation in tests/kv_plain.py.
+
+Tolerances, derived before the first run.  Cache: written bytes are equal (every operation of the format is
+one fp32 operation, rounded), and so are the values read back.  Attention, with u the output type's half
+unit (2^-11 fp16, 2^-8 bf16) and A the row's sum of weights times (|floor| + code * step):
+  weights and code * step are each rounded to fp16 (2^-11 at most), 2^-10 A; fp32 sums of D products and the
+  exponential add at most 2^-11 A at these magnitudes; so |error| <= u |o| + 2^-9 A.
+  Rows that run in tiles use keys rounded to fp16 (values too): a score then has independent errors of
+  standard deviation 2^-11/sqrt(3) times the root sum of squares of its terms; six of them, twice (numerator
+  and sum), times A are added for those calls."""
+import math
+
+import numpy as np
+import pytest
+
+from tests import kv_plain as kp
+from tests.gpu_common import say, torch_dev
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = [(64, 4, 32), (64, 4, 64), (64, 8, 32), (64, 8, 64), (128, 4, 32), (128, 4, 64), (128, 4, 128), (128, 8, 32),
+           (128, 8, 64), (128, 8, 128)]
+
+
+def lib():
+    import weight_only_quantization_amd as hq
+    return hq, torch_dev()
+
+
+def make_cache(hq, torch, f, num_pages, fill=0xFF):
+    """Pages filled with a byte (0xFF: NaN steps and floors wherever nothing is written)."""
+    pages = torch.full((num_pages, f.hkv, f.block), fill, dtype=torch.uint8, device="cuda")
+    assert hq.hqq_kv_page_bytes(f.hkv, f.d, f.bits, f.g, f.page) == f.hkv * f.block
+    return hq.KVCache(pages, f.hkv, f.d, f.bits, f.g, f.page)
+
+
+def values(rng, n, hkv, d, special=False):
+    k = (rng.normal(size=(n, hkv, d)) * np.exp(0.5 * rng.normal(size=d)) + rng.normal(size=d)).astype(np.float32)
+    v = rng.normal(size=(n, hkv, d)).astype(np.float32)
+    if special and n > 6:
+        k[0], v[0] = 0.0, -0.0                # flat groups
+        k[1], v[1] = 3.14159, -7.7
+        k[2, 0, 3], v[2, 0, 5] = np.nan, np.inf
+        k[3, -1, d - 1], v[3, -1, 0] = -np.inf, np.nan
+        k[4] *= 1e-6                          # subnormal steps
+        v[4] *= 1e-7
+        k[5] *= 1e4                           # wide groups
+        v[5] = 1000 + 0.25 * rng.normal(size=(hkv, d))   # a far floor
+    return k, v
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("d,bits,g", FORMATS)
+def test_write_and_read(d, bits, g, dtype):
+    hq, torch = lib()
+    dt = getattr(torch, dtype)
+    for page, hkv, n in ((16, 3, 37), (64, 1, 1), (256, 2, 70)):
+        say("kv write", d, bits, g, dtype, page, hkv, n)
+        f = kp.Fmt(hkv, d, bits, g, page)
+        rng = np.random.default_rng(d + bits + g + n)
+        cache = make_cache(hq, torch, f, 9, fill=0xA5)
+        want = cache.pages.cpu().numpy().copy()
+        k, v = (kp.to(x, dt) for x in values(rng, n, hkv, d, special=True))
+        slots = rng.permutation(9 * page)[:n].astype(np.int64)
+        if n > 8:
+            slots[6], slots[7], slots[8] = -1, 9 * page, -(1 << 40)      # outside the cache
+        kp.write(f, want, kp.as_f32(k), kp.as_f32(v), slots)
+        ke, ve = hq.hqq_kv_write(cache, k.cuda(), v.cuda(), torch.from_numpy(slots).cuda(), echo=True)
+        assert np.array_equal(cache.pages.cpu().numpy(), want)
+        ask = np.concatenate([slots, slots[:1], [1 << 50]])
+        kr, vr = hq.hqq_kv_read(cache, torch.from_numpy(ask).cuda(), dtype=dt)
+        for x, echo, back in ((k, ke, kr), (v, ve, vr)):
+            val = kp.to(kp.stands_for(*kp.quantise(kp.as_f32(x), bits, g)), torch.float32).to(dt)
+            assert torch.equal(echo.cpu(), val)
+            got = back.cpu()
+            there = torch.from_numpy((ask >= 0) & (ask < 9 * page))
+            assert torch.equal(got[:n][there[:n]], val[there[:n]])
+            assert torch.equal(got[n], got[0]) and not got[~there].any()
+
+
+def test_write_strides_and_quiet_write():
+    """k and v as slices of one projection (token stride), of a [head, token] tensor (head stride larger than
+    the token's), with and without the echo."""
+    hq, torch = lib()
+    f = kp.Fmt(2, 128, 4, 64, 32)
+    rng = np.random.default_rng(5)
+    n = 21
+    qkv = kp.to(rng.normal(size=(n, 10, 128)).astype(np.float32), torch.float16).cuda()
+    slots = torch.from_numpy(rng.permutation(96)[:n].astype(np.int64)).cuda()
+    a, b, c = (make_cache(hq, torch, f, 3, fill=0) for _ in range(3))
+    k, v = qkv[:, 6:8], qkv[:, 8:10]
+    assert hq.hqq_kv_write(a, k, v, slots) is None
+    hq.hqq_kv_write(b, k.contiguous(), v.contiguous(), slots, echo=True)
+    ht = k.transpose(0, 1).contiguous().transpose(0, 1)
+    assert ht.stride(0) == 128 and ht.stride(1) == 128 * n
+    hq.hqq_kv_write(c, ht, v, slots)
+    assert torch.equal(a.pages, b.pages) and torch.equal(a.pages, c.pages)
+    hq.hqq_kv_write(a, k[:0], v[:0], slots[:0])                # no token
+    assert torch.equal(a.pages, b.pages)
+    k0, v0 = hq.hqq_kv_read(a, slots[:0])
+    assert k0.shape == (0, 2, 128) and v0.shape == (0, 2, 128)
+
+
+# ------------------------------------------------------------------------------ attention
+
+class Scene:
+    """A cache with sequences of the given own lengths (and a prefix) on shuffled pages, and queries."""
+
+    def __init__(self, hq, torch, f, lens, new, per, dtype, prefix=0, seed=0, vscale=1.0, qscale=2.0, cols=None):
+        self.f, self.lens, self.new, self.prefix = f, lens, new, prefix
+        rng = np.random.default_rng(seed)
+        cols = cols if cols is not None else max(1, max(-(-n // f.page) for n in lens))
+        pre = -(-prefix // f.page)
+        count = len(lens) * cols + pre + 2
+        ids = rng.permutation(count)
+        self.table = ids[:len(lens) * cols].reshape(len(lens), cols).astype(np.int32)
+        self.prefix_table = ids[len(lens) * cols:len(lens) * cols + pre].astype(np.int32)
+        self.cache = make_cache(hq, torch, f, count)
+        self.dt = getattr(torch, dtype)
+        self.kv = []
+        for table, n in list(zip(self.table, lens)) + [(self.prefix_table, prefix)]:
+            k, v = values(rng, n, f.hkv, f.d)
+            k, v = kp.to(k, self.dt), kp.to(v * vscale, self.dt)
+            slots = np.array([int(table[j // f.page]) * f.page + j % f.page for j in range(n)], np.int64)
+            if n:
+                hq.hqq_kv_write(self.cache, k.cuda(), v.cuda(), torch.from_numpy(slots).cuda())
+            self.kv.append([kp.quantise(kp.as_f32(x), f.bits, f.g) for x in (k, v)])
+        self.q = kp.to((qscale * rng.normal(size=(sum(new), f.hkv * per, f.d))).astype(np.float32), self.dt)
+        self.per, self.scale = per, 1.0 / math.sqrt(f.d)
+
+    def dense(self, i):
+        out = []
+        for code, step, floor in self.kv[i]:
+            g = self.f.g
+            c = code.reshape(*step.shape, g).astype(np.float64) * step.astype(np.float64)[..., None]
+            m = floor.astype(np.float64)[..., None]
+            out += [(c + m).reshape(code.shape), (c + abs(m)).reshape(code.shape)]
+        return out  # k, |k|, v, |floor| + code * step
+
+    def expect(self, causal=True, hidden=None):
+        """out, lse, A and the scores' term sizes of all query tokens; hidden[b]: masked own keys."""
+        outs, at = [], 0
+        pk, _, pv, pa = self.dense(len(self.lens))
+        for b, (n, t) in enumerate(zip(self.lens, self.new)):
+            q = kp.as_f32(self.q[at:at + t]).astype(np.float64)
+            at += t
+            k, _, v, a = self.dense(b)
+            see = np.ones((t, n), bool)
+            if causal:
+                see = np.arange(n)[None] <= (n - t + np.arange(t))[:, None]
+            if hidden is not None:
+                see[:, hidden[b]] = False
+            see = np.concatenate([np.ones((t, self.prefix), bool), see], 1)
+            k, v, a = (np.concatenate(x) for x in ((pk, k), (pv, v), (pa, a)))
+            o, lse, _, terms = kp.attend(q, k, v, see, self.scale)
+            _, _, mag, _ = kp.attend(q, k, a, see, self.scale)
+            outs.append((o, lse, mag, terms))
+        return [np.concatenate(x) for x in zip(*outs)]
+
+
+def check(torch, got, lse, want, dt, tiles=False, what=""):
+    o, wl, mag, terms = want
+    u = 2.0 ** -11 if dt == torch.float16 else 2.0 ** -8
+    extra = 2 * 6 * 2.0 ** -11 / math.sqrt(3) * terms if tiles else 0 * terms
+    got = got.double().cpu().numpy()
+    assert np.isfinite(got).all(), what
+    tol = u * np.abs(o) + (2.0 ** -9 + extra)[..., None] * mag + 1e-7
+    err = np.abs(got - o)
+    assert (err <= tol).all(), "%s: error %.3g of tolerance %.3g" % (what, err.flat[(err / tol).argmax()], tol.flat[(err / tol).argmax()])
+    empty = np.isinf(wl)
+    assert (got[empty] == 0).all(), what
+    if lse is not None:
+        lse = lse.double().cpu().numpy()
+        assert np.array_equal(np.isinf(lse), empty) and (lse[empty] < 0).all(), what
+        lerr = np.abs(lse - wl)[~empty]
+        # fp32 scores (2^-24 of about 200 roundings of terms of this size) and the exponential's 2^-22
+        ltol = (1e-5 * (1 + np.abs(wl) + terms * 11.3) + extra / 2)[~empty]
+        assert (lerr <= ltol).all(), "%s: lse error %.3g of %.3g" % (what, lerr.max(), ltol.min())
+
+
+def cu(torch, new):
+    return torch.from_numpy(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)).cuda()
+
+
+def attend(hq, torch, s, shared=False, ragged=None, **kw):
+    t = torch.from_numpy(s.table).cuda()
+    lens = torch.tensor(s.lens, dtype=torch.int32, device="cuda")
+    ragged = len(set(s.new)) > 1 if ragged is None else ragged
+    kw.setdefault("max_len", max(s.lens))
+    if ragged:
+        kw.update(cu_q=cu(torch, s.new), max_q=kw.get("max_q", max(s.new)))
+    if shared:
+        return hq.hqq_kv_attention_shared(s.cache, s.q.cuda(), torch.from_numpy(s.prefix_table).cuda(), s.prefix, t, lens,
+                                          scale=s.scale, return_lse=True, **kw)
+    return hq.hqq_kv_attention(s.cache, s.q.cuda(), t, lens, scale=s.scale, return_lse=True, **kw)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("d,bits,g", FORMATS)
+def test_single_tokens(d, bits, g, dtype):
+    """One query token a sequence; lengths 0 and 1, around the 16- and 32-key tiles, several pages, several
+    splits; unwritten memory is NaN."""
+    hq, torch = lib()
+    for per, page in ((1, 16), (4, 64), (7, 256)):
+        say("kv single tokens", d, bits, g, dtype, per, page)
+        f = kp.Fmt(2, d, bits, g, page)
+        s = Scene(hq, torch, f, [0, 1, 15, 16, 17, 33, 129, 700], [1] * 8, per, dtype, seed=per + d)
+        o, lse = attend(hq, torch, s)
+        check(torch, o, lse, s.expect(), s.dt, what="single")
+
+
+@pytest.mark.parametrize("per,t", [(8, 2), (3, 5), (16, 1), (32, 1), (5, 4), (1, 16), (8, 5), (4, 33), (1, 130)])
+def test_several_tokens(per, t):
+    """Drafts and chunks, causal and not: rows of one and of several tiles; sequences shorter than their queries
+    leave rows empty."""
+    hq, torch = lib()
+    for d, bits, g, dtype in ((128, 4, 64, "float16"), (64, 8, 32, "bfloat16")):
+        say("kv several tokens", per, t, d, bits)
+        f = kp.Fmt(2, d, bits, g, 32)
+        s = Scene(hq, torch, f, [t + 300, t, max(0, t - 3), 0, t + 31], [t] * 5, per, dtype, seed=t)
+        for causal in (True, False):
+            o, lse = attend(hq, torch, s, causal=causal)
+            check(torch, o, lse, s.expect(causal), s.dt, tiles=per * t > 32, what="causal %s" % causal)
+
+
+def test_ragged_queries():
+    """cu_q: sequences with no, one and many query tokens in one call; the table wider than needed."""
+    hq, torch = lib()
+    f = kp.Fmt(2, 128, 4, 64, 16)
+    s = Scene(hq, torch, f, [50, 400, 0, 77, 300, 9], [1, 0, 0, 77, 20, 1], 4, "float16", seed=3, cols=40)
+    o, lse = attend(hq, torch, s, max_len=None)
+    check(torch, o, lse, s.expect(), s.dt, tiles=True, what="ragged")
+    # a sequence whose range leaves the query tensor gets no output, the others keep theirs
+    bad = cu(torch, s.new)
+    bad[-1] += 5
+    out = torch.full(s.q.shape, 7.0, dtype=s.dt, device="cuda")
+    hq.hqq_kv_attention(s.cache, s.q.cuda(), torch.from_numpy(s.table).cuda(),
+                        torch.tensor(s.lens, dtype=torch.int32, device="cuda"), scale=s.scale, cu_q=bad, max_q=77, max_len=400, out=out)
+    assert torch.equal(out[:-1], o[:-1])
+
+
+def test_missing_pages_and_bounds():
+    """Pages outside the cache mask their tokens; lengths beyond max_len or the table are limited."""
+    hq, torch = lib()
+    f = kp.Fmt(2, 128, 8, 128, 16)
+    s = Scene(hq, torch, f, [200, 64, 40], [1, 1, 1], 4, "float16", seed=11)
+    s.table[0, 3], s.table[0, 7], s.table[1, :], s.table[2, 0] = -1, 1 << 30, -5, s.cache.num_pages
+    hidden = [np.r_[48:64, 112:128], np.r_[0:64], np.r_[0:16]]
+    o, lse = attend(hq, torch, s)
+    check(torch, o, lse, s.expect(hidden=hidden), s.dt, what="missing pages")
+    cut = Scene(hq, torch, f, [96, 64, 40], [1, 1, 1], 4, "float16", seed=12)
+    want = cut.expect()
+    cut_lens, cut.lens = cut.lens, [1000, 64, 40]        # the table holds 96
+    o, lse = attend(hq, torch, cut, max_len=None)
+    check(torch, o, lse, want, cut.dt, what="length beyond the table")
+    cut.lens = [-3, 64, 40]
+    o, lse = attend(hq, torch, cut, max_len=64)
+    assert not o[0].any() and torch.isinf(lse[0]).all()
+    check(torch, o[1:], lse[1:], [x[1:] for x in want], cut.dt, what="negative length")
+
+
+@pytest.mark.parametrize("bits,vscale", [(4, 1e-5), (4, 300.0), (4, 9000.0), (8, 9000.0), (8, 1e-4)])
+def test_value_ranges(bits, vscale):
+    """Values of very small and very large steps (a 4-bit step of 64 and more passes fp16 times 1024)."""
+    hq, torch = lib()
+    for t in (1, 40):
+        f = kp.Fmt(1, 128, bits, 64, 32)
+        s = Scene(hq, torch, f, [150 + t, t + 30], [t, t], 2, "bfloat16", seed=21, vscale=vscale)
+        o, lse = attend(hq, torch, s)
+        if vscale < 1:   # steps near fp16's smallest numbers: absolute units of 2^-24 a weight
+            want = s.expect()
+            err = np.abs(o.double().cpu().numpy() - want[0])
+            assert (err <= 2.0 ** -8 * np.abs(want[0]) + 2.0 ** -9 * want[2] + 2.0 ** -24).all()
+        else:
+            check(torch, o, lse, s.expect(), s.dt, tiles=t > 16, what="vscale %g" % vscale)
+
+
+@pytest.mark.parametrize("qscale", [0.0, 1e-7, 30.0, 500.0])
+def test_query_ranges(qscale):
+    """Flat, ordinary and one-key softmaxes; a query row of NaN touches no other row."""
+    hq, torch = lib()
+    f = kp.Fmt(2, 128, 4, 64, 16)
+    s = Scene(hq, torch, f, [333, 90], [1, 1], 4, "bfloat16", seed=31, qscale=qscale)
+    o, lse = attend(hq, torch, s)
+    want = s.expect()
+    if qscale <= 1:
+        check(torch, o, lse, want, s.dt, what="qscale")
+    else:
+        # scores of hundreds: their fp32 error (2^-24 of about 200 roundings) moves the weights
+        want[3] = want[3] * 0
+        o64, _, mag, _ = want
+        err = np.abs(o.double().cpu().numpy() - o64)
+        assert (err <= 2.0 ** -8 * np.abs(o64) + (2.0 ** -9 + 4e-5 * qscale) * mag).all()
+    s.q[0, 3] = float("nan")
+    o2, _ = attend(hq, torch, s)
+    assert torch.isnan(o2[0, 3]).all()
+    o2[0, 3] = o[0, 3]
+    assert torch.equal(o2, o)
+
+
+@pytest.mark.parametrize("per,batch,t", [(1, 3, 1), (4, 2, 2), (4, 9, 1), (8, 9, 3)])
+def test_shared_prefix(per, batch, t):
+    """A prefix in front of every sequence equals attention over both parts together; prefixes of one token,
+    of odd lengths and none; own parts that are empty."""
+    hq, torch = lib()
+    for d, bits, g, dtype in ((128, 4, 64, "float16"), (64, 8, 64, "bfloat16"), (64, 4, 32, "float16")):
+        for prefix in (0, 1, 47, 300):
+            say("kv shared", per, batch, t, d, bits, prefix)
+            f = kp.Fmt(2, d, bits, g, 16)
+            lens = [(37 * i) % 90 for i in range(batch)]
+            s = Scene(hq, torch, f, lens, [t] * batch, per, dtype, prefix=prefix, seed=prefix + per)
+            o, lse = attend(hq, torch, s, shared=True)
+            check(torch, o, lse, s.expect(), s.dt, tiles=per * batch * t > 32, what="prefix %d" % prefix)
+
+
+def test_shared_ragged_queries():
+    hq, torch = lib()
+    f = kp.Fmt(2, 128, 4, 128, 64)
+    s = Scene(hq, torch, f, [20, 5, 130], [3, 1, 40], 4, "float16", prefix=100, seed=8)
+    o, lse = attend(hq, torch, s, shared=True)
+    check(torch, o, lse, s.expect(), s.dt, tiles=True, what="shared ragged")
+
+
+def test_query_strides_and_repeats():
+    """Queries as a slice of a fused projection; the same call twice gives the same bits, in the given output and
+    workspace too."""
+    hq, torch = lib()
+    f = kp.Fmt(2, 128, 4, 64, 64)
+    s = Scene(hq, torch, f, [2000, 1500, 3], [1, 1, 1], 4, "float16", seed=41)
+    t, lens = torch.from_numpy(s.table).cuda(), torch.tensor(s.lens, dtype=torch.int32, device="cuda")
+    a = hq.hqq_kv_attention(s.cache, s.q.cuda(), t, lens, max_len=2000)
+    wide = torch.zeros(3, 12, 128, dtype=s.dt, device="cuda")
+    wide[:, 2:10] = s.q.cuda()
+    ws = torch.full((64 << 20,), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(a)
+    b = hq.hqq_kv_attention(s.cache, wide[:, 2:10], t, lens, max_len=2000, out=out, workspace=ws)
+    assert b is out and torch.equal(a, b)
+    ht = s.q.cuda().transpose(0, 1).contiguous().transpose(0, 1)
+    assert torch.equal(hq.hqq_kv_attention(s.cache, ht, t, lens, max_len=2000), a)
+    none = hq.hqq_kv_attention(s.cache, s.q.cuda()[:0], t[:0], lens[:0], max_len=2000)
+    assert none.shape == (0, 8, 128)
+
+
+def test_cache_past_32_bits():
+    """Pages whose bytes lie past 2^32: written, read and attended at their own place."""
+    hq, torch = lib()
+    f = kp.Fmt(8, 128, 8, 64, 256)
+    page_bytes = f.hkv * f.block
+    num = (5 << 30) // page_bytes
+    say("kv past 32 bits", num, page_bytes)
+    cache = hq.hqq_kv_cache(num, 8, 128, 8, 64, 256)
+    rng = np.random.default_rng(51)
+    k, v = (kp.to(x, torch.float16) for x in values(rng, 300, 8, 128))
+    ids = np.array([num - 1, num // 2 + 3], np.int64)
+    slots = torch.from_numpy(np.array([ids[j // 256] * 256 + j % 256 for j in range(300)], np.int64)).cuda()
+    ke, ve = hq.hqq_kv_write(cache, k.cuda(), v.cuda(), slots, echo=True)
+    kr, vr = hq.hqq_kv_read(cache, slots)
+    assert torch.equal(ke, kr) and torch.equal(ve, vr)
+    small = hq.hqq_kv_cache(2, 8, 128, 8, 64, 256)
+    hq.hqq_kv_write(small, k.cuda(), v.cuda(), torch.arange(300, device="cuda"))
+    lens = torch.tensor([300], dtype=torch.int32, device="cuda")
+    for t in (1, 40):
+        q = kp.to(rng.normal(size=(t, 32, 128)).astype(np.float32), torch.float16).cuda()
+        a = hq.hqq_kv_attention(cache, q, torch.from_numpy(ids.astype(np.int32))[None].cuda(), lens)
+        b = hq.hqq_kv_attention(small, q, torch.arange(2, dtype=torch.int32, device="cuda")[None], lens)
+        assert torch.equal(a, b) and torch.isfinite(a).all()
+
+
+def test_side_stream_and_graph():
+    """Calls on a side stream while the current stream allocates and writes; a decode step (write, attention)
+    captured into a graph and replayed with new inputs, each replay against the eager calls."""
+    hq, torch = lib()
+    f = kp.Fmt(2, 128, 4, 64, 64)
+    s = Scene(hq, torch, f, [900, 31, 640], [1, 1, 1], 4, "float16", seed=61, prefix=500)
+    base, lse0 = attend(hq, torch, s, shared=True)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    outs = []
+    for rep in range(4):
+        outs.append(attend(hq, torch, s, shared=True, stream=side))
+        junk = [torch.full((1 << 20,), float(rep), device="cuda") for _ in range(8)]
+        del junk
+    side.synchronize()
+    torch.cuda.synchronize()
+    for o, lse in outs:
+        assert torch.equal(o, base) and torch.equal(lse, lse0)
+
+    rng = np.random.default_rng(62)
+    t = torch.from_numpy(s.table).cuda()
+    lens = torch.tensor(s.lens, dtype=torch.int32, device="cuda")
+    slots = torch.tensor([int(s.table[b, (n - 1) // 64]) * 64 + (n - 1) % 64 for b, n in enumerate(s.lens)], device="cuda")
+    q, k, v = (torch.zeros(3, n, 128, dtype=s.dt, device="cuda") for n in (8, 2, 2))
+
+    def step():
+        hq.hqq_kv_write(s.cache, k, v, slots)
+        return hq.hqq_kv_attention(s.cache, q, t, lens, max_len=960)
+
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        step()
+    torch.cuda.current_stream().wait_stream(warm)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for rep in range(4):
+        for x in (q, k, v):
+            x.copy_(kp.to(rng.normal(size=tuple(x.shape)).astype(np.float32), s.dt))
+        graph.replay()
+        got = out.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(got, step())
+        torch.cuda.synchronize()

@@ -6,7 +6,8 @@ product runs in the library's kernels.  There is no fallback: when the library i
 the import of a compute function raises.
 
 Names follow the C ABI (``include/hqq.h``): ``hqq_quantize``, ``hqq_dequantize``,
-``hqq_gemv_w4a16``, ``hqq_gemv`` (the other stored formats), plus the size queries.
+``hqq_gemv_w4a16``, ``hqq_gemv`` (the other stored formats), the quantised key/value cache and its
+attention (``hqq_kv_*``, module ``kv_cache``), plus the size queries.
 """
 from __future__ import annotations
 
@@ -37,6 +38,8 @@ EXPORTS = ("hqq_packed_bytes", "hqq_num_groups", "hqq_quantize_workspace_bytes",
            "hqq_quantize_v2", "hqq_quantize_v2_workspace_bytes",
            "hqq_dequantize", "hqq_gemv_w4a16", "hqq_gemm_workspace_bytes", "hqq_gemm_w4a16",
            "hqq_gemm_dx_workspace_bytes", "hqq_gemm_w4a16_dx", "hqq_gemm_dx", "hqq_gemv", "hqq_gemm",
+           "hqq_kv_page_bytes", "hqq_kv_write", "hqq_kv_read", "hqq_kv_attention_workspace_bytes", "hqq_kv_attention",
+           "hqq_kv_attention_shared",
            "hqq_release_workspaces", "hqq_status_string", "hqq_last_error")
 
 _lib = None
@@ -97,6 +100,7 @@ def load(path: str = LIB_PATH):
     lib.hqq_release_workspaces.restype = i32
     lib.hqq_last_error.argtypes = []
     lib.hqq_last_error.restype = ctypes.c_char_p
+    kv_cache.declare(lib)
     _lib = lib
     return lib
 
@@ -593,3 +597,10 @@ def probe_read(bufs, sink, unroll: int = 4, stream=None) -> int:
                                    _stream_ptr(stream)) != 0:
         raise RuntimeError("hqq_probe_read failed")
     return sum(nb)
+
+
+# ------------------------------------------------------------------------------ key/value cache
+
+from . import kv_cache  # noqa: E402
+from .kv_cache import (KVCache, hqq_kv_attention, hqq_kv_attention_shared, hqq_kv_cache, hqq_kv_page_bytes,  # noqa: E402,F401
+                       hqq_kv_read, hqq_kv_write)

@@ -25,6 +25,15 @@ int fail(int status, const char* fmt, ...) {
   return status;
 }
 
+}  // namespace
+
+// The calling thread's error message, for the entry points of other files.
+namespace hqq {
+int api_fail(int status, const char* message) { return fail(status, "%s", message); }
+}  // namespace hqq
+
+namespace {
+
 int device_fail(hipError_t e, const char* what) {
   return fail(HQQ_ERR_DEVICE, "%s: %s", what, hipGetErrorString(e));
 }

@@ -9,6 +9,9 @@
 
 namespace hqq {
 
+// Sets the calling thread's message of hqq_last_error and returns status.
+int api_fail(int status, const char* message);
+
 // Arguments of the quantizer kernels (passed by value in the kernel argument segment).
 struct SolveArgs {
   const __half* W;     // [rows, cols] fp16

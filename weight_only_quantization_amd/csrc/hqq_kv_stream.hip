@@ -1,0 +1,514 @@
+// Attention of a few query rows over a quantised key/value cache: one stream over the keys.
+//
+//   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - max),  k = m + c s,  v = m + c s per group.
+//
+// A wave owns 16 * NT rows (the query tokens and heads that share a KV head) and walks its keys in
+// steps of 32, without LDS: the cache is stored so that each lane's wide loads are operands of the
+// matrix unit.
+//   scores  S^T[key][row] = sum_g s_jg (sum_{d in g} c_jd q_d) + m_jg (sum_{d in g} q_d): the codes go
+//           in exactly, as fp16 subnormals c 2^-24 (a mask of the word is the operand; the other
+//           nibble of a byte is 16 c, its q carries 1/16), step and floor apply to the fp32 sums.
+//   softmax one pass, running maximum and sum in fp32; a lane holds 8 keys of one row.  The maximum is
+//           raised (and the sums rescaled) only when a score passes it by 2^5, so the cross-lane
+//           reduction is rare; the weights stay within fp16.
+//   values  O^T[channel][row] += (c s)[channel][key] p[key][row]: a lane's 8 scores are its operand as
+//           they are (keys keep their order inside the step).  c s is one fp16 rounding,
+//           fma(1024 + c, s, -1024 s); the floors enter as one more product, sum_j p_j m_j.
+//           p is rounded to fp16 (2^-12 relative, independent per key).
+// Keys of the next step are loaded before this step's arithmetic.  The four waves of a block take
+// every fourth step of the block's chunk and are joined through LDS; chunks are joined by k_join.
+#include "hqq_kv.h"
+
+namespace hqq {
+namespace kv {
+namespace {
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// mask and or in one instruction (its constants in registers)
+struct Masks {
+  uint32_t lo, hi;        // 0x000f000f, 0x00f000f0
+  uint32_t or1024, or64;  // fp16 pairs (1024, 1024), (64, 64)
+};
+
+template <int D, int BITS>
+struct Geo {
+  static constexpr int kRow = D * BITS / 8;     // bytes of a token's codes
+  static constexpr int kUnit = D * BITS / 128;  // V: bytes of a token in one lane's unit
+  static constexpr int kKW = kRow / 16;         // dwords of K codes per lane and 16-key tile
+  static constexpr int kVW = kUnit;             // dwords of V codes per lane and 16-key tile (4 tokens)
+  static constexpr int kMf = D / 32;            // MFMAs of a K tile
+  static constexpr int kVm = D / 16;            // MFMAs of the values (= channels of a unit)
+};
+
+template <int D, int BITS, int NG>
+struct Step {
+  uint32_t k[2][Geo<D, BITS>::kKW];
+  uint32_t v[2][Geo<D, BITS>::kVW];
+  u32x4 km[2][NG];
+  u32x4 vm[2];
+  uint32_t bad;  // bit t: tile t has no keys here (past the end, or no such page)
+};
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const u32x4 t = reinterpret_cast<const u32x4*>(p)[i];
+      w[4 * i] = t[0], w[4 * i + 1] = t[1], w[4 * i + 2] = t[2], w[4 * i + 3] = t[3];
+    }
+  } else {
+    const u32x2 t = *reinterpret_cast<const u32x2*>(p);
+    w[0] = t[0], w[1] = t[1];
+  }
+}
+
+// Selector that takes byte `b` of token `t` and of token `t + 1` (bytes t * U + b of the lane's dwords)
+// to bytes 0 and 2, zeros between; of v_perm_b32(second word, first word).
+template <int U>
+constexpr uint32_t pair_sel(int t, int b) {
+  const int x = t * U + b, y = (t + 1) * U + b;
+  const uint32_t sx = x % 4, sy = y / 4 == x / 4 ? y % 4 : 4 + y % 4;
+  return 0x0c000c00u | sy << 16 | sx;
+}
+
+template <int D, int BITS, int GS, int NT>
+__global__ __launch_bounds__(256) void k_kv_stream(AttnArgs a) {
+  using G = Geo<D, BITS>;
+  constexpr int NG = D / GS;
+  constexpr int kLdsRow = D + 4;
+  __shared__ __attribute__((aligned(16))) float sh_o[4][16][kLdsRow];
+  __shared__ float sh_m[4][16 * NT], sh_l[4][16 * NT];
+
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, h = lane >> 4;
+  const int split = blockIdx.x, hk = blockIdx.y % a.f.hkv, tile = blockIdx.y / a.f.hkv, seq = blockIdx.z;
+
+  // the sequence's query tokens and keys
+  int q0 = seq * a.tq, tq = a.tq;
+  if (a.cu_q) {
+    q0 = a.cu_q[seq];
+    tq = a.cu_q[seq + 1] - q0;
+    // (offsets outside the query tensor leave the sequence out)
+    if (q0 < 0 || tq < 0 || tq > a.max_q || (int64_t)q0 + tq > a.total_q) tq = 0;
+  }
+  const int rows = tq * a.per;
+  const int row0 = tile * 16 * NT;
+  if (row0 >= rows) return;
+  const int page = 1 << a.f.page_shift;
+  int len = a.lens ? a.lens[seq] : a.fixed_len;
+  len = min(min(max(len, 0), a.max_len), a.table_cols << a.f.page_shift);
+  const int last_t = (min(row0 + 16 * NT, rows) - 1) / a.per;
+  const int end_all = a.causal ? min(len, max(0, len - tq + last_t + 1)) : len;
+  const int kb = split * a.chunk;
+  const int ke = min(kb + a.chunk, end_all);
+  const int first_t = row0 / a.per;
+  const int end_min = a.causal ? len - tq + first_t + 1 : len;  // keys below it are seen by every row
+
+  // ---- queries: rows in fp16 with a power of two of their own, sums per group
+  h8 qf[NT][G::kMf];
+  float sq[NT][NG], cs[NT];
+  int lim[NT];  // last key the lane's row sees
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int r = row0 + 16 * t + n;
+    const bool there = r < rows;
+    const int rt = (there ? r : row0) / a.per, rg = (there ? r : row0) % a.per;
+    const int64_t at = (int64_t)(q0 + rt) * a.q_ts + (int64_t)(hk * a.per + rg) * a.q_hs;
+    float x[G::kMf][8];
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < G::kMf; ++i) {
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q) + at + 32 * i + 8 * h;
+      if (a.dtype == HQQ_KV_BF16)
+        load8<true>(p, x[i]);
+      else
+        load8<false>(p, x[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[i][j] = there ? x[i][j] : 0.f;
+        top = fmaxf(top, fabsf(x[i][j]));
+      }
+    }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    // the row's largest value to [2^14, 2^15): q / 16 keeps fp16's full precision for 2^13 below it
+    int e = 0;
+    if (top > 0.f && top < INFINITY) e = 14 - (int)((__builtin_bit_cast(uint32_t, top) >> 23) & 255) + 127;
+    e = min(e, 100);
+    cs[t] = ldexpf(a.scale_log2, 24 - e);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) sq[t][g] = 0.f;
+#pragma unroll
+    for (int i = 0; i < G::kMf; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float y = ldexpf(x[i][j], e);
+        sq[t][i * 32 / GS] += y;
+        qf[t][i][j] = (_Float16)(BITS == 4 && (j & 2) ? y * 0.0625f : y);
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      sq[t][g] += __shfl_xor(sq[t][g], 16);
+      sq[t][g] += __shfl_xor(sq[t][g], 32);
+      sq[t][g] *= 0x1p-24f;  // the scale of the codes' products
+    }
+    lim[t] = there ? (a.causal ? min(len - 1, len - tq + rt) : len - 1) : -1;
+  }
+
+  // ---- the stream
+  Masks mk;
+  asm("s_mov_b32 %0, 0x000f000f" : "=s"(mk.lo));
+  asm("s_mov_b32 %0, 0x00f000f0" : "=s"(mk.hi));
+  asm("v_mov_b32 %0, 0x64006400" : "=v"(mk.or1024));
+  asm("v_mov_b32 %0, 0x54005400" : "=v"(mk.or64));
+  const uint32_t k_off = n * G::kRow + h * (G::kRow / 4);
+  const uint32_t v_off = page * G::kRow + (h * 16 + n) * (4 * G::kUnit);
+  const uint32_t km_off = 2 * page * G::kRow + 16 * h;
+  const uint32_t vm_off = km_off + 4 * page * (NG + (n * (D / 16)) / GS);
+  const int32_t* table = a.table + (int64_t)seq * a.table_stride;
+
+  f32x4 o[NT][G::kVm], fl[NT];  // channels (4h + i) * (D/16) + j; floors' sums of those units
+  float mref[NT], l[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    mref[t] = kNoKey, l[t] = 0.f;
+    fl[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < G::kVm; ++j) o[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  auto fetch = [&](int key0, Step<D, BITS, NG>& s) {
+    s.bad = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int key = key0 + 16 * t;
+      uint32_t id = 0;
+      bool ok = key < ke;
+      if (ok) {
+        id = (uint32_t)table[key >> a.f.page_shift];
+        ok = id < a.f.num_pages;
+      }
+      s.bad |= ok ? 0u : 1u << t;
+      const int off = key & (page - 1);
+      const uint8_t* base = a.f.pages + (int64_t)(ok ? id : 0) * a.f.page_bytes + hk * a.f.block_bytes;
+      load_words(base + off * G::kRow + k_off, s.k[t]);
+      load_words(base + off * G::kRow + v_off, s.v[t]);
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+        s.km[t][g] = *reinterpret_cast<const u32x4*>(base + (off + g * page) * 4 + km_off);
+      s.vm[t] = *reinterpret_cast<const u32x4*>(base + off * 4 + vm_off);
+    }
+  };
+
+  auto consume = [&](int key0, Step<D, BITS, NG>& s) {
+    // scores
+    float p[NT][8];
+#pragma unroll
+    for (int t2 = 0; t2 < 2; ++t2) {
+      f32x4 acc[NT][NG];
+#pragma unroll
+      for (int i = 0; i < G::kMf; ++i) {
+        u32x4 w;
+        if (BITS == 4) {
+          const uint32_t c = s.k[t2][i], d = c >> 8;
+          w = u32x4{c & mk.lo, c & mk.hi, d & mk.lo, d & mk.hi};
+        } else {
+          const uint32_t c = s.k[t2][2 * i], d = s.k[t2][2 * i + 1];
+          w = u32x4{__builtin_amdgcn_perm(0, c, 0x0c010c00), __builtin_amdgcn_perm(0, c, 0x0c030c02),
+                    __builtin_amdgcn_perm(0, d, 0x0c010c00), __builtin_amdgcn_perm(0, d, 0x0c030c02)};
+        }
+        const h8 kf = __builtin_bit_cast(h8, w);
+        const int g = i * 32 / GS;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const f32x4 from = i * 32 % GS == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[t][g];
+          acc[t][g] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[t][i], from, 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float x = 0.f;
+#pragma unroll
+          for (int g = 0; g < NG; ++g) {
+            const h2 m = as_h2((uint32_t)s.km[t2][g][c]);
+            x = g ? fmaf((float)m.y, sq[t][g], x) : (float)m.y * sq[t][g];
+            x = fmaf(acc[t][g][c], (float)m.x, x);
+          }
+          p[t][4 * t2 + c] = x;
+        }
+      }
+    }
+    if (s.bad | (uint32_t)(key0 + 32 > end_min) | (uint32_t)(key0 + 32 > len)) {
+      // keys that a row does not see (by selection: whatever their memory holds), and floors and
+      // steps of keys that are not there
+#pragma unroll
+      for (int t2 = 0; t2 < 2; ++t2) {
+        const bool bad = s.bad >> t2 & 1;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int key = key0 + 16 * t2 + 4 * h + c;
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            p[t][4 * t2 + c] = bad || key > lim[t] ? -INFINITY : p[t][4 * t2 + c];
+          s.vm[t2][c] = bad || key >= len ? 0u : (uint32_t)s.vm[t2][c];
+        }
+      }
+    }
+    // values: steps and floors of the lane's unit as pairs of keys
+    h2 st[4], fm[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = s.vm[i >> 1][2 * (i & 1)], y = s.vm[i >> 1][2 * (i & 1) + 1];
+      st[i] = as_h2(__builtin_amdgcn_perm(y, x, 0x05040100));
+      fm[i] = as_h2(__builtin_amdgcn_perm(y, x, 0x07060302));
+    }
+    // 1024 s passes fp16 for steps of 64 and more: such a step of the stream takes its values 2^-8
+    // smaller (a 4-bit step is at most 8734) and its weights, then held to 1, 2^8 larger
+    const h2 widest = __builtin_elementwise_max(__builtin_elementwise_max(st[0], st[1]),
+                                                __builtin_elementwise_max(st[2], st[3]));
+    const bool wide = __any((float)widest.x > 60.f || (float)widest.y > 60.f);
+    float slack = 5.f, lift = 0.f, drop = 1.f;
+    if (wide) {
+      slack = 0.f, lift = 8.f, drop = 0x1p-8f;
+      const h2 vs = {(_Float16)0x1p-8f, (_Float16)0x1p-8f};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st[i] *= vs, fm[i] *= vs;
+    }
+    h8 pf[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float top = p[t][0];
+#pragma unroll
+      for (int c = 1; c < 8; ++c) top = fmaxf(top, p[t][c]);
+      top *= cs[t];
+      if (__any(top > mref[t] + slack)) {
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float next = fmaxf(mref[t], top);
+        const float f = exp2_(mref[t] - next);
+        mref[t] = next;
+        l[t] *= f;
+#pragma unroll
+        for (int j = 0; j < G::kVm; ++j) o[t][j] *= f;
+        fl[t] *= f;
+      }
+      float sum = 0.f;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const float e = exp2_(fmaf(p[t][c], cs[t], lift - mref[t]));
+        sum += e;
+        p[t][c] = e;
+      }
+      l[t] = fmaf(sum, drop, l[t]);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const f32x2 e = {p[t][2 * c], p[t][2 * c + 1]};
+        const h2 r = __builtin_convertvector(e, h2);
+        pf[t][2 * c] = r.x, pf[t][2 * c + 1] = r.y;
+      }
+    }
+    h2 s1024[4], s64[4];
+    u32x4 flw;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      flw[i] = as_u32(fm[i]);
+      s1024[i] = st[i] * h2{(_Float16)-1024.f, (_Float16)-1024.f};
+      if (BITS == 4) s64[i] = st[i] * h2{(_Float16)-64.f, (_Float16)-64.f};
+    }
+    const h8 ff = __builtin_bit_cast(h8, flw);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) fl[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ff, pf[t], fl[t], 0, 0, 0);
+#pragma unroll
+    for (int b = 0; b < G::kUnit; ++b) {
+      u32x4 lo, hi;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        constexpr int U = G::kUnit;
+        const int t0 = 2 * (i & 1);  // first token of the pair within the tile
+        const uint32_t(&v)[G::kVW] = s.v[i >> 1];
+        const uint32_t wx = v[(t0 * U + b) / 4], wy = v[((t0 + 1) * U + b) / 4];
+        const uint32_t c = __builtin_amdgcn_perm(wy, wx, pair_sel<U>(t0, b));
+        const h2 x = as_h2(BITS == 4 ? (c & mk.lo) | mk.or1024 : c | mk.or1024);
+        lo[i] = as_u32(__builtin_elementwise_fma(x, st[i], s1024[i]));
+        if (BITS == 4) {
+          const h2 y = as_h2((c & mk.hi) | mk.or64);
+          hi[i] = as_u32(__builtin_elementwise_fma(y, st[i], s64[i]));
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (BITS == 4) {
+          o[t][2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, lo), pf[t], o[t][2 * b], 0, 0, 0);
+          o[t][2 * b + 1] =
+              __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, hi), pf[t], o[t][2 * b + 1], 0, 0, 0);
+        } else {
+          o[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, lo), pf[t], o[t][b], 0, 0, 0);
+        }
+      }
+    }
+  };
+
+  int key0 = kb + 32 * wave;
+  if (key0 < ke) {
+    Step<D, BITS, NG> cur, next;
+    fetch(key0, cur);
+    while (true) {
+      const bool more = key0 + 128 < ke;
+      if (more) fetch(key0 + 128, next);
+      consume(key0, cur);
+      if (!more) break;
+      cur = next;
+      key0 += 128;
+    }
+  }
+
+  // ---- the block's four waves joined, then written
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    l[t] += __shfl_xor(l[t], 16);
+    l[t] += __shfl_xor(l[t], 32);
+    if (h == 0) sh_m[wave][16 * t + n] = mref[t], sh_l[wave][16 * t + n] = l[t];
+  }
+  __syncthreads();
+  const int64_t total_rows = a.total_q * a.hq;
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    float mm = sh_m[0][16 * t + n];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) mm = fmaxf(mm, sh_m[w][16 * t + n]);
+    const float f = exp2_(mref[t] - mm);
+    if (t) __syncthreads();  // the tile before has been read
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < G::kVm; j += 4) {
+        f32x4 x;
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) x[jj] = (o[t][j + jj][i] + fl[t][i]) * f;
+        *reinterpret_cast<f32x4*>(&sh_o[wave][n][(4 * h + i) * (D / 16) + j]) = x;
+      }
+    __syncthreads();
+    // 256 threads, 16 rows: D / 16 channels each
+    const int r = threadIdx.x / 16, d0 = threadIdx.x % 16 * (D / 16);
+    const int row = row0 + 16 * t + r;
+    if (row < rows) {
+      float rm = sh_m[0][16 * t + r];
+#pragma unroll
+      for (int w = 1; w < 4; ++w) rm = fmaxf(rm, sh_m[w][16 * t + r]);
+      float sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) sum += sh_l[w][16 * t + r] * exp2_(sh_m[w][16 * t + r] - rm);
+      const int64_t token = q0 + row / a.per;
+      const int64_t at = token * a.hq + hk * a.per + row % a.per;
+      float x[D / 16];
+#pragma unroll
+      for (int j = 0; j < D / 16; j += 4) {
+        f32x4 y = *reinterpret_cast<const f32x4*>(&sh_o[0][r][d0 + j]);
+#pragma unroll
+        for (int w = 1; w < 4; ++w) y += *reinterpret_cast<const f32x4*>(&sh_o[w][r][d0 + j]);
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) x[j + jj] = y[jj];
+      }
+      if (a.parts > 1) {
+        const int64_t part = (int64_t)(a.part0 + split) * total_rows + at;
+        if (d0 == 0) a.part_ml[part] = float2{rm, sum};
+        float* to = a.part_o + part * D + d0;
+        if (sum != 0.f)  // (an empty part's sums are never read)
+#pragma unroll
+          for (int j = 0; j < D / 16; j += 4) *reinterpret_cast<f32x4*>(to + j) = f32x4{x[j], x[j + 1], x[j + 2], x[j + 3]};
+      } else {
+        const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+        uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + at * D + d0;
+#pragma unroll
+        for (int j = 0; j < D / 16; j += 4) {
+          u32x2 w;
+          if (a.dtype == HQQ_KV_BF16)
+            w = u32x2{pack2<true>(x[j] * inv, x[j + 1] * inv), pack2<true>(x[j + 2] * inv, x[j + 3] * inv)};
+          else
+            w = u32x2{pack2<false>(x[j] * inv, x[j + 1] * inv), pack2<false>(x[j + 2] * inv, x[j + 3] * inv)};
+          *reinterpret_cast<u32x2*>(to + j) = w;
+        }
+        if (a.lse && d0 == 0) a.lse[at] = sum != 0.f ? (rm + __log2f(sum)) * 0.69314718056f : -INFINITY;
+      }
+    }
+  }
+}
+
+// Joins the parts of each row: a wave a row.
+template <int D>
+__global__ __launch_bounds__(256) void k_kv_join(AttnArgs a) {
+  const int64_t total_rows = a.total_q * a.hq;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= total_rows) return;
+  const int lane = threadIdx.x & 63;
+  float top = kNoKey;
+  for (int p = lane; p < a.parts; p += 64) {
+    const float2 ml = a.part_ml[p * total_rows + row];
+    if (ml.y != 0.f) top = fmaxf(top, ml.x);
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  float sum = 0.f;
+  f32x2 x = {0.f, 0.f};
+#pragma unroll 4
+  for (int p = 0; p < a.parts; ++p) {
+    const int64_t at = p * total_rows + row;
+    const float2 ml = a.part_ml[at];
+    if (ml.y != 0.f) {
+      const float f = exp2_(ml.x - top);
+      sum += f * ml.y;
+      const float* from = a.part_o + at * D;
+      if (D == 128)
+        x += *reinterpret_cast<const f32x2*>(from + 2 * lane) * f;
+      else
+        x[0] += from[lane] * f;
+    }
+  }
+  const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+  uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + row * D;
+  const uint32_t w = a.dtype == HQQ_KV_BF16 ? pack2<true>(x[0] * inv, x[1] * inv) : pack2<false>(x[0] * inv, x[1] * inv);
+  if (D == 128)
+    *reinterpret_cast<uint32_t*>(to + 2 * lane) = w;
+  else
+    to[lane] = (uint16_t)w;
+  if (a.lse && lane == 0) a.lse[row] = sum != 0.f ? (top + __log2f(sum)) * 0.69314718056f : -INFINITY;
+}
+
+template <int D, int BITS, int GS>
+hipError_t stream_t(const AttnArgs& a, int nt, hipStream_t st) {
+  const int tiles = (int)(((int64_t)a.max_q * a.per + 16 * nt - 1) / (16 * nt));
+  const dim3 grid(a.nsplit, a.f.hkv * tiles, a.num_seqs);
+  if (nt == 2)
+    k_kv_stream<D, BITS, GS, 2><<<grid, 256, 0, st>>>(a);
+  else
+    k_kv_stream<D, BITS, GS, 1><<<grid, 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_stream(const AttnArgs& a, int D, int bits, int gs, int nt, hipStream_t st) {
+#define X(d, b, g) \
+  if (D == d && bits == b && gs == g) return stream_t<d, b, g>(a, nt, st);
+  X(64, 4, 32) X(64, 4, 64) X(64, 8, 32) X(64, 8, 64) X(128, 4, 32) X(128, 4, 64) X(128, 4, 128) X(128, 8, 32)
+  X(128, 8, 64) X(128, 8, 128)
+#undef X
+  return hipErrorInvalidValue;
+}
+
+hipError_t launch_kv_join(const AttnArgs& a, int D, hipStream_t st) {
+  const dim3 grid((unsigned)((a.total_q * a.hq + 3) / 4));
+  if (D == 128)
+    k_kv_join<128><<<grid, 256, 0, st>>>(a);
+  else
+    k_kv_join<64><<<grid, 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace kv
+}  // namespace hqq
