@@ -77,6 +77,8 @@ hipError_t launch_kv_write(const WriteArgs& a, int D, int bits, int gs, int dtyp
 hipError_t launch_kv_read(const ReadArgs& a, int D, int bits, int gs, int dtype, hipStream_t st);
 // Rows of up to 16 * NT per wave, streamed keys; NT 1 or 2.
 hipError_t launch_kv_stream(const AttnArgs& a, int D, int bits, int gs, int nt, hipStream_t st);
+// Tiles of 256 rows.
+hipError_t launch_kv_tile(const AttnArgs& a, int D, int bits, int gs, hipStream_t st);
 hipError_t launch_kv_join(const AttnArgs& a, int D, hipStream_t st);
 
 constexpr float kNoKey = -1e30f;  // running maximum before any key (finite: differences of two stay numbers)

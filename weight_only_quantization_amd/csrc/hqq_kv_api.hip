@@ -56,19 +56,26 @@ bool known_type(int dtype) { return dtype == HQQ_KV_F16 || dtype == HQQ_KV_BF16;
 // The passes of one attention call: over the sequences' own keys, and over the shared prefix.
 struct Plan {
   AttnArgs own, prefix;
-  int own_nt, prefix_nt;
+  int own_kind, prefix_kind;  // row kernel of each
   bool has_prefix;
   int parts;
   size_t workspace;
 };
 
-// Blocks of a pass: row tiles of the widest sequence times KV heads times sequences.
-int64_t pass_tiles(int64_t rows, int nt) { return (rows + 16 * nt - 1) / (16 * nt); }
+// Row kernels: the stream with 16 or 32 rows a wave, or tiles of 256 rows.
+enum { kStream16, kStream32, kTile };
 
-// Key splits: enough blocks to fill the 256 CUs several times over, at least 256 keys each (two
-// stream steps a wave).
-void split_keys(AttnArgs* a, int64_t blocks, int64_t keys) {
-  int64_t n = (2048 + blocks - 1) / blocks;
+int row_kernel(int64_t rows) { return rows <= 16 ? kStream16 : rows <= 64 ? kStream32 : kTile; }
+int64_t row_tiles(int64_t rows, int kind) {
+  const int64_t of = kind == kStream16 ? 16 : kind == kStream32 ? 32 : 256;
+  return (rows + of - 1) / of;
+}
+
+// Key splits: enough blocks to fill the 256 CUs several times over (a tile block fills one), at least
+// 256 keys each.
+void split_keys(AttnArgs* a, int kind, int64_t blocks, int64_t keys) {
+  const int64_t want = kind == kTile ? 512 : 2048;
+  int64_t n = kind == kTile ? want / blocks : (want + blocks - 1) / blocks;
   const int64_t most = (keys + 255) / 256;
   n = n > most ? most : n;
   n = n < 1 ? 1 : n;
@@ -77,6 +84,11 @@ void split_keys(AttnArgs* a, int64_t blocks, int64_t keys) {
   a->chunk = (int)chunk;
   a->nsplit = (int)((keys + chunk - 1) / chunk);
   if (a->nsplit < 1) a->nsplit = 1;
+}
+
+hipError_t launch_pass(const AttnArgs& a, int kind, const hqq_kv_cache& c, hipStream_t st) {
+  if (kind == kTile) return hqq::kv::launch_kv_tile(a, c.head_dim, c.nbits, c.group_size, st);
+  return hqq::kv::launch_kv_stream(a, c.head_dim, c.nbits, c.group_size, kind == kStream16 ? 1 : 2, st);
 }
 
 int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
@@ -137,11 +149,11 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
   if (x->total_q == 0 || x->num_seqs == 0 || a.max_q == 0) return HQQ_OK;
 
   const int64_t rows = (int64_t)a.max_q * a.per;
-  p->own_nt = rows <= 16 ? 1 : 2;
-  const int64_t tiles = pass_tiles(rows, p->own_nt);
+  p->own_kind = row_kernel(rows);
+  const int64_t tiles = row_tiles(rows, p->own_kind);
   KV_NEED(x->num_seqs <= 65535, HQQ_ERR_UNSUPPORTED, "at most 65535 sequences in a call");
   KV_NEED(tiles * f.hkv <= 65535, HQQ_ERR_UNSUPPORTED, "too many query rows in a sequence");
-  split_keys(&p->own, tiles * f.hkv * x->num_seqs, x->max_len);
+  split_keys(&p->own, p->own_kind, tiles * f.hkv * x->num_seqs, x->max_len);
   p->parts = p->own.nsplit;
   if (p->has_prefix) {
     AttnArgs& b = p->prefix;
@@ -155,10 +167,10 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
     b.fixed_len = b.max_len = (int)x->prefix_len;
     b.causal = 0;
     const int64_t all = x->total_q * a.per;
-    p->prefix_nt = all <= 16 ? 1 : 2;
-    const int64_t t = pass_tiles(all, p->prefix_nt);
+    p->prefix_kind = row_kernel(all);
+    const int64_t t = row_tiles(all, p->prefix_kind);
     KV_NEED(t * f.hkv <= 65535, HQQ_ERR_UNSUPPORTED, "too many query rows in a call");
-    split_keys(&b, t * f.hkv, x->prefix_len);
+    split_keys(&b, p->prefix_kind, t * f.hkv, x->prefix_len);
     b.part0 = p->own.nsplit;
     p->parts += b.nsplit;
   }
@@ -194,8 +206,8 @@ int run_attention(const hqq_kv_attention_args* x) {
   }
   hipStream_t stream = static_cast<hipStream_t>(x->stream);
   hipError_t e = hipSuccess;
-  if (p.has_prefix) e = hqq::kv::launch_kv_stream(p.prefix, c.head_dim, c.nbits, c.group_size, p.prefix_nt, stream);
-  if (e == hipSuccess) e = hqq::kv::launch_kv_stream(p.own, c.head_dim, c.nbits, c.group_size, p.own_nt, stream);
+  if (p.has_prefix) e = launch_pass(p.prefix, p.prefix_kind, c, stream);
+  if (e == hipSuccess) e = launch_pass(p.own, p.own_kind, c, stream);
   if (e == hipSuccess && p.parts > 1) e = hqq::kv::launch_kv_join(p.own, c.head_dim, stream);
   return device_status(e);
 }

@@ -1,0 +1,355 @@
+// Attention of many query rows over a quantised key/value cache: tiles of 256 rows by 128 keys.
+//
+// Prompts' chunks, and a prefix under all the rows of a batch: the keys of a tile are dequantised once
+// for 256 rows, k = fp16(m + c s) with one rounding, into LDS, and both products run on the matrix unit:
+//   S^T[key][row] = K Q^T,  o^T[channel][row] += V^T P^T,
+// so a lane's scores (16 of one row) are its operand of the second product as they are: V^T is kept
+// in LDS with its keys in that order.
+// Eight waves, 32 rows each; all of them unpack 1/8 of the next tile while they work on this one (two
+// buffers of K and V, one barrier a tile).  Codes, step and floor become values in packed fp16:
+// (1024 + c) - 1024 is exact, fma(c, s, m) rounds once.
+// Softmax as in the stream kernel: one pass, fp32, the maximum raised only when a score passes it by 2^5.
+#include "hqq_kv.h"
+
+namespace hqq {
+namespace kv {
+namespace {
+
+constexpr int kWaves = 8, kRows = 32 * kWaves, kKeys = 128;
+
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const u32x4 t = reinterpret_cast<const u32x4*>(p)[i];
+      w[4 * i] = t[0], w[4 * i + 1] = t[1], w[4 * i + 2] = t[2], w[4 * i + 3] = t[3];
+    }
+  } else {
+    const u32x2 t = *reinterpret_cast<const u32x2*>(p);
+    w[0] = t[0], w[1] = t[1];
+  }
+}
+
+template <int U>
+constexpr uint32_t pair_sel(int t, int b) {
+  const int x = t * U + b, y = (t + 1) * U + b;
+  const uint32_t sx = x % 4, sy = y / 4 == x / 4 ? y % 4 : 4 + y % 4;
+  return 0x0c000c00u | sy << 16 | sx;
+}
+
+// 16-byte chunk of a row of K (D halves) and of V^T (128 halves), swizzled so that 16 lanes reading one
+// chunk column, and the unpacking writes, spread over all banks.
+template <int D>
+__device__ __forceinline__ int k_chunk(int key, int c) {
+  return D == 128 ? key * 16 + (c ^ (key & 15)) : key * 8 + (c ^ ((key >> 1) & 7));
+}
+__device__ __forceinline__ int v_chunk(int d, int c) { return d * 16 + (c ^ ((d ^ (d >> 3)) & 15)); }
+
+template <int D, int BITS, int NG>
+struct Raw {
+  uint32_t k[D * BITS / 128];  // a quarter of a key's codes
+  uint32_t v[D * BITS / 128];  // a unit's codes of four tokens
+  uint32_t km[NG];
+  u32x4 vm;
+};
+
+template <int D, int BITS, int GS>
+__global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a) {
+  constexpr int NG = D / GS, U = D * BITS / 128;
+  constexpr int kRow = D * BITS / 8;
+  constexpr int KS = D / 16, DT = D / 32;  // MFMA steps of a score, channel tiles of the output
+  __shared__ __attribute__((aligned(16))) u32x4 sh_k[2][kKeys * D / 8];
+  __shared__ __attribute__((aligned(16))) u32x4 sh_v[2][kKeys * D / 8];
+
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int n = lane & 31, h = lane >> 5;
+  const int tiles = gridDim.y / a.f.hkv;
+  // (the tiles with the most keys under a causal rule start first)
+  const int split = blockIdx.x, hk = blockIdx.y % a.f.hkv, tile = tiles - 1 - (int)blockIdx.y / a.f.hkv, seq = blockIdx.z;
+
+  int q0 = seq * a.tq, tq = a.tq;
+  if (a.cu_q) {
+    q0 = a.cu_q[seq];
+    tq = a.cu_q[seq + 1] - q0;
+    if (q0 < 0 || tq < 0 || tq > a.max_q || (int64_t)q0 + tq > a.total_q) tq = 0;
+  }
+  const int rows = tq * a.per;
+  const int row0 = tile * kRows;
+  if (row0 >= rows) return;
+  const int page = 1 << a.f.page_shift;
+  int len = a.lens ? a.lens[seq] : a.fixed_len;
+  len = min(min(max(len, 0), a.max_len), a.table_cols << a.f.page_shift);
+  const int last_t = (min(row0 + kRows, rows) - 1) / a.per;
+  const int end_all = a.causal ? min(len, max(0, len - tq + last_t + 1)) : len;
+  const int kb = split * a.chunk;
+  const int ke = min(kb + a.chunk, end_all);
+  // the wave's own rows
+  const int w_row0 = row0 + 32 * wave;
+  const bool w_on = w_row0 < rows;
+  const int w_first = w_on ? w_row0 / a.per : 0, w_last = w_on ? (min(w_row0 + 32, rows) - 1) / a.per : 0;
+  const int w_end = !w_on ? 0 : a.causal ? min(ke, len - tq + w_last + 1) : ke;   // keys that some row sees
+  const int w_min = a.causal ? len - tq + w_first + 1 : len;                       // keys that all rows see
+
+  // ---- queries
+  h8 qf[KS];
+  float cs;
+  int lim;
+  const int r = w_row0 + n;
+  const bool there = r < rows;
+  const int rt = (there ? r : 0) / a.per, rg = (there ? r : 0) % a.per;
+  {
+    const int64_t at = (int64_t)(q0 + rt) * a.q_ts + (int64_t)(hk * a.per + rg) * a.q_hs;
+    float top = 0.f;
+    float x[KS][8];
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q) + at + 16 * i + 8 * h;
+      if (a.dtype == HQQ_KV_BF16)
+        load8<true>(p, x[i]);
+      else
+        load8<false>(p, x[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[i][j] = there ? x[i][j] : 0.f;
+        top = fmaxf(top, fabsf(x[i][j]));
+      }
+    }
+    top = fmaxf(top, __shfl_xor(top, 32));
+    // the row's largest value to [2^14, 2^15): bfloat16 rows of any size keep their bits in fp16
+    int e = 0;
+    if (top > 0.f && top < INFINITY) e = 14 - (int)((__builtin_bit_cast(uint32_t, top) >> 23) & 255) + 127;
+    e = min(e, 100);
+    cs = ldexpf(a.scale_log2, -e);
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) qf[i][j] = (_Float16)ldexpf(x[i][j], e);
+    lim = there ? (a.causal ? min(len - 1, len - tq + rt) : len - 1) : -1;
+  }
+
+  // ---- unpacking: a quarter of one key and one unit of four tokens a thread
+  const int32_t* table = a.table + (int64_t)seq * a.table_stride;
+  const int ik = tid >> 2, iv = (tid >> 4) * 4;
+  const uint32_t k_off = (tid & 3) * (kRow / 4);
+  const int unit = tid & 15;
+  auto page_id = [&](int key) -> int {
+    if (key >= ke) return -1;
+    const uint32_t id = (uint32_t)table[key >> a.f.page_shift];
+    return id < a.f.num_pages ? (int)id : -1;
+  };
+  auto fetch = [&](int key0, int id_k, int id_v, Raw<D, BITS, NG>& s) {
+    {
+      const int off = (key0 + ik) & (page - 1);
+      const uint8_t* base = a.f.pages + (int64_t)max(id_k, 0) * a.f.page_bytes + hk * a.f.block_bytes;
+      load_words(base + off * kRow + k_off, s.k);
+      const uint32_t* m = reinterpret_cast<const uint32_t*>(base + 2 * page * kRow) + off;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) s.km[g] = m[g * page];
+      // (keys that are not there: any finite value; their scores are masked)
+      if (id_k < 0)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) s.km[g] = 0;
+    }
+    {
+      const int off = (key0 + iv) & (page - 1);
+      const uint8_t* base = a.f.pages + (int64_t)max(id_v, 0) * a.f.page_bytes + hk * a.f.block_bytes;
+      load_words(base + page * kRow + off * kRow + unit * 4 * U, s.v);
+      s.vm = *reinterpret_cast<const u32x4*>(base + 2 * page * kRow + 4 * (page * (NG + unit * (D / 16) / GS) + off));
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (id_v < 0 || key0 + iv + c >= len) s.vm[c] = 0;
+    }
+  };
+  uint32_t m_lo, m_hi, or1024, or64;
+  asm("s_mov_b32 %0, 0x000f000f" : "=s"(m_lo));
+  asm("s_mov_b32 %0, 0x00f000f0" : "=s"(m_hi));
+  asm("v_mov_b32 %0, 0x64006400" : "=v"(or1024));
+  asm("v_mov_b32 %0, 0x54005400" : "=v"(or64));
+  const h2 n1024 = {(_Float16)-1024.f, (_Float16)-1024.f}, n64 = {(_Float16)-64.f, (_Float16)-64.f};
+  auto unpack = [&](Raw<D, BITS, NG>& s, u32x4* to_k, u32x4* to_v) {
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint32_t mm = s.km[i * 32 / GS];
+      const h2 st = as_h2(__builtin_amdgcn_perm(mm, mm, 0x01000100)), fm = as_h2(__builtin_amdgcn_perm(mm, mm, 0x03020302));
+      u32x4 w;
+      if (BITS == 4) {
+        const uint32_t c = s.k[i], d = c >> 8;
+        w[0] = as_u32(__builtin_elementwise_fma(as_h2((c & m_lo) | or1024) + n1024, st, fm));
+        w[1] = as_u32(__builtin_elementwise_fma(as_h2((c & m_hi) | or64) + n64, st, fm));
+        w[2] = as_u32(__builtin_elementwise_fma(as_h2((d & m_lo) | or1024) + n1024, st, fm));
+        w[3] = as_u32(__builtin_elementwise_fma(as_h2((d & m_hi) | or64) + n64, st, fm));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t c = __builtin_amdgcn_perm(0, s.k[2 * i + j / 2], j & 1 ? 0x0c030c02 : 0x0c010c00) | or1024;
+          w[j] = as_u32(__builtin_elementwise_fma(as_h2(c) + n1024, st, fm));
+        }
+      }
+      to_k[k_chunk<D>(ik, 4 * i + (tid & 3))] = w;
+    }
+    h2 st[2], fm[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t x = s.vm[2 * i], y = s.vm[2 * i + 1];
+      st[i] = as_h2(__builtin_amdgcn_perm(y, x, 0x05040100));
+      fm[i] = as_h2(__builtin_amdgcn_perm(y, x, 0x07060302));
+    }
+    // a 16-key group's chunks: keys 0-3 8-11, keys 4-7 12-15
+    const int q = tid >> 4, chunk = 2 * (q >> 2) + (q & 1), half = (q >> 1) & 1;
+#pragma unroll
+    for (int b = 0; b < U; ++b) {
+      u32x2 lo, hi;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t c = __builtin_amdgcn_perm(s.v[((2 * i + 1) * U + b) / 4], s.v[(2 * i * U + b) / 4], pair_sel<U>(2 * i, b));
+        lo[i] = as_u32(__builtin_elementwise_fma(as_h2(BITS == 4 ? (c & m_lo) | or1024 : c | or1024) + n1024, st[i], fm[i]));
+        if (BITS == 4) hi[i] = as_u32(__builtin_elementwise_fma(as_h2((c & m_hi) | or64) + n64, st[i], fm[i]));
+      }
+      const int d = unit * (D / 16) + (BITS == 4 ? 2 * b : b);
+      reinterpret_cast<u32x2*>(to_v)[2 * v_chunk(d, chunk) + half] = lo;
+      if (BITS == 4) reinterpret_cast<u32x2*>(to_v)[2 * v_chunk(d + 1, chunk) + half] = hi;
+    }
+  };
+
+  f32x16 o[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
+  float mref = kNoKey, l = 0.f;
+
+  auto attend = [&](int key0, const u32x4* kt, const u32x4* vt, bool holes) {
+#pragma unroll 1
+    for (int sub = 0; sub < kKeys / 32; ++sub) {
+      const int first = key0 + 32 * sub;
+      if (first >= w_end) return;
+      f32x16 s;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) s[i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) {
+        const h8 kf = __builtin_bit_cast(h8, kt[k_chunk<D>(32 * sub + n, 2 * i + h)]);
+        s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[i], s, 0, 0, 0);
+      }
+      if (holes | (first + 32 > w_min) | (first + 32 > ke)) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int key = first + 8 * (i >> 2) + 4 * h + (i & 3);
+          bool on = key <= lim && key < ke;
+          if (holes && on) on = (uint32_t)table[key >> a.f.page_shift] < a.f.num_pages;
+          s[i] = on ? s[i] : -INFINITY;
+        }
+      }
+      float top = s[0];
+#pragma unroll
+      for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+      top *= cs;
+      if (__any(top > mref + 5.f)) {
+        top = fmaxf(top, __shfl_xor(top, 32));
+        const float next = fmaxf(mref, top);
+        const float f = exp2_(mref - next);
+        mref = next;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] *= f;
+      }
+      float sum = 0.f;
+      h8 pf[2];
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        const f32x2 e = {exp2_(fmaf(s[i], cs, -mref)), exp2_(fmaf(s[i + 1], cs, -mref))};
+        sum += e[0] + e[1];
+        const h2 p = __builtin_convertvector(e, h2);
+        pf[i >> 3][i & 7] = p.x, pf[i >> 3][(i & 7) + 1] = p.y;
+      }
+      l += sum;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const h8 vf = __builtin_bit_cast(h8, vt[v_chunk(32 * d + n, 4 * sub + 2 * t + h)]);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[t], o[d], 0, 0, 0);
+        }
+    }
+  };
+
+  if (kb < ke) {
+    Raw<D, BITS, NG> raw;
+    int id_k = page_id(kb + ik), id_v = page_id(kb + iv);
+    bool holes = __syncthreads_or((id_k < 0 && kb + ik < ke) ? 1 : 0);
+    fetch(kb, id_k, id_v, raw);
+    id_k = page_id(kb + kKeys + ik), id_v = page_id(kb + kKeys + iv);
+    unpack(raw, sh_k[0], sh_v[0]);
+    int buf = 0;
+    for (int key0 = kb; key0 < ke; key0 += kKeys) {
+      const int next = key0 + kKeys;
+      const bool more = next < ke;
+      const int bad = id_k < 0 && next + ik < ke;
+      if (more) {
+        fetch(next, id_k, id_v, raw);
+        id_k = page_id(next + kKeys + ik), id_v = page_id(next + kKeys + iv);
+      }
+      const bool next_holes = __syncthreads_or(bad);  // this tile is written; the other buffer is free
+      attend(key0, sh_k[buf], sh_v[buf], holes);
+      if (more) unpack(raw, sh_k[buf ^ 1], sh_v[buf ^ 1]);
+      holes = next_holes;
+      buf ^= 1;
+    }
+  }
+
+  // ---- output: channels 32 d + 8 (i / 4) + 4 h + i % 4 of the lane's row
+  l += __shfl_xor(l, 32);
+  if (!there) return;
+  const int64_t total_rows = a.total_q * a.hq;
+  const int64_t at = (int64_t)(q0 + rt) * a.hq + hk * a.per + rg;
+  if (a.parts > 1) {
+    const int64_t part = (int64_t)(a.part0 + split) * total_rows + at;
+    if (h == 0) a.part_ml[part] = float2{mref, l};
+    if (l != 0.f)
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<f32x4*>(a.part_o + part * D + 32 * d + 2 * i + 4 * h) =
+              f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+  } else {
+    const float inv = l != 0.f ? 1.0f / l : 0.f;
+    uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + at * D + 4 * h;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        u32x2 w;
+        if (a.dtype == HQQ_KV_BF16)
+          w = u32x2{pack2<true>(o[d][i] * inv, o[d][i + 1] * inv), pack2<true>(o[d][i + 2] * inv, o[d][i + 3] * inv)};
+        else
+          w = u32x2{pack2<false>(o[d][i] * inv, o[d][i + 1] * inv), pack2<false>(o[d][i + 2] * inv, o[d][i + 3] * inv)};
+        *reinterpret_cast<u32x2*>(to + 32 * d + 2 * i) = w;
+      }
+    if (a.lse && h == 0) a.lse[at] = l != 0.f ? (mref + __log2f(l)) * 0.69314718056f : -INFINITY;
+  }
+}
+
+template <int D, int BITS, int GS>
+hipError_t tile_t(const AttnArgs& a, hipStream_t st) {
+  const int tiles = (int)(((int64_t)a.max_q * a.per + kRows - 1) / kRows);
+  k_kv_tile<D, BITS, GS><<<dim3(a.nsplit, a.f.hkv * tiles, a.num_seqs), 512, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_tile(const AttnArgs& a, int D, int bits, int gs, hipStream_t st) {
+#define X(d, b, g) \
+  if (D == d && bits == b && gs == g) return tile_t<d, b, g>(a, st);
+  X(64, 4, 32) X(64, 4, 64) X(64, 8, 32) X(64, 8, 64) X(128, 4, 32) X(128, 4, 64) X(128, 4, 128) X(128, 8, 32)
+  X(128, 8, 64) X(128, 8, 128)
+#undef X
+  return hipErrorInvalidValue;
+}
+
+}  // namespace kv
+}  // namespace hqq
