@@ -31,8 +31,10 @@ PROBE_SOURCES = ["hqq_probe.hip"]
 
 # The split GEMM keeps its 128 MFMA accumulators per lane in ordinary VGPRs: with the default
 # (accumulation-register) form the register allocator does not tie each MFMA's result to its
-# accumulator input and copies accumulators between register files around most MFMAs.
-EXTRA = {"hqq_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+# accumulator input and copies accumulators between register files around most MFMAs.  The cache's
+# attention kernels the same (88 of the stream's 449 vector instructions a step were such copies).
+_VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
+EXTRA = {"hqq_gemm.hip": _VGPR_FORM, "hqq_kv_stream.hip": _VGPR_FORM, "hqq_kv_tile.hip": _VGPR_FORM}
 
 
 def _compile(src: str) -> str:

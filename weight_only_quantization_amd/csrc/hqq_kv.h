@@ -122,6 +122,19 @@ __device__ __forceinline__ u32x4 pack8(const float (&x)[8]) {
   return w;
 }
 
+// A block's KV head and sequence (grid x), row tile (y) and key split (z).  Blocks go round the eight
+// XCDs in order of x, so the pairs are turned by tile and split: the parts of one long sequence
+// spread over all XCDs, and so do those of short ones, which end early.  (With the split in x, XCD 0 had every
+// sequence's first keys and XCD 7 only the longest ones': 35 us for the ragged lengths of 32 sequences of
+// up to 4096 keys, as long as if all had 4096.)
+struct BlockPlace {
+  int hk, seq, tile, split;
+};
+__device__ __forceinline__ BlockPlace block_place(int hkv) {
+  const uint32_t pair = (blockIdx.x + blockIdx.y + blockIdx.z) % gridDim.x;
+  return {(int)(pair % hkv), (int)(pair / hkv), (int)blockIdx.y, (int)blockIdx.z};
+}
+
 // Page id and address of a slot; nullptr where the slot is outside the cache.
 __device__ __forceinline__ uint8_t* slot_block(const Format& f, int64_t slot, int head, int* off) {
   if (slot < 0) return nullptr;

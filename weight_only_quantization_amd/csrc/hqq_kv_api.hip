@@ -74,7 +74,7 @@ int64_t row_tiles(int64_t rows, int kind) {
 // Key splits: enough blocks to fill the 256 CUs several times over (a tile block fills one), at least
 // 256 keys each.
 void split_keys(AttnArgs* a, int kind, int64_t blocks, int64_t keys) {
-  const int64_t want = kind == kTile ? 512 : 2048;
+  const int64_t want = kind == kTile ? 256 : 2048;
   int64_t n = kind == kTile ? want / blocks : (want + blocks - 1) / blocks;
   const int64_t most = (keys + 255) / 256;
   n = n > most ? most : n;
@@ -152,7 +152,7 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
   p->own_kind = row_kernel(rows);
   const int64_t tiles = row_tiles(rows, p->own_kind);
   KV_NEED(x->num_seqs <= 65535, HQQ_ERR_UNSUPPORTED, "at most 65535 sequences in a call");
-  KV_NEED(tiles * f.hkv <= 65535, HQQ_ERR_UNSUPPORTED, "too many query rows in a sequence");
+  KV_NEED(tiles <= 65535, HQQ_ERR_UNSUPPORTED, "too many query rows in a sequence");
   split_keys(&p->own, p->own_kind, tiles * f.hkv * x->num_seqs, x->max_len);
   p->parts = p->own.nsplit;
   if (p->has_prefix) {
@@ -169,7 +169,7 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
     const int64_t all = x->total_q * a.per;
     p->prefix_kind = row_kernel(all);
     const int64_t t = row_tiles(all, p->prefix_kind);
-    KV_NEED(t * f.hkv <= 65535, HQQ_ERR_UNSUPPORTED, "too many query rows in a call");
+    KV_NEED(t <= 65535, HQQ_ERR_UNSUPPORTED, "too many query rows in a call");
     split_keys(&b, p->prefix_kind, t * f.hkv, x->prefix_len);
     b.part0 = p->own.nsplit;
     p->parts += b.nsplit;

@@ -15,7 +15,10 @@
 //           they are (keys keep their order inside the step).  c s is one fp16 rounding,
 //           fma(1024 + c, s, -1024 s); the floors enter as one more product, sum_j p_j m_j.
 //           p is rounded to fp16 (2^-12 relative, independent per key).
-// Keys of the next step are loaded before this step's arithmetic.  The four waves of a block take
+// The next step's keys are loaded as soon as this step's scores are done, the next values after this
+// step's product, each into the registers just read: few registers, so three waves a SIMD cover the
+// memory's latency (two with both steps' registers held: 3.2 TB/s at 16 sequences of 16384-32768 keys,
+// 64 heads on 8).  The four waves of a block take
 // every fourth step of the block's chunk and are joined through LDS; chunks are joined by k_join.
 #include "hqq_kv.h"
 
@@ -41,13 +44,16 @@ struct Geo {
   static constexpr int kVm = D / 16;            // MFMAs of the values (= channels of a unit)
 };
 
+// One step's keys or values as loaded: two tiles of 16 keys.
 template <int D, int BITS, int NG>
-struct Step {
-  uint32_t k[2][Geo<D, BITS>::kKW];
-  uint32_t v[2][Geo<D, BITS>::kVW];
-  u32x4 km[2][NG];
-  u32x4 vm[2];
-  uint32_t bad;  // bit t: tile t has no keys here (past the end, or no such page)
+struct StepK {
+  uint32_t c[2][Geo<D, BITS>::kKW];
+  u32x4 m[2][NG];
+};
+template <int D, int BITS>
+struct StepV {
+  uint32_t c[2][Geo<D, BITS>::kVW];
+  u32x4 m[2];
 };
 
 template <int N>
@@ -55,11 +61,11 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
   if (N % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const u32x4 t = reinterpret_cast<const u32x4*>(p)[i];
+      const u32x4 t = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p) + i);
       w[4 * i] = t[0], w[4 * i + 1] = t[1], w[4 * i + 2] = t[2], w[4 * i + 3] = t[3];
     }
   } else {
-    const u32x2 t = *reinterpret_cast<const u32x2*>(p);
+    const u32x2 t = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
     w[0] = t[0], w[1] = t[1];
   }
 }
@@ -73,8 +79,15 @@ constexpr uint32_t pair_sel(int t, int b) {
   return 0x0c000c00u | sy << 16 | sx;
 }
 
-template <int D, int BITS, int GS, int NT>
-__global__ __launch_bounds__(256) void k_kv_stream(AttnArgs a) {
+// Blocks (waves per SIMD) that the registers are held to: the most that does not spill.
+constexpr int stream_blocks(int D, int GS, int NT) {
+  if (NT == 1) return D == 64 ? (GS == 64 ? 4 : 3) : D / GS <= 2 ? 3 : 2;
+  return D == 64 ? (GS == 64 ? 3 : 2) : D / GS <= 2 ? 2 : 1;
+}
+
+// PAIR: pages of at least 32 tokens, so a step's two tiles share a page (one lookup, one address).
+template <int D, int BITS, int GS, int NT, bool PAIR>
+__global__ __launch_bounds__(256, stream_blocks(D, GS, NT)) void k_kv_stream(AttnArgs a) {
   using G = Geo<D, BITS>;
   constexpr int NG = D / GS;
   constexpr int kLdsRow = D + 4;
@@ -83,7 +96,8 @@ __global__ __launch_bounds__(256) void k_kv_stream(AttnArgs a) {
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, h = lane >> 4;
-  const int split = blockIdx.x, hk = blockIdx.y % a.f.hkv, tile = blockIdx.y / a.f.hkv, seq = blockIdx.z;
+  const BlockPlace place = block_place(a.f.hkv);
+  const int split = place.split, hk = place.hk, tile = place.tile, seq = place.seq;
 
   // the sequence's query tokens and keys
   int q0 = seq * a.tq, tq = a.tq;
@@ -103,8 +117,81 @@ __global__ __launch_bounds__(256) void k_kv_stream(AttnArgs a) {
   const int end_all = a.causal ? min(len, max(0, len - tq + last_t + 1)) : len;
   const int kb = split * a.chunk;
   const int ke = min(kb + a.chunk, end_all);
+  const int64_t total_rows = a.total_q * a.hq;
+  if (kb >= end_all && a.parts > 1) {  // no key of this split
+    const int row = row0 + threadIdx.x;
+    if (threadIdx.x < 16 * NT && row < rows)
+      a.part_ml[(int64_t)(a.part0 + split) * total_rows + (int64_t)(q0 + row / a.per) * a.hq + hk * a.per + row % a.per] =
+          float2{kNoKey, 0.f};
+    return;
+  }
   const int first_t = row0 / a.per;
   const int end_min = a.causal ? len - tq + first_t + 1 : len;  // keys below it are seen by every row
+
+  // ---- the wave's first keys are on their way while the queries are prepared
+  uint32_t k_off = n * G::kRow + h * (G::kRow / 4);
+  uint32_t v_off = page * G::kRow + (h * 16 + n) * (4 * G::kUnit);
+  uint32_t km_off = 2 * page * G::kRow + 16 * h;
+  uint32_t vm_off = km_off + 4 * page * (NG + (n * (D / 16)) / GS);
+  const int32_t* table = a.table + (int64_t)seq * a.table_stride;
+
+  // page ids of a step's two tiles (-1: past the end, or no such page), loaded a step before the codes
+  struct Ids {
+    int id[2];
+  };
+  auto page_ids = [&](int key0) {
+    Ids x;
+#pragma unroll
+    for (int t = 0; t < (PAIR ? 1 : 2); ++t) {
+      const int key = key0 + 16 * t;
+      x.id[t] = key < ke ? table[key >> a.f.page_shift] : -1;
+      x.id[t] = (uint32_t)x.id[t] < a.f.num_pages ? x.id[t] : -1;
+    }
+    if (PAIR) x.id[1] = x.id[0];
+    return x;
+  };
+  auto tile_at = [&](int key, int id, int* off) {
+    *off = key & (page - 1);
+    return (const uint8_t*)a.f.pages + (uint64_t)(uint32_t)max(id, 0) * (uint64_t)a.f.page_bytes + hk * a.f.block_bytes;
+  };
+  auto fetch_k = [&](int key0, Ids x, StepK<D, BITS, NG>& s) {
+    // (opaque per step, so that the lane's 32-bit offset stays one next to the wave's 64-bit address)
+    asm volatile("" : "+v"(k_off), "+v"(km_off));
+    int off;
+    const uint8_t* base = tile_at(key0, x.id[0], &off);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (!PAIR && t) base = tile_at(key0 + 16, x.id[1], &off);
+      const int more = PAIR ? 16 * t : 0;
+      load_words(base + off * G::kRow + k_off + more * G::kRow, s.c[t]);
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+        s.m[t][g] =
+            __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(base + (off + g * page) * 4 + km_off + more * 4));
+    }
+  };
+  auto fetch_v = [&](int key0, Ids x, StepV<D, BITS>& s) {
+    asm volatile("" : "+v"(v_off), "+v"(vm_off));
+    int off;
+    const uint8_t* base = tile_at(key0, x.id[0], &off);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (!PAIR && t) base = tile_at(key0 + 16, x.id[1], &off);
+      const int more = PAIR ? 16 * t : 0;
+      load_words(base + off * G::kRow + v_off + more * G::kRow, s.c[t]);
+      s.m[t] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(base + off * 4 + vm_off + more * 4));
+    }
+  };
+  const int first = kb + 32 * wave;
+  StepK<D, BITS, NG> sk;
+  StepV<D, BITS> sv;
+  Ids ids{{-1, -1}}, ids1{{-1, -1}};  // of this step and of the next
+  if (first < ke) {
+    ids = page_ids(first);
+    ids1 = page_ids(first + 128);
+    fetch_k(first, ids, sk);
+    fetch_v(first, ids, sv);
+  }
 
   // ---- queries: rows in fp16 with a power of two of their own, sums per group
   h8 qf[NT][G::kMf];
@@ -164,12 +251,8 @@ __global__ __launch_bounds__(256) void k_kv_stream(AttnArgs a) {
   asm("s_mov_b32 %0, 0x00f000f0" : "=s"(mk.hi));
   asm("v_mov_b32 %0, 0x64006400" : "=v"(mk.or1024));
   asm("v_mov_b32 %0, 0x54005400" : "=v"(mk.or64));
-  const uint32_t k_off = n * G::kRow + h * (G::kRow / 4);
-  const uint32_t v_off = page * G::kRow + (h * 16 + n) * (4 * G::kUnit);
-  const uint32_t km_off = 2 * page * G::kRow + 16 * h;
-  const uint32_t vm_off = km_off + 4 * page * (NG + (n * (D / 16)) / GS);
-  const int32_t* table = a.table + (int64_t)seq * a.table_stride;
-
+  float zero;  // (opaque: a fused step and floor instead of a conversion and a product)
+  asm("v_mov_b32 %0, 0" : "=v"(zero));
   f32x4 o[NT][G::kVm], fl[NT];  // channels (4h + i) * (D/16) + j; floors' sums of those units
   float mref[NT], l[NT];
 #pragma unroll
@@ -180,30 +263,8 @@ __global__ __launch_bounds__(256) void k_kv_stream(AttnArgs a) {
     for (int j = 0; j < G::kVm; ++j) o[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  auto fetch = [&](int key0, Step<D, BITS, NG>& s) {
-    s.bad = 0;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int key = key0 + 16 * t;
-      uint32_t id = 0;
-      bool ok = key < ke;
-      if (ok) {
-        id = (uint32_t)table[key >> a.f.page_shift];
-        ok = id < a.f.num_pages;
-      }
-      s.bad |= ok ? 0u : 1u << t;
-      const int off = key & (page - 1);
-      const uint8_t* base = a.f.pages + (int64_t)(ok ? id : 0) * a.f.page_bytes + hk * a.f.block_bytes;
-      load_words(base + off * G::kRow + k_off, s.k[t]);
-      load_words(base + off * G::kRow + v_off, s.v[t]);
-#pragma unroll
-      for (int g = 0; g < NG; ++g)
-        s.km[t][g] = *reinterpret_cast<const u32x4*>(base + (off + g * page) * 4 + km_off);
-      s.vm[t] = *reinterpret_cast<const u32x4*>(base + off * 4 + vm_off);
-    }
-  };
-
-  auto consume = [&](int key0, Step<D, BITS, NG>& s) {
+  for (int key0 = first; key0 < ke; key0 += 128) {
+    const uint32_t bad = (ids.id[0] < 0 ? 1u : 0u) | (ids.id[1] < 0 ? 2u : 0u);
     // scores
     float p[NT][8];
 #pragma unroll
@@ -213,10 +274,10 @@ __global__ __launch_bounds__(256) void k_kv_stream(AttnArgs a) {
       for (int i = 0; i < G::kMf; ++i) {
         u32x4 w;
         if (BITS == 4) {
-          const uint32_t c = s.k[t2][i], d = c >> 8;
+          const uint32_t c = sk.c[t2][i], d = c >> 8;
           w = u32x4{c & mk.lo, c & mk.hi, d & mk.lo, d & mk.hi};
         } else {
-          const uint32_t c = s.k[t2][2 * i], d = s.k[t2][2 * i + 1];
+          const uint32_t c = sk.c[t2][2 * i], d = sk.c[t2][2 * i + 1];
           w = u32x4{__builtin_amdgcn_perm(0, c, 0x0c010c00), __builtin_amdgcn_perm(0, c, 0x0c030c02),
                     __builtin_amdgcn_perm(0, d, 0x0c010c00), __builtin_amdgcn_perm(0, d, 0x0c030c02)};
         }
@@ -232,30 +293,38 @@ __global__ __launch_bounds__(256) void k_kv_stream(AttnArgs a) {
       for (int t = 0; t < NT; ++t) {
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float x = 0.f;
+          float x = zero;
 #pragma unroll
           for (int g = 0; g < NG; ++g) {
-            const h2 m = as_h2((uint32_t)s.km[t2][g][c]);
-            x = g ? fmaf((float)m.y, sq[t][g], x) : (float)m.y * sq[t][g];
+            const h2 m = as_h2((uint32_t)sk.m[t2][g][c]);
+            x = fmaf((float)m.y, sq[t][g], x);
             x = fmaf(acc[t][g][c], (float)m.x, x);
           }
           p[t][4 * t2 + c] = x;
         }
       }
     }
-    if (s.bad | (uint32_t)(key0 + 32 > end_min) | (uint32_t)(key0 + 32 > len)) {
+    // the next keys take the registers of these, the next values those of this step's further down
+    // (the scores are done before: else these registers are copied)
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) asm volatile("" : "+v"(p[t][c]));
+    const bool more = key0 + 128 < ke;
+    if (more) fetch_k(key0 + 128, ids1, sk);
+    if (bad | (uint32_t)(key0 + 32 > end_min) | (uint32_t)(key0 + 32 > len)) {
       // keys that a row does not see (by selection: whatever their memory holds), and floors and
       // steps of keys that are not there
 #pragma unroll
       for (int t2 = 0; t2 < 2; ++t2) {
-        const bool bad = s.bad >> t2 & 1;
+        const bool gone = bad >> t2 & 1;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int key = key0 + 16 * t2 + 4 * h + c;
 #pragma unroll
           for (int t = 0; t < NT; ++t)
-            p[t][4 * t2 + c] = bad || key > lim[t] ? -INFINITY : p[t][4 * t2 + c];
-          s.vm[t2][c] = bad || key >= len ? 0u : (uint32_t)s.vm[t2][c];
+            p[t][4 * t2 + c] = gone || key > lim[t] ? -INFINITY : p[t][4 * t2 + c];
+          sv.m[t2][c] = gone || key >= len ? 0u : (uint32_t)sv.m[t2][c];
         }
       }
     }
@@ -263,15 +332,14 @@ __global__ __launch_bounds__(256) void k_kv_stream(AttnArgs a) {
     h2 st[4], fm[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t x = s.vm[i >> 1][2 * (i & 1)], y = s.vm[i >> 1][2 * (i & 1) + 1];
+      const uint32_t x = sv.m[i >> 1][2 * (i & 1)], y = sv.m[i >> 1][2 * (i & 1) + 1];
       st[i] = as_h2(__builtin_amdgcn_perm(y, x, 0x05040100));
       fm[i] = as_h2(__builtin_amdgcn_perm(y, x, 0x07060302));
     }
-    // 1024 s passes fp16 for steps of 64 and more: such a step of the stream takes its values 2^-8
-    // smaller (a 4-bit step is at most 8734) and its weights, then held to 1, 2^8 larger
-    const h2 widest = __builtin_elementwise_max(__builtin_elementwise_max(st[0], st[1]),
-                                                __builtin_elementwise_max(st[2], st[3]));
-    const bool wide = __any((float)widest.x > 60.f || (float)widest.y > 60.f);
+    // 1024 s passes fp16 for steps of 64 and more: with a step of 2 or more (bit 14 of its half) this step of
+    // the stream takes its values 2^-8 smaller (a 4-bit step is at most 8734) and its weights, then
+    // held to 1, 2^8 larger
+    const bool wide = __any((as_u32(st[0]) | as_u32(st[1]) | as_u32(st[2]) | as_u32(st[3])) & 0x40004000u);
     float slack = 5.f, lift = 0.f, drop = 1.f;
     if (wide) {
       slack = 0.f, lift = 8.f, drop = 0x1p-8f;
@@ -330,7 +398,7 @@ __global__ __launch_bounds__(256) void k_kv_stream(AttnArgs a) {
       for (int i = 0; i < 4; ++i) {
         constexpr int U = G::kUnit;
         const int t0 = 2 * (i & 1);  // first token of the pair within the tile
-        const uint32_t(&v)[G::kVW] = s.v[i >> 1];
+        const uint32_t(&v)[G::kVW] = sv.c[i >> 1];
         const uint32_t wx = v[(t0 * U + b) / 4], wy = v[((t0 + 1) * U + b) / 4];
         const uint32_t c = __builtin_amdgcn_perm(wy, wx, pair_sel<U>(t0, b));
         const h2 x = as_h2(BITS == 4 ? (c & mk.lo) | mk.or1024 : c | mk.or1024);
@@ -351,20 +419,9 @@ __global__ __launch_bounds__(256) void k_kv_stream(AttnArgs a) {
         }
       }
     }
-  };
-
-  int key0 = kb + 32 * wave;
-  if (key0 < ke) {
-    Step<D, BITS, NG> cur, next;
-    fetch(key0, cur);
-    while (true) {
-      const bool more = key0 + 128 < ke;
-      if (more) fetch(key0 + 128, next);
-      consume(key0, cur);
-      if (!more) break;
-      cur = next;
-      key0 += 128;
-    }
+    if (more) fetch_v(key0 + 128, ids1, sv);
+    ids = ids1;
+    ids1 = page_ids(key0 + 256);
   }
 
   // ---- the block's four waves joined, then written
@@ -375,7 +432,6 @@ __global__ __launch_bounds__(256) void k_kv_stream(AttnArgs a) {
     if (h == 0) sh_m[wave][16 * t + n] = mref[t], sh_l[wave][16 * t + n] = l[t];
   }
   __syncthreads();
-  const int64_t total_rows = a.total_q * a.hq;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     float mm = sh_m[0][16 * t + n];
@@ -479,14 +535,22 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a) {
   if (a.lse && lane == 0) a.lse[row] = sum != 0.f ? (top + __log2f(sum)) * 0.69314718056f : -INFINITY;
 }
 
+template <int D, int BITS, int GS, int NT>
+void stream_nt(const AttnArgs& a, dim3 grid, hipStream_t st) {
+  if (a.f.page_shift >= 5)
+    k_kv_stream<D, BITS, GS, NT, true><<<grid, 256, 0, st>>>(a);
+  else
+    k_kv_stream<D, BITS, GS, NT, false><<<grid, 256, 0, st>>>(a);
+}
+
 template <int D, int BITS, int GS>
 hipError_t stream_t(const AttnArgs& a, int nt, hipStream_t st) {
   const int tiles = (int)(((int64_t)a.max_q * a.per + 16 * nt - 1) / (16 * nt));
-  const dim3 grid(a.nsplit, a.f.hkv * tiles, a.num_seqs);
+  const dim3 grid(a.f.hkv * a.num_seqs, tiles, a.nsplit);
   if (nt == 2)
-    k_kv_stream<D, BITS, GS, 2><<<grid, 256, 0, st>>>(a);
+    stream_nt<D, BITS, GS, 2>(a, grid, st);
   else
-    k_kv_stream<D, BITS, GS, 1><<<grid, 256, 0, st>>>(a);
+    stream_nt<D, BITS, GS, 1>(a, grid, st);
   return hipGetLastError();
 }
 

@@ -66,9 +66,9 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a) {
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, h = lane >> 5;
-  const int tiles = gridDim.y / a.f.hkv;
+  const BlockPlace place = block_place(a.f.hkv);
   // (the tiles with the most keys under a causal rule start first)
-  const int split = blockIdx.x, hk = blockIdx.y % a.f.hkv, tile = tiles - 1 - (int)blockIdx.y / a.f.hkv, seq = blockIdx.z;
+  const int split = place.split, hk = place.hk, tile = (int)gridDim.y - 1 - place.tile, seq = place.seq;
 
   int q0 = seq * a.tq, tq = a.tq;
   if (a.cu_q) {
@@ -82,10 +82,18 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a) {
   const int page = 1 << a.f.page_shift;
   int len = a.lens ? a.lens[seq] : a.fixed_len;
   len = min(min(max(len, 0), a.max_len), a.table_cols << a.f.page_shift);
+  const int64_t total_rows = a.total_q * a.hq;
   const int last_t = (min(row0 + kRows, rows) - 1) / a.per;
   const int end_all = a.causal ? min(len, max(0, len - tq + last_t + 1)) : len;
   const int kb = split * a.chunk;
   const int ke = min(kb + a.chunk, end_all);
+  if (kb >= end_all && a.parts > 1) {  // no key of this split
+    const int row = row0 + tid;
+    if (tid < kRows && row < rows)
+      a.part_ml[(int64_t)(a.part0 + split) * total_rows + (int64_t)(q0 + row / a.per) * a.hq + hk * a.per + row % a.per] =
+          float2{kNoKey, 0.f};
+    return;
+  }
   // the wave's own rows
   const int w_row0 = row0 + 32 * wave;
   const bool w_on = w_row0 < rows;
@@ -303,7 +311,6 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a) {
   // ---- output: channels 32 d + 8 (i / 4) + 4 h + i % 4 of the lane's row
   l += __shfl_xor(l, 32);
   if (!there) return;
-  const int64_t total_rows = a.total_q * a.hq;
   const int64_t at = (int64_t)(q0 + rt) * a.hq + hk * a.per + rg;
   if (a.parts > 1) {
     const int64_t part = (int64_t)(a.part0 + split) * total_rows + at;
@@ -336,7 +343,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a) {
 template <int D, int BITS, int GS>
 hipError_t tile_t(const AttnArgs& a, hipStream_t st) {
   const int tiles = (int)(((int64_t)a.max_q * a.per + kRows - 1) / kRows);
-  k_kv_tile<D, BITS, GS><<<dim3(a.nsplit, a.f.hkv * tiles, a.num_seqs), 512, 0, st>>>(a);
+  k_kv_tile<D, BITS, GS><<<dim3(a.f.hkv * a.num_seqs, tiles, a.nsplit), 512, 0, st>>>(a);
   return hipGetLastError();
 }
 
