@@ -74,8 +74,9 @@ int64_t row_tiles(int64_t rows, int kind) {
 // Key splits: enough blocks to fill the 256 CUs several times over (a tile block fills one), at least
 // 256 keys each.
 void split_keys(AttnArgs* a, int kind, int64_t blocks, int64_t keys) {
-  const int64_t want = kind == kTile ? 256 : 2048;
+  const int64_t want = kind == kTile ? 256 : 1024;
   int64_t n = kind == kTile ? want / blocks : (want + blocks - 1) / blocks;
+  if (kind != kTile && keys / 2048 > n) n = keys / 2048;
   const int64_t most = (keys + 255) / 256;
   n = n > most ? most : n;
   n = n < 1 ? 1 : n;

@@ -143,9 +143,10 @@ __global__ __launch_bounds__(256, stream_blocks(D, GS, NT)) void k_kv_stream(Att
     Ids x;
 #pragma unroll
     for (int t = 0; t < (PAIR ? 1 : 2); ++t) {
+      // (the entry is loaded before the length that says whether it counts has arrived)
       const int key = key0 + 16 * t;
-      x.id[t] = key < ke ? table[key >> a.f.page_shift] : -1;
-      x.id[t] = (uint32_t)x.id[t] < a.f.num_pages ? x.id[t] : -1;
+      const int id = a.table_cols > 0 ? table[min(key >> a.f.page_shift, a.table_cols - 1)] : -1;
+      x.id[t] = key < ke && (uint32_t)id < a.f.num_pages ? id : -1;
     }
     if (PAIR) x.id[1] = x.id[0];
     return x;
@@ -495,44 +496,69 @@ __global__ __launch_bounds__(256, stream_blocks(D, GS, NT)) void k_kv_stream(Att
   }
 }
 
-// Joins the parts of each row: a wave a row.
+// Joins the parts of each row: a wave a row.  The parts that hold keys are listed first (their
+// weights a lane each), then read 64 / (D / 4) at a time, 16 bytes a lane, four such reads in flight.
 template <int D>
 __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a) {
+  constexpr int LP = D / 4, PP = 64 / LP;
   const int64_t total_rows = a.total_q * a.hq;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (row >= total_rows) return;
-  const int lane = threadIdx.x & 63;
-  float top = kNoKey;
-  for (int p = lane; p < a.parts; p += 64) {
-    const float2 ml = a.part_ml[p * total_rows + row];
-    if (ml.y != 0.f) top = fmaxf(top, ml.x);
+  const int lane = threadIdx.x & 63, sub = lane / LP, d = lane % LP * 4;
+  float2 ml = float2{kNoKey, 0.f};
+  if (lane < a.parts) ml = a.part_ml[lane * total_rows + row];
+  float top = ml.y != 0.f ? ml.x : kNoKey;
+  for (int p = lane + 64; p < a.parts; p += 64) {
+    const float2 x = a.part_ml[p * total_rows + row];
+    if (x.y != 0.f) top = fmaxf(top, x.x);
   }
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+  for (int i = 1; i < 64; i <<= 1) top = fmaxf(top, __shfl_xor(top, i));
   float sum = 0.f;
-  f32x2 x = {0.f, 0.f};
-#pragma unroll 4
-  for (int p = 0; p < a.parts; ++p) {
-    const int64_t at = p * total_rows + row;
-    const float2 ml = a.part_ml[at];
-    if (ml.y != 0.f) {
-      const float f = exp2_(ml.x - top);
-      sum += f * ml.y;
-      const float* from = a.part_o + at * D;
-      if (D == 128)
-        x += *reinterpret_cast<const f32x2*>(from + 2 * lane) * f;
-      else
-        x[0] += from[lane] * f;
+  f32x4 o = {0.f, 0.f, 0.f, 0.f};
+  for (int p0 = 0; p0 < a.parts; p0 += 64) {
+    if (p0) {
+      ml = float2{kNoKey, 0.f};
+      if (p0 + lane < a.parts) ml = a.part_ml[(p0 + lane) * total_rows + row];
+    }
+    const bool on = ml.y != 0.f;
+    const float w = on ? exp2_(ml.x - top) : 0.f;
+    sum += on ? w * ml.y : 0.f;
+    const uint64_t mask = __ballot(on), below = (1ull << lane) - 1;
+    const int count = __popcll(mask);
+    const int to = on ? __popcll(mask & below) : count + __popcll(~mask & below);
+    const int listed = __builtin_amdgcn_ds_permute(4 * to, lane);  // lane i: the i-th part with keys
+    for (int k = 0; k < count; k += 4 * PP) {
+      f32x4 x[4];
+      float wx[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = k + u * PP + sub;
+        const int part = __shfl(listed, i < count ? i : 0);
+        wx[u] = __shfl(w, part);
+        if (i >= count) wx[u] = 0.f;
+        x[u] = *reinterpret_cast<const f32x4*>(a.part_o + ((p0 + part) * total_rows + row) * D + d);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) o += x[u] * wx[u];
     }
   }
-  const float inv = sum != 0.f ? 1.0f / sum : 0.f;
-  uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + row * D;
-  const uint32_t w = a.dtype == HQQ_KV_BF16 ? pack2<true>(x[0] * inv, x[1] * inv) : pack2<false>(x[0] * inv, x[1] * inv);
-  if (D == 128)
-    *reinterpret_cast<uint32_t*>(to + 2 * lane) = w;
-  else
-    to[lane] = (uint16_t)w;
-  if (a.lse && lane == 0) a.lse[row] = sum != 0.f ? (top + __log2f(sum)) * 0.69314718056f : -INFINITY;
+#pragma unroll
+  for (int i = 1; i < 64; i <<= 1) sum += __shfl_xor(sum, i);
+#pragma unroll
+  for (int i = LP; i < 64; i <<= 1)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[c] += __shfl_xor(o[c], i);
+  if (sub == 0) {
+    const float inv = sum != 0.f ? 1.0f / sum : 0.f;
+    u32x2 w;
+    if (a.dtype == HQQ_KV_BF16)
+      w = u32x2{pack2<true>(o[0] * inv, o[1] * inv), pack2<true>(o[2] * inv, o[3] * inv)};
+    else
+      w = u32x2{pack2<false>(o[0] * inv, o[1] * inv), pack2<false>(o[2] * inv, o[3] * inv)};
+    *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + row * D + d) = w;
+    if (a.lse && lane == 0) a.lse[row] = sum != 0.f ? (top + __log2f(sum)) * 0.69314718056f : -INFINITY;
+  }
 }
 
 template <int D, int BITS, int GS, int NT>
