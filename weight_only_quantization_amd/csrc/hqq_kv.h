@@ -46,40 +46,55 @@ struct ReadArgs {
   void* v;
 };
 
-// One pass of attention rows over one list of keys per sequence (lens, table), or over a list that
-// all rows share (lens == nullptr: fixed_len keys, one "sequence" of every query token).
+// A list of keys for every sequence: each its own, or one that all query tokens share (lens == nullptr:
+// fixed_len keys, a single "sequence" of every query token).
+struct KeyList {
+  const int32_t* table;
+  int64_t table_stride;
+  int table_cols;
+  const int32_t* lens;
+  int fixed_len, max_len;
+  const int32_t* cu_q;
+  int num_seqs, tq, max_q;
+  int causal;
+  // where the partial results of its rows begin (in rows of part_o), and their layout: the stream's
+  // segments of `cap` rows (see Schedule), or split s of row r at s * total_rows + r (tiles)
+  int64_t part0;
+  int tiled;
+  int nsplit, chunk;  // tiles: key splits and the keys of one
+  int32_t* segments;  // stream: per pair, its first segment and their number
+  int cap;            // stream: rows of a segment, min(16 NT, the widest sequence's rows)
+};
+
 struct AttnArgs {
   Format f;
   const void* q;
   int64_t q_ts, q_hs;
   int dtype;
   int hq, per;  // query heads, query heads of one KV head
-  int num_seqs, tq, max_q;
   int64_t total_q;
-  const int32_t* cu_q;
-  const int32_t* table;
-  int64_t table_stride;
-  int table_cols;
-  const int32_t* lens;
-  int fixed_len, max_len;
-  int causal;
   float scale_log2;  // softmax scale * log2(e)
-  int nsplit, chunk;  // key splits and the keys of one
-  // nsplit_total == 1: the rows go to out (and lse); else to the partials, from index part0 on
+  KeyList list[2];   // the sequences' own keys, the shared prefix
+  int joined;        // partial results of both lists meet in the join: no row is finished before it
+  int first_list, lists;  // stream: the lists of this launch
+  int blocks;             // stream: the grid
   void* out;
   float* lse;
-  float* part_o;    // [parts][total_q * hq][D], not divided by the sum
-  float2* part_ml;  // [parts][total_q * hq]: running maximum (log2 units) and sum
-  int part0, parts;
+  float* part_o;    // [rows][D], not divided by the sum
+  float2* part_ml;  // [rows]: running maximum (log2 units) and sum
 };
 
 hipError_t launch_kv_write(const WriteArgs& a, int D, int bits, int gs, int dtype, hipStream_t st);
 hipError_t launch_kv_read(const ReadArgs& a, int D, int bits, int gs, int dtype, hipStream_t st);
-// Rows of up to 16 * NT per wave, streamed keys; NT 1 or 2.
+// Rows of up to 16 * nt per block, streamed keys; nt 1 or 2.  stream_blocks: the grid that fills the GPU.
+int stream_blocks(int D, int gs, int nt);
 hipError_t launch_kv_stream(const AttnArgs& a, int D, int bits, int gs, int nt, hipStream_t st);
-// Tiles of 256 rows.
-hipError_t launch_kv_tile(const AttnArgs& a, int D, int bits, int gs, hipStream_t st);
-hipError_t launch_kv_join(const AttnArgs& a, int D, hipStream_t st);
+// Tiles of 256 rows of list `which`.
+hipError_t launch_kv_tile(const AttnArgs& a, int which, int D, int bits, int gs, hipStream_t st);
+// Joins the partial results of every row; nt: of the stream's lists.
+hipError_t launch_kv_join(const AttnArgs& a, int D, int nt_own, int nt_prefix, hipStream_t st);
+
+constexpr int kUnitKeys = 128;  // keys of the stream's unit of work: a step of each of a block's four waves
 
 constexpr float kNoKey = -1e30f;  // running maximum before any key (finite: differences of two stay numbers)
 
@@ -88,8 +103,7 @@ __device__ __forceinline__ h2 as_h2(uint32_t v) { return __builtin_bit_cast(h2, 
 __device__ __forceinline__ uint32_t as_u32(h2 v) { return __builtin_bit_cast(uint32_t, v); }
 
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* p, float (&x)[8]) {
-  const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+__device__ __forceinline__ void floats8(u32x4 w, float (&x)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     if (BF16) {
@@ -101,6 +115,17 @@ __device__ __forceinline__ void load8(const void* p, float (&x)[8]) {
       x[2 * i + 1] = (float)t.y;
     }
   }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* p, float (&x)[8]) {
+  floats8<BF16>(*reinterpret_cast<const u32x4*>(p), x);
+}
+__device__ __forceinline__ void floats8(u32x4 w, int dtype, float (&x)[8]) {
+  if (dtype == HQQ_KV_BF16)
+    floats8<true>(w, x);
+  else
+    floats8<false>(w, x);
 }
 
 template <bool BF16>
@@ -122,17 +147,27 @@ __device__ __forceinline__ u32x4 pack8(const float (&x)[8]) {
   return w;
 }
 
-// A block's KV head and sequence (grid x), row tile (y) and key split (z).  Blocks go round the eight
-// XCDs in order of x, so the pairs are turned by tile and split: the parts of one long sequence
-// spread over all XCDs, and so do those of short ones, which end early.  (With the split in x, XCD 0 had every
-// sequence's first keys and XCD 7 only the longest ones': 35 us for the ragged lengths of 32 sequences of
-// up to 4096 keys, as long as if all had 4096.)
-struct BlockPlace {
-  int hk, seq, tile, split;
+// An entry of an array that no kernel of the call writes, at an index all lanes share: a scalar load.
+__device__ __forceinline__ int entry(const int32_t* p, int64_t i) {
+  return reinterpret_cast<const __attribute__((address_space(4))) int32_t*>(reinterpret_cast<uintptr_t>(p))[i];
+}
+
+// Query tokens and keys of a sequence of a list; nothing of it (tq = 0) where its range of query tokens
+// leaves the query tensor.
+struct Sequence {
+  int q0, tq, len;
 };
-__device__ __forceinline__ BlockPlace block_place(int hkv) {
-  const uint32_t pair = (blockIdx.x + blockIdx.y + blockIdx.z) % gridDim.x;
-  return {(int)(pair % hkv), (int)(pair / hkv), (int)blockIdx.y, (int)blockIdx.z};
+template <bool SHARED>  // SHARED: all lanes ask for the same sequence
+__device__ __forceinline__ Sequence sequence_of(const AttnArgs& a, const KeyList& l, int seq) {
+  auto at = [](const int32_t* p, int i) { return SHARED ? entry(p, i) : p[i]; };
+  Sequence s{seq * l.tq, l.tq, l.lens ? at(l.lens, seq) : l.fixed_len};
+  if (l.cu_q) {
+    s.q0 = at(l.cu_q, seq);
+    s.tq = at(l.cu_q, seq + 1) - s.q0;
+    if (s.q0 < 0 || s.tq < 0 || s.tq > l.max_q || (int64_t)s.q0 + s.tq > a.total_q) s.tq = 0;
+  }
+  s.len = min(min(max(s.len, 0), l.max_len), l.table_cols << a.f.page_shift);
+  return s;
 }
 
 // Page id and address of a slot; nullptr where the slot is outside the cache.

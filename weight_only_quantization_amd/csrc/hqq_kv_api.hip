@@ -10,6 +10,7 @@ namespace {
 using hqq::api_fail;
 using hqq::kv::AttnArgs;
 using hqq::kv::Format;
+using hqq::kv::KeyList;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -53,43 +54,47 @@ int check_cache(const hqq_kv_cache& c, Format* f) {
 
 bool known_type(int dtype) { return dtype == HQQ_KV_F16 || dtype == HQQ_KV_BF16; }
 
-// The passes of one attention call: over the sequences' own keys, and over the shared prefix.
+// One attention call: its kernels' arguments, the row kernel of each list, the workspace.
+enum { kStream16, kStream32, kTile };  // the stream with 16 or 32 rows a block, or tiles of 256 rows
+
 struct Plan {
-  AttnArgs own, prefix;
-  int own_kind, prefix_kind;  // row kernel of each
-  bool has_prefix;
-  int parts;
+  AttnArgs a;
+  int kind[2];
+  bool join;
+  int64_t part_rows, segment_words;
   size_t workspace;
 };
 
-// Row kernels: the stream with 16 or 32 rows a wave, or tiles of 256 rows.
-enum { kStream16, kStream32, kTile };
-
 int row_kernel(int64_t rows) { return rows <= 16 ? kStream16 : rows <= 64 ? kStream32 : kTile; }
+int nt_of(int kind) { return kind == kStream16 ? 1 : 2; }
 int64_t row_tiles(int64_t rows, int kind) {
   const int64_t of = kind == kStream16 ? 16 : kind == kStream32 ? 32 : 256;
   return (rows + of - 1) / of;
 }
 
-// Key splits: enough blocks to fill the 256 CUs several times over (a tile block fills one), at least
-// 256 keys each.
-void split_keys(AttnArgs* a, int kind, int64_t blocks, int64_t keys) {
-  const int64_t want = kind == kTile ? 256 : 1024;
-  int64_t n = kind == kTile ? want / blocks : (want + blocks - 1) / blocks;
-  if (kind != kTile && keys / 2048 > n) n = keys / 2048;
-  const int64_t most = (keys + 255) / 256;
+// Key splits of the tiles: enough blocks for the 256 CUs (a block fills one), at least 256 keys each.
+void split_keys(KeyList* l, int64_t blocks) {
+  const int64_t keys = l->max_len, most = (keys + 255) / 256;
+  int64_t n = 256 / blocks;
   n = n > most ? most : n;
   n = n < 1 ? 1 : n;
-  int64_t chunk = ((keys + n - 1) / n + 127) / 128 * 128;
-  chunk = chunk < 128 ? 128 : chunk;
-  a->chunk = (int)chunk;
-  a->nsplit = (int)((keys + chunk - 1) / chunk);
-  if (a->nsplit < 1) a->nsplit = 1;
+  const int64_t chunk = ((keys + n - 1) / n + 127) / 128 * 128;
+  l->chunk = (int)(chunk < 128 ? 128 : chunk);
+  l->nsplit = (int)((keys + l->chunk - 1) / l->chunk);
+  if (l->nsplit < 1) l->nsplit = 1;
 }
 
-hipError_t launch_pass(const AttnArgs& a, int kind, const hqq_kv_cache& c, hipStream_t st) {
-  if (kind == kTile) return hqq::kv::launch_kv_tile(a, c.head_dim, c.nbits, c.group_size, st);
-  return hqq::kv::launch_kv_stream(a, c.head_dim, c.nbits, c.group_size, kind == kStream16 ? 1 : 2, st);
+// Blocks of a stream launch: what fills the GPU, but at least two units each.
+int stream_grid(const Plan& p, const hqq_kv_cache& c, int first, int lists) {
+  int64_t units = 0;
+  for (int i = first; i < first + lists; ++i) {
+    const KeyList& l = p.a.list[i];
+    const int64_t keys = l.max_len > 0 ? (l.max_len + hqq::kv::kUnitKeys - 1) / hqq::kv::kUnitKeys : 1;
+    units += keys * l.num_seqs * p.a.f.hkv * row_tiles((int64_t)l.max_q * p.a.per, p.kind[i]);
+  }
+  const int64_t most = hqq::kv::stream_blocks(c.head_dim, c.group_size, nt_of(p.kind[first]));
+  const int64_t n = (units + 1) / 2;
+  return (int)(n > most ? most : n < 1 ? 1 : n);
 }
 
 int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
@@ -121,7 +126,8 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
   KV_NEED(x->causal == 0 || x->causal == 1, HQQ_ERR_INVALID_ARGUMENT, "causal must be 0 or 1");
   KV_NEED(x->scale > 0.f && x->scale <= 3.0e38f, HQQ_ERR_INVALID_ARGUMENT, "scale must be finite and positive");
 
-  AttnArgs a{};
+  *p = Plan{};
+  AttnArgs& a = p->a;
   a.f = f;
   a.q = x->q;
   a.q_ts = x->q_token_stride;
@@ -129,57 +135,72 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
   a.dtype = x->dtype;
   a.hq = x->num_q_heads;
   a.per = x->num_q_heads / c.num_kv_heads;
-  a.num_seqs = (int)x->num_seqs;
-  a.tq = x->num_seqs ? (int)(x->total_q / x->num_seqs) : 0;
-  a.max_q = x->cu_q ? (int)x->max_q : a.tq;
   a.total_q = x->total_q;
-  a.cu_q = x->cu_q;
-  a.table = x->page_table;
-  a.table_stride = x->table_stride;
-  a.table_cols = (int)x->table_cols;
-  a.lens = x->seq_lens;
-  a.max_len = (int)x->max_len;
-  a.causal = x->causal;
   a.scale_log2 = x->scale * 1.44269504089f;
   a.out = x->out;
   a.lse = x->lse;
-  p->own = p->prefix = a;
-  p->has_prefix = x->prefix_len > 0;
-  p->workspace = 0;
-  p->parts = 1;
-  if (x->total_q == 0 || x->num_seqs == 0 || a.max_q == 0) return HQQ_OK;
-
-  const int64_t rows = (int64_t)a.max_q * a.per;
-  p->own_kind = row_kernel(rows);
-  const int64_t tiles = row_tiles(rows, p->own_kind);
+  a.joined = x->prefix_len > 0;
+  KeyList& own = a.list[0];
+  own.table = x->page_table;
+  own.table_stride = x->table_stride;
+  own.table_cols = (int)x->table_cols;
+  own.lens = x->seq_lens;
+  own.max_len = (int)x->max_len;
+  own.cu_q = x->cu_q;
+  own.num_seqs = (int)x->num_seqs;
+  own.tq = x->num_seqs ? (int)(x->total_q / x->num_seqs) : 0;
+  own.max_q = x->cu_q ? (int)x->max_q : own.tq;
+  own.causal = x->causal;
+  if (x->total_q == 0 || x->num_seqs == 0 || own.max_q == 0) return HQQ_OK;
   KV_NEED(x->num_seqs <= 65535, HQQ_ERR_UNSUPPORTED, "at most 65535 sequences in a call");
-  KV_NEED(tiles <= 65535, HQQ_ERR_UNSUPPORTED, "too many query rows in a sequence");
-  split_keys(&p->own, p->own_kind, tiles * f.hkv * x->num_seqs, x->max_len);
-  p->parts = p->own.nsplit;
-  if (p->has_prefix) {
-    AttnArgs& b = p->prefix;
-    b.num_seqs = 1;
-    b.tq = b.max_q = (int)x->total_q;
-    b.cu_q = nullptr;
-    b.table = x->prefix_table;
-    b.table_stride = 0;
-    b.table_cols = (int)((x->prefix_len + c.page_size - 1) / c.page_size);
-    b.lens = nullptr;
-    b.fixed_len = b.max_len = (int)x->prefix_len;
-    b.causal = 0;
-    const int64_t all = x->total_q * a.per;
-    p->prefix_kind = row_kernel(all);
-    const int64_t t = row_tiles(all, p->prefix_kind);
-    KV_NEED(t <= 65535, HQQ_ERR_UNSUPPORTED, "too many query rows in a call");
-    split_keys(&b, p->prefix_kind, t * f.hkv, x->prefix_len);
-    b.part0 = p->own.nsplit;
-    p->parts += b.nsplit;
+  KeyList& pre = a.list[1];
+  if (a.joined) {
+    pre.table = x->prefix_table;
+    pre.table_cols = (int)((x->prefix_len + c.page_size - 1) / c.page_size);
+    pre.fixed_len = pre.max_len = (int)x->prefix_len;
+    pre.num_seqs = 1;
+    pre.tq = pre.max_q = (int)x->total_q;
   }
-  p->own.parts = p->prefix.parts = p->parts;
-  if (p->parts > 1) {
-    const size_t all_rows = (size_t)x->total_q * x->num_q_heads;
-    p->workspace = (size_t)p->parts * all_rows * (4 * (size_t)c.head_dim + sizeof(float2));
+  p->join = a.joined;
+  for (int i = 0; i < (a.joined ? 2 : 1); ++i) {
+    KeyList& l = a.list[i];
+    const int64_t rows = (int64_t)l.max_q * a.per;
+    p->kind[i] = row_kernel(rows);
+    const int64_t tiles = row_tiles(rows, p->kind[i]), pairs = tiles * f.hkv * l.num_seqs;
+    KV_NEED(tiles <= 65535 && pairs * (l.max_len / hqq::kv::kUnitKeys + 1) <= (int64_t(1) << 30), HQQ_ERR_UNSUPPORTED,
+            "too many query rows and keys in a call");
+    if (p->kind[i] == kTile) {
+      l.tiled = 1;
+      split_keys(&l, pairs);
+      if (l.nsplit > 1) p->join = true;
+    } else {
+      const int64_t most = 16 * nt_of(p->kind[i]);
+      l.cap = (int)(rows < most ? rows : most);
+      if (l.max_len > hqq::kv::kUnitKeys) p->join = true;
+    }
   }
+  if (!p->join) {
+    if (p->kind[0] != kTile) a.blocks = stream_grid(*p, c, 0, 1);
+    return HQQ_OK;
+  }
+  // the lists' partial results, one after the other; the streams' segment lists behind them
+  for (int i = 0; i < (a.joined ? 2 : 1); ++i) {
+    KeyList& l = a.list[i];
+    l.part0 = p->part_rows;
+    const int64_t rows = (int64_t)l.max_q * a.per;
+    if (p->kind[i] == kTile) {
+      if (l.nsplit > 1 || a.joined) p->part_rows += l.nsplit * x->total_q * a.hq;
+      continue;
+    }
+    const int64_t pairs = row_tiles(rows, p->kind[i]) * f.hkv * l.num_seqs;
+    const int64_t grid = hqq::kv::stream_blocks(c.head_dim, c.group_size, nt_of(p->kind[i]));
+    // (segments are counted over the pairs of both lists where one launch takes both)
+    const int64_t segments = a.joined ? grid + pairs + (i ? row_tiles((int64_t)own.max_q * a.per, p->kind[0]) * f.hkv * own.num_seqs : 0)
+                                      : 2 * grid;
+    p->part_rows += segments * l.cap;
+    p->segment_words += 2 * pairs;
+  }
+  p->workspace = (size_t)p->part_rows * (4 * (size_t)c.head_dim + sizeof(float2)) + (size_t)p->segment_words * 4;
   return HQQ_OK;
 }
 
@@ -187,7 +208,8 @@ int run_attention(const hqq_kv_attention_args* x) {
   Plan p;
   const int st = plan_attention(x, false, &p);
   if (st != HQQ_OK) return st;
-  if (x->total_q == 0 || p.own.max_q == 0) return HQQ_OK;
+  AttnArgs& a = p.a;
+  if (x->total_q == 0 || a.list[0].max_q == 0) return HQQ_OK;
   const hqq_kv_cache& c = x->cache;
   KV_NEED(x->q && aligned16(x->q) && x->out && aligned16(x->out), HQQ_ERR_INVALID_ARGUMENT,
           "q and out must be 16-byte aligned pointers");
@@ -195,21 +217,36 @@ int run_attention(const hqq_kv_attention_args* x) {
           HQQ_ERR_INVALID_ARGUMENT, "q strides must be non-negative multiples of 8 elements");
   KV_NEED(x->seq_lens, HQQ_ERR_INVALID_ARGUMENT, "seq_lens must not be NULL");
   KV_NEED(x->page_table || x->table_cols == 0, HQQ_ERR_INVALID_ARGUMENT, "page_table must not be NULL");
-  KV_NEED(!p.has_prefix || x->prefix_table, HQQ_ERR_INVALID_ARGUMENT, "prefix_table must not be NULL");
+  KV_NEED(!a.joined || x->prefix_table, HQQ_ERR_INVALID_ARGUMENT, "prefix_table must not be NULL");
   if (p.workspace) {
     KV_NEED(x->workspace && x->workspace_bytes >= p.workspace, HQQ_ERR_WORKSPACE,
             "workspace missing or smaller than hqq_kv_attention_workspace_bytes");
     KV_NEED(aligned16(x->workspace), HQQ_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
-    const size_t all_rows = (size_t)x->total_q * x->num_q_heads;
-    p.own.part_o = p.prefix.part_o = static_cast<float*>(x->workspace);
-    p.own.part_ml = p.prefix.part_ml =
-        reinterpret_cast<float2*>(static_cast<float*>(x->workspace) + (size_t)p.parts * all_rows * c.head_dim);
+    a.part_o = static_cast<float*>(x->workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + p.part_rows * c.head_dim);
+    int32_t* words = reinterpret_cast<int32_t*>(a.part_ml + p.part_rows);
+    for (int i = 0; i < (a.joined ? 2 : 1); ++i) {
+      if (p.kind[i] == kTile) continue;
+      KeyList& l = a.list[i];
+      l.segments = words;
+      words += 2 * row_tiles((int64_t)l.max_q * a.per, p.kind[i]) * a.f.hkv * l.num_seqs;
+    }
   }
   hipStream_t stream = static_cast<hipStream_t>(x->stream);
+  const int D = c.head_dim, bits = c.nbits, gs = c.group_size, lists = a.joined ? 2 : 1;
   hipError_t e = hipSuccess;
-  if (p.has_prefix) e = launch_pass(p.prefix, p.prefix_kind, c, stream);
-  if (e == hipSuccess) e = launch_pass(p.own, p.own_kind, c, stream);
-  if (e == hipSuccess && p.parts > 1) e = hqq::kv::launch_kv_join(p.own, c.head_dim, stream);
+  // tiles of a prefix first (the longest work), then the streams: one launch where both lists stream alike
+  for (int i = lists - 1; i >= 0 && e == hipSuccess; --i)
+    if (p.kind[i] == kTile) e = hqq::kv::launch_kv_tile(a, i, D, bits, gs, stream);
+  for (int i = 0; i < lists && e == hipSuccess; ++i) {
+    if (p.kind[i] == kTile) continue;
+    a.first_list = i;
+    a.lists = i == 0 && lists == 2 && p.kind[1] == p.kind[0] ? 2 : 1;
+    a.blocks = stream_grid(p, c, i, a.lists);
+    e = hqq::kv::launch_kv_stream(a, D, bits, gs, nt_of(p.kind[i]), stream);
+    i += a.lists - 1;
+  }
+  if (e == hipSuccess && p.join) e = hqq::kv::launch_kv_join(a, D, nt_of(p.kind[0]), nt_of(p.kind[1]), stream);
   return device_status(e);
 }
 

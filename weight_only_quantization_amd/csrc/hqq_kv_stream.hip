@@ -79,15 +79,35 @@ constexpr uint32_t pair_sel(int t, int b) {
   return 0x0c000c00u | sy << 16 | sx;
 }
 
-// Blocks (waves per SIMD) that the registers are held to: the most that does not spill.
-constexpr int stream_blocks(int D, int GS, int NT) {
+// Waves per SIMD (blocks per CU) that the registers are held to: the most that does not spill.
+constexpr int stream_waves(int D, int GS, int NT) {
   if (NT == 1) return D == 64 ? (GS == 64 ? 4 : 3) : D / GS <= 2 ? 3 : 2;
-  return D == 64 ? (GS == 64 ? 3 : 2) : D / GS <= 2 ? 2 : 1;
+  return D == 64 || D / GS <= 2 ? 2 : 1;
 }
+
+// The work of a launch: units of 128 keys of every (sequence, row tile, KV head), in one order, cut into
+// equal shares, one a block.  A block walks the pieces ("segments") of its share; a pair that several
+// blocks share leaves a partial result per segment, a pair within one share is finished there.
+// Lengths live on the device, so every wave works the cut out for itself.
+struct Share {
+  uint32_t per, more;  // units of a block; the first `more` blocks have one more
+  __device__ uint32_t begin(uint32_t i) const { return i * per + min(i, more); }
+  __device__ uint32_t block_of(uint32_t u) const {
+    const uint32_t wide = more * (per + 1);
+    return u < wide ? u / (per + 1) : more + (u - wide) / per;
+  }
+};
+
+template <int NT>
+__device__ __forceinline__ uint32_t tiles_of(const AttnArgs& a, int tq) {
+  return (uint32_t)(tq * a.per + 16 * NT - 1) / (16 * NT);
+}
+// (a sequence without keys has one unit: its rows are written all the same)
+__device__ __forceinline__ uint32_t units_of(int len) { return max(1u, (uint32_t)(len + kUnitKeys - 1) / kUnitKeys); }
 
 // PAIR: pages of at least 32 tokens, so a step's two tiles share a page (one lookup, one address).
 template <int D, int BITS, int GS, int NT, bool PAIR>
-__global__ __launch_bounds__(256, stream_blocks(D, GS, NT)) void k_kv_stream(AttnArgs a) {
+__global__ __launch_bounds__(256, stream_waves(D, GS, NT)) void k_kv_stream(AttnArgs a) {
   using G = Geo<D, BITS>;
   constexpr int NG = D / GS;
   constexpr int kLdsRow = D + 4;
@@ -96,44 +116,92 @@ __global__ __launch_bounds__(256, stream_blocks(D, GS, NT)) void k_kv_stream(Att
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, h = lane >> 4;
-  const BlockPlace place = block_place(a.f.hkv);
-  const int split = place.split, hk = place.hk, tile = place.tile, seq = place.seq;
+  const int page = 1 << a.f.page_shift;
 
-  // the sequence's query tokens and keys
-  int q0 = seq * a.tq, tq = a.tq;
-  if (a.cu_q) {
-    q0 = a.cu_q[seq];
-    tq = a.cu_q[seq + 1] - q0;
-    // (offsets outside the query tensor leave the sequence out)
-    if (q0 < 0 || tq < 0 || tq > a.max_q || (int64_t)q0 + tq > a.total_q) tq = 0;
+  // ---- the block's share, and where it begins
+  auto weight = [&](const KeyList& l, int seq) -> uint32_t {
+    const Sequence s = sequence_of<false>(a, l, seq);
+    return units_of(s.len) * tiles_of<NT>(a, s.tq) * a.f.hkv;
+  };
+  uint32_t total = 0;
+  for (int li = a.first_list; li < a.first_list + a.lists; ++li) {
+    const KeyList l = li ? a.list[1] : a.list[0];
+    for (int s0 = 0; s0 < l.num_seqs; s0 += 64) {
+      uint32_t w = s0 + lane < l.num_seqs ? weight(l, s0 + lane) : 0;
+#pragma unroll
+      for (int i = 1; i < 64; i <<= 1) w += __shfl_xor(w, i);
+      total += w;
+    }
   }
+  total = __builtin_amdgcn_readfirstlane(total);
+  const uint32_t blocks = min((uint32_t)a.blocks, total);
+  if (blockIdx.x >= blocks) return;
+  const uint32_t per_block = __builtin_amdgcn_readfirstlane(total / blocks);
+  const Share share{per_block, total - per_block * blocks};
+  uint32_t u = share.begin(blockIdx.x);
+  const uint32_t u_end = share.begin(blockIdx.x + 1);
+  int li = a.first_list, seq = 0;
+  uint32_t before = 0, pairs = 0;  // units and pairs in front of the sequence
+  for (bool found = false; !found;) {
+    const KeyList l = li ? a.list[1] : a.list[0];
+    for (int s0 = 0; s0 < l.num_seqs && !found; s0 += 64) {
+      uint32_t w = 0, p = 0;
+      if (s0 + lane < l.num_seqs) {
+        const Sequence s = sequence_of<false>(a, l, s0 + lane);
+        p = tiles_of<NT>(a, s.tq) * a.f.hkv;
+        w = units_of(s.len) * p;
+      }
+      uint32_t wi = w, pi = p;
+#pragma unroll
+      for (int i = 1; i < 64; i <<= 1) {
+        const uint32_t x = __shfl_up(wi, i), y = __shfl_up(pi, i);
+        if (lane >= i) wi += x, pi += y;
+      }
+      const uint64_t past = __ballot(before + wi > u);
+      if (past) {
+        const int at = __builtin_ctzll(past);
+        seq = s0 + at;
+        before += __shfl(wi - w, at);
+        pairs += __shfl(pi - p, at);
+        found = true;
+      } else {
+        before += __shfl(wi, 63);
+        pairs += __shfl(pi, 63);
+      }
+    }
+    if (!found) ++li;
+  }
+  seq = __builtin_amdgcn_readfirstlane(seq);
+  before = __builtin_amdgcn_readfirstlane(before);
+  pairs = __builtin_amdgcn_readfirstlane(pairs);
+  const uint32_t u_begin = u;
+  KeyList list = li ? a.list[1] : a.list[0];
+  Sequence sq_ = sequence_of<true>(a, list, seq);
+  uint32_t units = units_of(sq_.len);
+  // within the sequence: tile * hkv + KV head, and the first unit of the segment
+  uint32_t pair = __builtin_amdgcn_readfirstlane((u - before) / units);
+  uint32_t x0 = (u - before) - pair * units;
+  pairs += pair;
+
+  while (true) {
+  const int q0 = sq_.q0, tq = sq_.tq, len = sq_.len;
+  const int tile = __builtin_amdgcn_readfirstlane(pair / a.f.hkv), hk = pair - tile * a.f.hkv;
+  const uint32_t x1 = min(units, x0 + (u_end - u));
   const int rows = tq * a.per;
   const int row0 = tile * 16 * NT;
-  if (row0 >= rows) return;
-  const int page = 1 << a.f.page_shift;
-  int len = a.lens ? a.lens[seq] : a.fixed_len;
-  len = min(min(max(len, 0), a.max_len), a.table_cols << a.f.page_shift);
-  const int last_t = (min(row0 + 16 * NT, rows) - 1) / a.per;
-  const int end_all = a.causal ? min(len, max(0, len - tq + last_t + 1)) : len;
-  const int kb = split * a.chunk;
-  const int ke = min(kb + a.chunk, end_all);
-  const int64_t total_rows = a.total_q * a.hq;
-  if (kb >= end_all && a.parts > 1) {  // no key of this split
-    const int row = row0 + threadIdx.x;
-    if (threadIdx.x < 16 * NT && row < rows)
-      a.part_ml[(int64_t)(a.part0 + split) * total_rows + (int64_t)(q0 + row / a.per) * a.hq + hk * a.per + row % a.per] =
-          float2{kNoKey, 0.f};
-    return;
-  }
-  const int first_t = row0 / a.per;
-  const int end_min = a.causal ? len - tq + first_t + 1 : len;  // keys below it are seen by every row
+  const int last_t = __builtin_amdgcn_readfirstlane((min(row0 + 16 * NT, rows) - 1) / a.per);
+  const int end_all = list.causal ? min(len, max(0, len - tq + last_t + 1)) : len;
+  const int kb = x0 * kUnitKeys;
+  const int ke = min((int)x1 * kUnitKeys, end_all);
+  const int first_t = __builtin_amdgcn_readfirstlane(row0 / a.per);
+  const int end_min = list.causal ? len - tq + first_t + 1 : len;  // keys below it are seen by every row
 
   // ---- the wave's first keys are on their way while the queries are prepared
   uint32_t k_off = n * G::kRow + h * (G::kRow / 4);
   uint32_t v_off = page * G::kRow + (h * 16 + n) * (4 * G::kUnit);
   uint32_t km_off = 2 * page * G::kRow + 16 * h;
   uint32_t vm_off = km_off + 4 * page * (NG + (n * (D / 16)) / GS);
-  const int32_t* table = a.table + (int64_t)seq * a.table_stride;
+  const int32_t* table = list.table + (int64_t)seq * list.table_stride;
 
   // page ids of a step's two tiles (-1: past the end, or no such page), loaded a step before the codes
   struct Ids {
@@ -145,7 +213,7 @@ __global__ __launch_bounds__(256, stream_blocks(D, GS, NT)) void k_kv_stream(Att
     for (int t = 0; t < (PAIR ? 1 : 2); ++t) {
       // (the entry is loaded before the length that says whether it counts has arrived)
       const int key = key0 + 16 * t;
-      const int id = a.table_cols > 0 ? table[min(key >> a.f.page_shift, a.table_cols - 1)] : -1;
+      const int id = list.table_cols > 0 ? entry(table, min(key >> a.f.page_shift, list.table_cols - 1)) : -1;
       x.id[t] = key < ke && (uint32_t)id < a.f.num_pages ? id : -1;
     }
     if (PAIR) x.id[1] = x.id[0];
@@ -204,20 +272,19 @@ __global__ __launch_bounds__(256, stream_blocks(D, GS, NT)) void k_kv_stream(Att
     const bool there = r < rows;
     const int rt = (there ? r : row0) / a.per, rg = (there ? r : row0) % a.per;
     const int64_t at = (int64_t)(q0 + rt) * a.q_ts + (int64_t)(hk * a.per + rg) * a.q_hs;
-    float x[G::kMf][8];
+    u32x4 w[G::kMf];
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < G::kMf; ++i) {
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q) + at + 32 * i + 8 * h;
-      if (a.dtype == HQQ_KV_BF16)
-        load8<true>(p, x[i]);
-      else
-        load8<false>(p, x[i]);
+      w[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.q) + at + 32 * i + 8 * h);
+      if (!there) w[i] = u32x4{0, 0, 0, 0};
+    }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[i][j] = there ? x[i][j] : 0.f;
-        top = fmaxf(top, fabsf(x[i][j]));
-      }
+    for (int i = 0; i < G::kMf; ++i) {
+      float x[8];
+      floats8(w[i], a.dtype, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
     }
     top = fmaxf(top, __shfl_xor(top, 16));
     top = fmaxf(top, __shfl_xor(top, 32));
@@ -230,9 +297,11 @@ __global__ __launch_bounds__(256, stream_blocks(D, GS, NT)) void k_kv_stream(Att
     for (int g = 0; g < NG; ++g) sq[t][g] = 0.f;
 #pragma unroll
     for (int i = 0; i < G::kMf; ++i) {
+      float x[8];
+      floats8(w[i], a.dtype, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float y = ldexpf(x[i][j], e);
+        const float y = ldexpf(x[j], e);
         sq[t][i * 32 / GS] += y;
         qf[t][i][j] = (_Float16)(BITS == 4 && (j & 2) ? y * 0.0625f : y);
       }
@@ -243,7 +312,7 @@ __global__ __launch_bounds__(256, stream_blocks(D, GS, NT)) void k_kv_stream(Att
       sq[t][g] += __shfl_xor(sq[t][g], 32);
       sq[t][g] *= 0x1p-24f;  // the scale of the codes' products
     }
-    lim[t] = there ? (a.causal ? min(len - 1, len - tq + rt) : len - 1) : -1;
+    lim[t] = there ? (list.causal ? min(len - 1, len - tq + rt) : len - 1) : -1;
   }
 
   // ---- the stream
@@ -426,6 +495,15 @@ __global__ __launch_bounds__(256, stream_blocks(D, GS, NT)) void k_kv_stream(Att
   }
 
   // ---- the block's four waves joined, then written
+  const bool whole = x0 == 0 && x1 == units;
+  // a pair's segment: of the block's share the first one or the last one; with a join of both lists every
+  // pair leaves one (blocks and pairs in front: each further segment adds one to the sum)
+  const uint32_t segment = a.joined ? blockIdx.x + pairs : 2 * blockIdx.x + (u == u_begin ? 0 : 1);
+  if (x0 == 0 && threadIdx.x == 0 && list.segments) {
+    const int64_t at = ((int64_t)seq * tiles_of<NT>(a, list.max_q) + tile) * a.f.hkv + hk;
+    list.segments[2 * at] = segment;
+    list.segments[2 * at + 1] = whole && !a.joined ? 0 : (int)(share.block_of(u + units - 1) - blockIdx.x + 1);
+  }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     l[t] += __shfl_xor(l[t], 16);
@@ -460,8 +538,7 @@ __global__ __launch_bounds__(256, stream_blocks(D, GS, NT)) void k_kv_stream(Att
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) sum += sh_l[w][16 * t + r] * exp2_(sh_m[w][16 * t + r] - rm);
-      const int64_t token = q0 + row / a.per;
-      const int64_t at = token * a.hq + hk * a.per + row % a.per;
+      const int64_t at = (int64_t)(q0 + row / a.per) * a.hq + hk * a.per + row % a.per;
       float x[D / 16];
 #pragma unroll
       for (int j = 0; j < D / 16; j += 4) {
@@ -471,8 +548,8 @@ __global__ __launch_bounds__(256, stream_blocks(D, GS, NT)) void k_kv_stream(Att
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) x[j + jj] = y[jj];
       }
-      if (a.parts > 1) {
-        const int64_t part = (int64_t)(a.part0 + split) * total_rows + at;
+      if (!whole || a.joined) {
+        const int64_t part = list.part0 + (int64_t)segment * list.cap + 16 * t + r;
         if (d0 == 0) a.part_ml[part] = float2{rm, sum};
         float* to = a.part_o + part * D + d0;
         if (sum != 0.f)  // (an empty part's sums are never read)
@@ -494,32 +571,97 @@ __global__ __launch_bounds__(256, stream_blocks(D, GS, NT)) void k_kv_stream(Att
       }
     }
   }
+
+  // ---- the next pair
+  u += x1 - x0;
+  if (u >= u_end) break;
+  ++pair, ++pairs;
+  x0 = 0;
+  if (pair >= tiles_of<NT>(a, tq) * a.f.hkv) {
+    pair = 0;
+    do {
+      if (++seq >= list.num_seqs) list = a.list[1], seq = 0;
+      sq_ = sequence_of<true>(a, list, seq);
+    } while (sq_.tq == 0);
+    units = units_of(sq_.len);
+  }
+  __syncthreads();  // the joined rows have been read
+  }
+}
+
+// Where a row's partial results of one list lie: the first, and the k-th at next + k * step.
+struct Parts {
+  int64_t first, next, step;
+  int count;
+};
+
+__device__ __forceinline__ Parts parts_of(const AttnArgs& a, const KeyList& l, int nt, int64_t token, int head,
+                                          int lane) {
+  const int64_t total_rows = a.total_q * a.hq;
+  if (l.tiled) {
+    const int64_t at = l.part0 + token * a.hq + head;
+    return {at, at, total_rows, l.nsplit};
+  }
+  int seq = 0, t = (int)token;
+  if (l.cu_q) {  // the last sequence that begins at or before the token
+    seq = -1;
+    for (int s0 = 0; s0 < l.num_seqs; s0 += 64) {
+      const uint64_t m = __ballot(s0 + lane < l.num_seqs && l.cu_q[s0 + lane] <= token && token < l.cu_q[s0 + lane + 1]);
+      if (m) seq = s0 + 63 - __builtin_clzll(m);
+    }
+    if (seq < 0) return {0, 0, 0, 0};
+    const Sequence s = sequence_of<true>(a, l, seq);
+    if (s.tq == 0) return {0, 0, 0, 0};
+    t = (int)token - s.q0;
+  } else if (l.num_seqs > 1) {
+    seq = (int)token / l.tq;
+    t = (int)token - seq * l.tq;
+  }
+  const int row = t * a.per + head % a.per, of = 16 * nt;
+  const int tiles = (l.max_q * a.per + of - 1) / of;
+  const int64_t at = ((int64_t)seq * tiles + row / of) * a.f.hkv + head / a.per;
+  const int segment = l.segments[2 * at], count = l.segments[2 * at + 1];
+  const int64_t r = l.part0 + row % of;
+  if (a.joined) return {r + (int64_t)segment * l.cap, r + (int64_t)segment * l.cap, l.cap, count};
+  return {r + (int64_t)segment * l.cap, r + (int64_t)(segment & ~1) * l.cap, 2 * (int64_t)l.cap, count};
 }
 
 // Joins the parts of each row: a wave a row.  The parts that hold keys are listed first (their
 // weights a lane each), then read 64 / (D / 4) at a time, 16 bytes a lane, four such reads in flight.
 template <int D>
-__global__ __launch_bounds__(256) void k_kv_join(AttnArgs a) {
+__global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int nt_own, int nt_prefix) {
   constexpr int LP = D / 4, PP = 64 / LP;
-  const int64_t total_rows = a.total_q * a.hq;
   const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (row >= total_rows) return;
+  if (row >= a.total_q * a.hq) return;
   const int lane = threadIdx.x & 63, sub = lane / LP, d = lane % LP * 4;
+  const int64_t token = row / a.hq;
+  const int head = (int)(row - token * a.hq);
+  const Parts own = parts_of(a, a.list[0], nt_own, token, head, lane);
+  Parts pre{0, 0, 0, 0};
+  if (a.joined) pre = parts_of(a, a.list[1], nt_prefix, token, head, lane);
+  const int parts = own.count + pre.count;
+  if (parts == 0) return;  // finished by the stream (or a token of no sequence)
+  auto place = [&](int p) -> int64_t {
+    const bool o = p < own.count;
+    const int k = o ? p : p - own.count;
+    const Parts& x = o ? own : pre;
+    return k == 0 ? x.first : x.next + k * x.step;
+  };
   float2 ml = float2{kNoKey, 0.f};
-  if (lane < a.parts) ml = a.part_ml[lane * total_rows + row];
+  if (lane < parts) ml = a.part_ml[place(lane)];
   float top = ml.y != 0.f ? ml.x : kNoKey;
-  for (int p = lane + 64; p < a.parts; p += 64) {
-    const float2 x = a.part_ml[p * total_rows + row];
+  for (int p = lane + 64; p < parts; p += 64) {
+    const float2 x = a.part_ml[place(p)];
     if (x.y != 0.f) top = fmaxf(top, x.x);
   }
 #pragma unroll
   for (int i = 1; i < 64; i <<= 1) top = fmaxf(top, __shfl_xor(top, i));
   float sum = 0.f;
   f32x4 o = {0.f, 0.f, 0.f, 0.f};
-  for (int p0 = 0; p0 < a.parts; p0 += 64) {
+  for (int p0 = 0; p0 < parts; p0 += 64) {
     if (p0) {
       ml = float2{kNoKey, 0.f};
-      if (p0 + lane < a.parts) ml = a.part_ml[(p0 + lane) * total_rows + row];
+      if (p0 + lane < parts) ml = a.part_ml[place(p0 + lane)];
     }
     const bool on = ml.y != 0.f;
     const float w = on ? exp2_(ml.x - top) : 0.f;
@@ -537,7 +679,7 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a) {
         const int part = __shfl(listed, i < count ? i : 0);
         wx[u] = __shfl(w, part);
         if (i >= count) wx[u] = 0.f;
-        x[u] = *reinterpret_cast<const f32x4*>(a.part_o + ((p0 + part) * total_rows + row) * D + d);
+        x[u] = *reinterpret_cast<const f32x4*>(a.part_o + place(p0 + part) * D + d);
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) o += x[u] * wx[u];
@@ -562,25 +704,25 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a) {
 }
 
 template <int D, int BITS, int GS, int NT>
-void stream_nt(const AttnArgs& a, dim3 grid, hipStream_t st) {
+void stream_nt(const AttnArgs& a, hipStream_t st) {
   if (a.f.page_shift >= 5)
-    k_kv_stream<D, BITS, GS, NT, true><<<grid, 256, 0, st>>>(a);
+    k_kv_stream<D, BITS, GS, NT, true><<<a.blocks, 256, 0, st>>>(a);
   else
-    k_kv_stream<D, BITS, GS, NT, false><<<grid, 256, 0, st>>>(a);
+    k_kv_stream<D, BITS, GS, NT, false><<<a.blocks, 256, 0, st>>>(a);
 }
 
 template <int D, int BITS, int GS>
 hipError_t stream_t(const AttnArgs& a, int nt, hipStream_t st) {
-  const int tiles = (int)(((int64_t)a.max_q * a.per + 16 * nt - 1) / (16 * nt));
-  const dim3 grid(a.f.hkv * a.num_seqs, tiles, a.nsplit);
   if (nt == 2)
-    stream_nt<D, BITS, GS, 2>(a, grid, st);
+    stream_nt<D, BITS, GS, 2>(a, st);
   else
-    stream_nt<D, BITS, GS, 1>(a, grid, st);
+    stream_nt<D, BITS, GS, 1>(a, st);
   return hipGetLastError();
 }
 
 }  // namespace
+
+int stream_blocks(int D, int gs, int nt) { return 256 * stream_waves(D, gs, nt); }
 
 hipError_t launch_kv_stream(const AttnArgs& a, int D, int bits, int gs, int nt, hipStream_t st) {
 #define X(d, b, g) \
@@ -591,12 +733,12 @@ hipError_t launch_kv_stream(const AttnArgs& a, int D, int bits, int gs, int nt, 
   return hipErrorInvalidValue;
 }
 
-hipError_t launch_kv_join(const AttnArgs& a, int D, hipStream_t st) {
+hipError_t launch_kv_join(const AttnArgs& a, int D, int nt_own, int nt_prefix, hipStream_t st) {
   const dim3 grid((unsigned)((a.total_q * a.hq + 3) / 4));
   if (D == 128)
-    k_kv_join<128><<<grid, 256, 0, st>>>(a);
+    k_kv_join<128><<<grid, 256, 0, st>>>(a, nt_own, nt_prefix);
   else
-    k_kv_join<64><<<grid, 256, 0, st>>>(a);
+    k_kv_join<64><<<grid, 256, 0, st>>>(a, nt_own, nt_prefix);
   return hipGetLastError();
 }
 

@@ -57,7 +57,8 @@ struct Raw {
 };
 
 template <int D, int BITS, int GS>
-__global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a) {
+__global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
+  const KeyList list = which ? a.list[1] : a.list[0];
   constexpr int NG = D / GS, U = D * BITS / 128;
   constexpr int kRow = D * BITS / 8;
   constexpr int KS = D / 16, DT = D / 32;  // MFMA steps of a score, channel tiles of the output
@@ -66,31 +67,28 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a) {
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, h = lane >> 5;
-  const BlockPlace place = block_place(a.f.hkv);
-  // (the tiles with the most keys under a causal rule start first)
-  const int split = place.split, hk = place.hk, tile = (int)gridDim.y - 1 - place.tile, seq = place.seq;
+  // Grid: KV head and sequence (x), row tile (y), key split (z).  Blocks go round the eight XCDs in order
+  // of x, so the pairs are turned by tile and split: the parts of one long sequence spread over
+  // all XCDs.  The tiles with the most keys under a causal rule start first.
+  const uint32_t pair = (blockIdx.x + blockIdx.y + blockIdx.z) % gridDim.x;
+  const int hk = pair % a.f.hkv, seq = pair / a.f.hkv, split = blockIdx.z, tile = gridDim.y - 1 - blockIdx.y;
 
-  int q0 = seq * a.tq, tq = a.tq;
-  if (a.cu_q) {
-    q0 = a.cu_q[seq];
-    tq = a.cu_q[seq + 1] - q0;
-    if (q0 < 0 || tq < 0 || tq > a.max_q || (int64_t)q0 + tq > a.total_q) tq = 0;
-  }
+  const Sequence sequence = sequence_of<true>(a, list, seq);
+  const int q0 = sequence.q0, tq = sequence.tq, len = sequence.len;
   const int rows = tq * a.per;
   const int row0 = tile * kRows;
   if (row0 >= rows) return;
   const int page = 1 << a.f.page_shift;
-  int len = a.lens ? a.lens[seq] : a.fixed_len;
-  len = min(min(max(len, 0), a.max_len), a.table_cols << a.f.page_shift);
   const int64_t total_rows = a.total_q * a.hq;
   const int last_t = (min(row0 + kRows, rows) - 1) / a.per;
-  const int end_all = a.causal ? min(len, max(0, len - tq + last_t + 1)) : len;
-  const int kb = split * a.chunk;
-  const int ke = min(kb + a.chunk, end_all);
-  if (kb >= end_all && a.parts > 1) {  // no key of this split
+  const int end_all = list.causal ? min(len, max(0, len - tq + last_t + 1)) : len;
+  const int kb = split * list.chunk;
+  const int ke = min(kb + list.chunk, end_all);
+  const bool partial = list.nsplit > 1 || a.joined;
+  if (kb >= end_all && partial) {  // no key of this split
     const int row = row0 + tid;
     if (tid < kRows && row < rows)
-      a.part_ml[(int64_t)(a.part0 + split) * total_rows + (int64_t)(q0 + row / a.per) * a.hq + hk * a.per + row % a.per] =
+      a.part_ml[list.part0 + split * total_rows + (int64_t)(q0 + row / a.per) * a.hq + hk * a.per + row % a.per] =
           float2{kNoKey, 0.f};
     return;
   }
@@ -98,8 +96,8 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a) {
   const int w_row0 = row0 + 32 * wave;
   const bool w_on = w_row0 < rows;
   const int w_first = w_on ? w_row0 / a.per : 0, w_last = w_on ? (min(w_row0 + 32, rows) - 1) / a.per : 0;
-  const int w_end = !w_on ? 0 : a.causal ? min(ke, len - tq + w_last + 1) : ke;   // keys that some row sees
-  const int w_min = a.causal ? len - tq + w_first + 1 : len;                       // keys that all rows see
+  const int w_end = !w_on ? 0 : list.causal ? min(ke, len - tq + w_last + 1) : ke;   // keys that some row sees
+  const int w_min = list.causal ? len - tq + w_first + 1 : len;                       // keys that all rows see
 
   // ---- queries
   h8 qf[KS];
@@ -111,19 +109,18 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a) {
   {
     const int64_t at = (int64_t)(q0 + rt) * a.q_ts + (int64_t)(hk * a.per + rg) * a.q_hs;
     float top = 0.f;
-    float x[KS][8];
+    u32x4 w[KS];
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
-      const uint16_t* p = reinterpret_cast<const uint16_t*>(a.q) + at + 16 * i + 8 * h;
-      if (a.dtype == HQQ_KV_BF16)
-        load8<true>(p, x[i]);
-      else
-        load8<false>(p, x[i]);
+      w[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.q) + at + 16 * i + 8 * h);
+      if (!there) w[i] = u32x4{0, 0, 0, 0};
+    }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        x[i][j] = there ? x[i][j] : 0.f;
-        top = fmaxf(top, fabsf(x[i][j]));
-      }
+    for (int i = 0; i < KS; ++i) {
+      float x[8];
+      floats8(w[i], a.dtype, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
     }
     top = fmaxf(top, __shfl_xor(top, 32));
     // the row's largest value to [2^14, 2^15): bfloat16 rows of any size keep their bits in fp16
@@ -132,14 +129,17 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a) {
     e = min(e, 100);
     cs = ldexpf(a.scale_log2, -e);
 #pragma unroll
-    for (int i = 0; i < KS; ++i)
+    for (int i = 0; i < KS; ++i) {
+      float x[8];
+      floats8(w[i], a.dtype, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) qf[i][j] = (_Float16)ldexpf(x[i][j], e);
-    lim = there ? (a.causal ? min(len - 1, len - tq + rt) : len - 1) : -1;
+      for (int j = 0; j < 8; ++j) qf[i][j] = (_Float16)ldexpf(x[j], e);
+    }
+    lim = there ? (list.causal ? min(len - 1, len - tq + rt) : len - 1) : -1;
   }
 
   // ---- unpacking: a quarter of one key and one unit of four tokens a thread
-  const int32_t* table = a.table + (int64_t)seq * a.table_stride;
+  const int32_t* table = list.table + (int64_t)seq * list.table_stride;
   const int ik = tid >> 2, iv = (tid >> 4) * 4;
   const uint32_t k_off = (tid & 3) * (kRow / 4);
   const int unit = tid & 15;
@@ -312,8 +312,8 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a) {
   l += __shfl_xor(l, 32);
   if (!there) return;
   const int64_t at = (int64_t)(q0 + rt) * a.hq + hk * a.per + rg;
-  if (a.parts > 1) {
-    const int64_t part = (int64_t)(a.part0 + split) * total_rows + at;
+  if (partial) {
+    const int64_t part = list.part0 + split * total_rows + at;
     if (h == 0) a.part_ml[part] = float2{mref, l};
     if (l != 0.f)
 #pragma unroll
@@ -341,17 +341,18 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a) {
 }
 
 template <int D, int BITS, int GS>
-hipError_t tile_t(const AttnArgs& a, hipStream_t st) {
-  const int tiles = (int)(((int64_t)a.max_q * a.per + kRows - 1) / kRows);
-  k_kv_tile<D, BITS, GS><<<dim3(a.f.hkv * a.num_seqs, tiles, a.nsplit), 512, 0, st>>>(a);
+hipError_t tile_t(const AttnArgs& a, int which, hipStream_t st) {
+  const KeyList& l = a.list[which];
+  const int tiles = (int)(((int64_t)l.max_q * a.per + kRows - 1) / kRows);
+  k_kv_tile<D, BITS, GS><<<dim3(a.f.hkv * l.num_seqs, tiles, l.nsplit), 512, 0, st>>>(a, which);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_kv_tile(const AttnArgs& a, int D, int bits, int gs, hipStream_t st) {
+hipError_t launch_kv_tile(const AttnArgs& a, int which, int D, int bits, int gs, hipStream_t st) {
 #define X(d, b, g) \
-  if (D == d && bits == b && gs == g) return tile_t<d, b, g>(a, st);
+  if (D == d && bits == b && gs == g) return tile_t<d, b, g>(a, which, st);
   X(64, 4, 32) X(64, 4, 64) X(64, 8, 32) X(64, 8, 64) X(128, 4, 32) X(128, 4, 64) X(128, 4, 128) X(128, 8, 32)
   X(128, 8, 64) X(128, 8, 128)
 #undef X
