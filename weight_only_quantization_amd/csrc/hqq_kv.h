@@ -58,9 +58,9 @@ struct KeyList {
   int num_seqs, tq, max_q;
   int causal;
   // where the partial results of its rows begin (in rows of part_o), and their layout: the stream's
-  // segments of `cap` rows (see Schedule), or split s of row r at s * total_rows + r (tiles)
+  // segments of `cap` rows, or by row
   int64_t part0;
-  int tiled;
+  int tiled;      // split s of row r at s * total_rows + r: of the tiles, or of a stream with a block a pair
   int nsplit, chunk;  // tiles: key splits and the keys of one
   int32_t* segments;  // stream: per pair, its first segment and their number
   int cap;            // stream: rows of a segment, min(16 NT, the widest sequence's rows)
@@ -77,7 +77,7 @@ struct AttnArgs {
   KeyList list[2];   // the sequences' own keys, the shared prefix
   int joined;        // partial results of both lists meet in the join: no row is finished before it
   int first_list, lists;  // stream: the lists of this launch
-  int blocks;             // stream: the grid
+  int blocks;             // stream: blocks that share the work of the launch; 0: a block a pair
   void* out;
   float* lse;
   float* part_o;    // [rows][D], not divided by the sum

@@ -84,6 +84,9 @@ void split_keys(KeyList* l, int64_t blocks) {
   if (l->nsplit < 1) l->nsplit = 1;
 }
 
+// Longest own keys that one block streams for a pair; longer ones are shared out over the blocks.
+constexpr int64_t kWholeKeys = 4096;
+
 // Blocks of a stream launch: what fills the GPU, but at least two units each.
 int stream_grid(const Plan& p, const hqq_kv_cache& c, int first, int lists) {
   int64_t units = 0;
@@ -176,19 +179,22 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
     } else {
       const int64_t most = 16 * nt_of(p->kind[i]);
       l.cap = (int)(rows < most ? rows : most);
-      if (l.max_len > hqq::kv::kUnitKeys) p->join = true;
+      // (own keys and a prefix that streams alike take one launch of shares)
+      const bool alone = !a.joined || row_kernel(x->total_q * a.per) != p->kind[0];
+      if (i == 0 && alone && l.max_len <= kWholeKeys) {
+        l.tiled = l.nsplit = 1;
+      } else {
+        p->join = true;
+      }
     }
   }
-  if (!p->join) {
-    if (p->kind[0] != kTile) a.blocks = stream_grid(*p, c, 0, 1);
-    return HQQ_OK;
-  }
+  if (!p->join) return HQQ_OK;
   // the lists' partial results, one after the other; the streams' segment lists behind them
   for (int i = 0; i < (a.joined ? 2 : 1); ++i) {
     KeyList& l = a.list[i];
     l.part0 = p->part_rows;
     const int64_t rows = (int64_t)l.max_q * a.per;
-    if (p->kind[i] == kTile) {
+    if (l.tiled) {
       if (l.nsplit > 1 || a.joined) p->part_rows += l.nsplit * x->total_q * a.hq;
       continue;
     }
@@ -226,7 +232,7 @@ int run_attention(const hqq_kv_attention_args* x) {
     a.part_ml = reinterpret_cast<float2*>(a.part_o + p.part_rows * c.head_dim);
     int32_t* words = reinterpret_cast<int32_t*>(a.part_ml + p.part_rows);
     for (int i = 0; i < (a.joined ? 2 : 1); ++i) {
-      if (p.kind[i] == kTile) continue;
+      if (a.list[i].tiled) continue;
       KeyList& l = a.list[i];
       l.segments = words;
       words += 2 * row_tiles((int64_t)l.max_q * a.per, p.kind[i]) * a.f.hkv * l.num_seqs;
@@ -241,8 +247,8 @@ int run_attention(const hqq_kv_attention_args* x) {
   for (int i = 0; i < lists && e == hipSuccess; ++i) {
     if (p.kind[i] == kTile) continue;
     a.first_list = i;
-    a.lists = i == 0 && lists == 2 && p.kind[1] == p.kind[0] ? 2 : 1;
-    a.blocks = stream_grid(p, c, i, a.lists);
+    a.lists = i == 0 && lists == 2 && !a.list[0].tiled && p.kind[1] == p.kind[0] ? 2 : 1;
+    a.blocks = a.list[i].tiled ? 0 : stream_grid(p, c, i, a.lists);
     e = hqq::kv::launch_kv_stream(a, D, bits, gs, nt_of(p.kind[i]), stream);
     i += a.lists - 1;
   }

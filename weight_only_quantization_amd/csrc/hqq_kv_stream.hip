@@ -15,7 +15,7 @@
 //           they are (keys keep their order inside the step).  c s is one fp16 rounding,
 //           fma(1024 + c, s, -1024 s); the floors enter as one more product, sum_j p_j m_j.
 //           p is rounded to fp16 (2^-12 relative, independent per key).
-// The next step's keys are loaded as soon as this step's scores are done, the next values after this
+// Next keys are loaded as soon as this step's scores are done, the next values after this
 // step's product, each into the registers just read: few registers, so three waves a SIMD cover the
 // memory's latency (two with both steps' registers held: 3.2 TB/s at 16 sequences of 16384-32768 keys,
 // 64 heads on 8).  The four waves of a block take
@@ -56,6 +56,17 @@ struct StepV {
   u32x4 m[2];
 };
 
+// A step's registers and the page ids of the step they hold and of the next one they will hold.
+struct Ids {
+  int id[2];
+};
+template <int D, int BITS, int NG>
+struct Stage {
+  StepK<D, BITS, NG> k;
+  StepV<D, BITS> v;
+  Ids now, then;
+};
+
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
   if (N % 4 == 0) {
@@ -85,6 +96,11 @@ constexpr int stream_waves(int D, int GS, int NT) {
   return D == 64 || D / GS <= 2 ? 2 : 1;
 }
 
+// Steps whose registers a wave of a whole pair holds (256 registers a lane there).
+constexpr int whole_sets(int D, int BITS, int GS, int NT) {
+  return D == 64 || (BITS == 4 ? NT == 1 || D / GS <= 2 : NT == 1 && D / GS <= 2) ? 2 : 1;
+}
+
 // The work of a launch: units of 128 keys of every (sequence, row tile, KV head), in one order, cut into
 // equal shares, one a block.  A block walks the pieces ("segments") of its share; a pair that several
 // blocks share leaves a partial result per segment, a pair within one share is finished there.
@@ -106,19 +122,28 @@ __device__ __forceinline__ uint32_t tiles_of(const AttnArgs& a, int tq) {
 __device__ __forceinline__ uint32_t units_of(int len) { return max(1u, (uint32_t)(len + kUnitKeys - 1) / kUnitKeys); }
 
 // PAIR: pages of at least 32 tokens, so a step's two tiles share a page (one lookup, one address).
-template <int D, int BITS, int GS, int NT, bool PAIR>
-__global__ __launch_bounds__(256, stream_waves(D, GS, NT)) void k_kv_stream(AttnArgs a) {
+// SPLIT: the shares above, four waves a block.  Else a block takes a whole pair with eight waves: what short
+// sequences want, with no schedule to work out and nothing to join.
+template <int D, int BITS, int GS, int NT, bool PAIR, bool SPLIT>
+__global__ __launch_bounds__(SPLIT ? 256 : 512, SPLIT ? stream_waves(D, GS, NT) : 2) void k_kv_stream(AttnArgs a) {
   using G = Geo<D, BITS>;
   constexpr int NG = D / GS;
   constexpr int kLdsRow = D + 4;
-  __shared__ __attribute__((aligned(16))) float sh_o[4][16][kLdsRow];
-  __shared__ float sh_m[4][16 * NT], sh_l[4][16 * NT];
+  constexpr int W = SPLIT ? 4 : 8;  // waves
+  constexpr int SETS = SPLIT ? 1 : whole_sets(D, BITS, GS, NT), kStride = 32 * W;  // steps whose registers are held; keys of a block's step
+  __shared__ __attribute__((aligned(16))) float sh_o[W][16][kLdsRow];
+  __shared__ float sh_m[W][16 * NT], sh_l[W][16 * NT];
 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int n = lane & 15, h = lane >> 4;
   const int page = 1 << a.f.page_shift;
 
   // ---- the block's share, and where it begins
+  KeyList list = a.first_list ? a.list[1] : a.list[0];
+  Share share{0, 0};
+  uint32_t u = 0, u_end = 0, u_begin = 0, pair = 0, x0 = 0, pairs = 0;  // pairs: in front of this one
+  int seq = 0;
+  if (SPLIT) {
   auto weight = [&](const KeyList& l, int seq) -> uint32_t {
     const Sequence s = sequence_of<false>(a, l, seq);
     return units_of(s.len) * tiles_of<NT>(a, s.tq) * a.f.hkv;
@@ -137,11 +162,11 @@ __global__ __launch_bounds__(256, stream_waves(D, GS, NT)) void k_kv_stream(Attn
   const uint32_t blocks = min((uint32_t)a.blocks, total);
   if (blockIdx.x >= blocks) return;
   const uint32_t per_block = __builtin_amdgcn_readfirstlane(total / blocks);
-  const Share share{per_block, total - per_block * blocks};
-  uint32_t u = share.begin(blockIdx.x);
-  const uint32_t u_end = share.begin(blockIdx.x + 1);
-  int li = a.first_list, seq = 0;
-  uint32_t before = 0, pairs = 0;  // units and pairs in front of the sequence
+  share = Share{per_block, total - per_block * blocks};
+  u = u_begin = share.begin(blockIdx.x);
+  u_end = share.begin(blockIdx.x + 1);
+  int li = a.first_list;
+  uint32_t before = 0;  // units in front of the sequence
   for (bool found = false; !found;) {
     const KeyList l = li ? a.list[1] : a.list[0];
     for (int s0 = 0; s0 < l.num_seqs && !found; s0 += 64) {
@@ -174,14 +199,22 @@ __global__ __launch_bounds__(256, stream_waves(D, GS, NT)) void k_kv_stream(Attn
   seq = __builtin_amdgcn_readfirstlane(seq);
   before = __builtin_amdgcn_readfirstlane(before);
   pairs = __builtin_amdgcn_readfirstlane(pairs);
-  const uint32_t u_begin = u;
-  KeyList list = li ? a.list[1] : a.list[0];
-  Sequence sq_ = sequence_of<true>(a, list, seq);
-  uint32_t units = units_of(sq_.len);
+  list = li ? a.list[1] : a.list[0];
   // within the sequence: tile * hkv + KV head, and the first unit of the segment
-  uint32_t pair = __builtin_amdgcn_readfirstlane((u - before) / units);
-  uint32_t x0 = (u - before) - pair * units;
+  const uint32_t each = units_of(sequence_of<true>(a, list, seq).len);
+  pair = __builtin_amdgcn_readfirstlane((u - before) / each);
+  x0 = (u - before) - pair * each;
   pairs += pair;
+  } else {
+    // (pairs of one sequence go round the XCDs, whatever its tile)
+    const uint32_t x = (blockIdx.x + blockIdx.y) % gridDim.x;
+    seq = x / a.f.hkv;
+    pair = blockIdx.y * a.f.hkv + x % a.f.hkv;
+    u_end = 0x7fffffff;
+  }
+  Sequence sq_ = sequence_of<true>(a, list, seq);
+  if (!SPLIT && pair >= tiles_of<NT>(a, sq_.tq) * a.f.hkv) return;
+  uint32_t units = units_of(sq_.len);
 
   while (true) {
   const int q0 = sq_.q0, tq = sq_.tq, len = sq_.len;
@@ -204,9 +237,6 @@ __global__ __launch_bounds__(256, stream_waves(D, GS, NT)) void k_kv_stream(Attn
   const int32_t* table = list.table + (int64_t)seq * list.table_stride;
 
   // page ids of a step's two tiles (-1: past the end, or no such page), loaded a step before the codes
-  struct Ids {
-    int id[2];
-  };
   auto page_ids = [&](int key0) {
     Ids x;
 #pragma unroll
@@ -252,14 +282,17 @@ __global__ __launch_bounds__(256, stream_waves(D, GS, NT)) void k_kv_stream(Attn
     }
   };
   const int first = kb + 32 * wave;
-  StepK<D, BITS, NG> sk;
-  StepV<D, BITS> sv;
-  Ids ids{{-1, -1}}, ids1{{-1, -1}};  // of this step and of the next
-  if (first < ke) {
-    ids = page_ids(first);
-    ids1 = page_ids(first + 128);
-    fetch_k(first, ids, sk);
-    fetch_v(first, ids, sv);
+  Stage<D, BITS, NG> stage[SETS];
+#pragma unroll
+  for (int i = 0; i < SETS; ++i) {
+    const int key0 = first + i * kStride;
+    stage[i].now = stage[i].then = Ids{{-1, -1}};
+    if (key0 < ke) {
+      stage[i].now = page_ids(key0);
+      stage[i].then = page_ids(key0 + SETS * kStride);
+      fetch_k(key0, stage[i].now, stage[i].k);
+      fetch_v(key0, stage[i].now, stage[i].v);
+    }
   }
 
   // ---- queries: rows in fp16 with a power of two of their own, sums per group
@@ -333,8 +366,10 @@ __global__ __launch_bounds__(256, stream_waves(D, GS, NT)) void k_kv_stream(Attn
     for (int j = 0; j < G::kVm; ++j) o[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  for (int key0 = first; key0 < ke; key0 += 128) {
-    const uint32_t bad = (ids.id[0] < 0 ? 1u : 0u) | (ids.id[1] < 0 ? 2u : 0u);
+  auto step = [&](int key0, Stage<D, BITS, NG>& g) {
+    StepK<D, BITS, NG>& sk = g.k;
+    StepV<D, BITS>& sv = g.v;
+    const uint32_t bad = (g.now.id[0] < 0 ? 1u : 0u) | (g.now.id[1] < 0 ? 2u : 0u);
     // scores
     float p[NT][8];
 #pragma unroll
@@ -380,8 +415,8 @@ __global__ __launch_bounds__(256, stream_waves(D, GS, NT)) void k_kv_stream(Attn
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int c = 0; c < 8; ++c) asm volatile("" : "+v"(p[t][c]));
-    const bool more = key0 + 128 < ke;
-    if (more) fetch_k(key0 + 128, ids1, sk);
+    const bool more = key0 + SETS * kStride < ke;
+    if (more) fetch_k(key0 + SETS * kStride, g.then, sk);
     if (bad | (uint32_t)(key0 + 32 > end_min) | (uint32_t)(key0 + 32 > len)) {
       // keys that a row does not see (by selection: whatever their memory holds), and floors and
       // steps of keys that are not there
@@ -489,17 +524,22 @@ __global__ __launch_bounds__(256, stream_waves(D, GS, NT)) void k_kv_stream(Attn
         }
       }
     }
-    if (more) fetch_v(key0 + 128, ids1, sv);
-    ids = ids1;
-    ids1 = page_ids(key0 + 256);
+    if (more) fetch_v(key0 + SETS * kStride, g.then, sv);
+    g.now = g.then;
+    g.then = page_ids(key0 + 2 * SETS * kStride);
+  };
+  for (int key0 = first; key0 < ke; key0 += SETS * kStride) {
+#pragma unroll
+    for (int i = 0; i < SETS; ++i)
+      if (i == 0 || key0 + i * kStride < ke) step(key0 + i * kStride, stage[i]);
   }
 
-  // ---- the block's four waves joined, then written
+  // ---- the block's waves joined, then written
   const bool whole = x0 == 0 && x1 == units;
   // a pair's segment: of the block's share the first one or the last one; with a join of both lists every
   // pair leaves one (blocks and pairs in front: each further segment adds one to the sum)
   const uint32_t segment = a.joined ? blockIdx.x + pairs : 2 * blockIdx.x + (u == u_begin ? 0 : 1);
-  if (x0 == 0 && threadIdx.x == 0 && list.segments) {
+  if (SPLIT && x0 == 0 && threadIdx.x == 0 && list.segments) {
     const int64_t at = ((int64_t)seq * tiles_of<NT>(a, list.max_q) + tile) * a.f.hkv + hk;
     list.segments[2 * at] = segment;
     list.segments[2 * at + 1] = whole && !a.joined ? 0 : (int)(share.block_of(u + units - 1) - blockIdx.x + 1);
@@ -515,7 +555,7 @@ __global__ __launch_bounds__(256, stream_waves(D, GS, NT)) void k_kv_stream(Attn
   for (int t = 0; t < NT; ++t) {
     float mm = sh_m[0][16 * t + n];
 #pragma unroll
-    for (int w = 1; w < 4; ++w) mm = fmaxf(mm, sh_m[w][16 * t + n]);
+    for (int w = 1; w < W; ++w) mm = fmaxf(mm, sh_m[w][16 * t + n]);
     const float f = exp2_(mref[t] - mm);
     if (t) __syncthreads();  // the tile before has been read
 #pragma unroll
@@ -528,44 +568,43 @@ __global__ __launch_bounds__(256, stream_waves(D, GS, NT)) void k_kv_stream(Attn
         *reinterpret_cast<f32x4*>(&sh_o[wave][n][(4 * h + i) * (D / 16) + j]) = x;
       }
     __syncthreads();
-    // 256 threads, 16 rows: D / 16 channels each
-    const int r = threadIdx.x / 16, d0 = threadIdx.x % 16 * (D / 16);
+    // 16 rows, CH channels a thread
+    constexpr int CH = D / (4 * W), VEC = CH < 4 ? 2 : 4;
+    typedef float vec __attribute__((ext_vector_type(VEC)));
+    const int r = threadIdx.x / (4 * W), d0 = threadIdx.x % (4 * W) * CH;
     const int row = row0 + 16 * t + r;
     if (row < rows) {
       float rm = sh_m[0][16 * t + r];
 #pragma unroll
-      for (int w = 1; w < 4; ++w) rm = fmaxf(rm, sh_m[w][16 * t + r]);
+      for (int w = 1; w < W; ++w) rm = fmaxf(rm, sh_m[w][16 * t + r]);
       float sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) sum += sh_l[w][16 * t + r] * exp2_(sh_m[w][16 * t + r] - rm);
+      for (int w = 0; w < W; ++w) sum += sh_l[w][16 * t + r] * exp2_(sh_m[w][16 * t + r] - rm);
       const int64_t at = (int64_t)(q0 + row / a.per) * a.hq + hk * a.per + row % a.per;
-      float x[D / 16];
+      vec x[CH / VEC];
 #pragma unroll
-      for (int j = 0; j < D / 16; j += 4) {
-        f32x4 y = *reinterpret_cast<const f32x4*>(&sh_o[0][r][d0 + j]);
+      for (int j = 0; j < CH / VEC; ++j) {
+        x[j] = *reinterpret_cast<const vec*>(&sh_o[0][r][d0 + j * VEC]);
 #pragma unroll
-        for (int w = 1; w < 4; ++w) y += *reinterpret_cast<const f32x4*>(&sh_o[w][r][d0 + j]);
-#pragma unroll
-        for (int jj = 0; jj < 4; ++jj) x[j + jj] = y[jj];
+        for (int w = 1; w < W; ++w) x[j] += *reinterpret_cast<const vec*>(&sh_o[w][r][d0 + j * VEC]);
       }
       if (!whole || a.joined) {
-        const int64_t part = list.part0 + (int64_t)segment * list.cap + 16 * t + r;
+        const int64_t part = list.part0 + (SPLIT ? (int64_t)segment * list.cap + 16 * t + r : at);
         if (d0 == 0) a.part_ml[part] = float2{rm, sum};
         float* to = a.part_o + part * D + d0;
         if (sum != 0.f)  // (an empty part's sums are never read)
 #pragma unroll
-          for (int j = 0; j < D / 16; j += 4) *reinterpret_cast<f32x4*>(to + j) = f32x4{x[j], x[j + 1], x[j + 2], x[j + 3]};
+          for (int j = 0; j < CH / VEC; ++j) *reinterpret_cast<vec*>(to + j * VEC) = x[j];
       } else {
         const float inv = sum != 0.f ? 1.0f / sum : 0.f;
         uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + at * D + d0;
 #pragma unroll
-        for (int j = 0; j < D / 16; j += 4) {
-          u32x2 w;
-          if (a.dtype == HQQ_KV_BF16)
-            w = u32x2{pack2<true>(x[j] * inv, x[j + 1] * inv), pack2<true>(x[j + 2] * inv, x[j + 3] * inv)};
-          else
-            w = u32x2{pack2<false>(x[j] * inv, x[j + 1] * inv), pack2<false>(x[j + 2] * inv, x[j + 3] * inv)};
-          *reinterpret_cast<u32x2*>(to + j) = w;
+        for (int j = 0; j < CH / VEC; ++j) {
+#pragma unroll
+          for (int i = 0; i < VEC; i += 2) {
+            const float y0 = x[j][i] * inv, y1 = x[j][i + 1] * inv;
+            *reinterpret_cast<uint32_t*>(to + j * VEC + i) = a.dtype == HQQ_KV_BF16 ? pack2<true>(y0, y1) : pack2<false>(y0, y1);
+          }
         }
         if (a.lse && d0 == 0) a.lse[at] = sum != 0.f ? (rm + __log2f(sum)) * 0.69314718056f : -INFINITY;
       }
@@ -573,6 +612,7 @@ __global__ __launch_bounds__(256, stream_waves(D, GS, NT)) void k_kv_stream(Attn
   }
 
   // ---- the next pair
+  if (!SPLIT) break;
   u += x1 - x0;
   if (u >= u_end) break;
   ++pair, ++pairs;
@@ -703,20 +743,24 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int nt_own, int nt_
   }
 }
 
-template <int D, int BITS, int GS, int NT>
+template <int D, int BITS, int GS, int NT, bool PAIR>
 void stream_nt(const AttnArgs& a, hipStream_t st) {
-  if (a.f.page_shift >= 5)
-    k_kv_stream<D, BITS, GS, NT, true><<<a.blocks, 256, 0, st>>>(a);
-  else
-    k_kv_stream<D, BITS, GS, NT, false><<<a.blocks, 256, 0, st>>>(a);
+  if (a.blocks) {
+    k_kv_stream<D, BITS, GS, NT, PAIR, true><<<a.blocks, 256, 0, st>>>(a);
+  } else {
+    const KeyList& l = a.list[a.first_list];
+    const int tiles = (int)(((int64_t)l.max_q * a.per + 16 * NT - 1) / (16 * NT));
+    k_kv_stream<D, BITS, GS, NT, PAIR, false><<<dim3(a.f.hkv * l.num_seqs, tiles), 512, 0, st>>>(a);
+  }
 }
 
 template <int D, int BITS, int GS>
 hipError_t stream_t(const AttnArgs& a, int nt, hipStream_t st) {
+  const bool pair = a.f.page_shift >= 5;
   if (nt == 2)
-    stream_nt<D, BITS, GS, 2>(a, st);
+    pair ? stream_nt<D, BITS, GS, 2, true>(a, st) : stream_nt<D, BITS, GS, 2, false>(a, st);
   else
-    stream_nt<D, BITS, GS, 1>(a, st);
+    pair ? stream_nt<D, BITS, GS, 1, true>(a, st) : stream_nt<D, BITS, GS, 1, false>(a, st);
   return hipGetLastError();
 }
 

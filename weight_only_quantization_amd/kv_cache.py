@@ -6,6 +6,7 @@ torch tensors, every step runs in the library's kernels on the given or the curr
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass
 
 import weight_only_quantization_amd as _pkg
@@ -43,16 +44,35 @@ class KvAttentionArgs(ctypes.Structure):
                 ("lse", _p), ("workspace", _p), ("workspace_bytes", ctypes.c_size_t), ("stream", _p)]
 
 
+# The same structures as packed bytes (native alignment; a nested hqq_kv_cache ends in 4 bytes of
+# padding): a call is a few microseconds, and filling a ctypes.Structure field by field would be a
+# good part of them.
+_CACHE = "Pqiiiiixxxx"
+_WRITE = struct.Struct("@" + _CACHE + "iPPqqqqqPPPP")
+_READ = struct.Struct("@" + _CACHE + "iqPPPP")
+_ATTENTION = struct.Struct("@" + _CACHE + "iPqqqiqPqPqqPqifPqPPPNP")
+assert (_WRITE.size, _READ.size, _ATTENTION.size) == tuple(map(ctypes.sizeof, (KvWriteArgs, KvReadArgs, KvAttentionArgs)))
+
+_fast = {}  # entry points that take packed bytes
+
+
 def declare(lib):
     """Argument types of the entry points (called when the library is loaded)."""
     lib.hqq_kv_page_bytes.argtypes = [_i32] * 5
     lib.hqq_kv_page_bytes.restype = ctypes.c_size_t
     for name, args in (("hqq_kv_write", KvWriteArgs), ("hqq_kv_read", KvReadArgs),
-                       ("hqq_kv_attention", KvAttentionArgs), ("hqq_kv_attention_shared", KvAttentionArgs)):
-        getattr(lib, name).argtypes = [ctypes.POINTER(args)]
-        getattr(lib, name).restype = _i32
-    lib.hqq_kv_attention_workspace_bytes.argtypes = [ctypes.POINTER(KvAttentionArgs)]
-    lib.hqq_kv_attention_workspace_bytes.restype = ctypes.c_size_t
+                       ("hqq_kv_attention", KvAttentionArgs), ("hqq_kv_attention_shared", KvAttentionArgs),
+                       ("hqq_kv_attention_workspace_bytes", KvAttentionArgs)):
+        fn = getattr(lib, name)
+        fn.argtypes = [ctypes.POINTER(args)]
+        fn.restype = ctypes.c_size_t if name.endswith("bytes") else _i32
+        _fast[name] = ctypes.CFUNCTYPE(fn.restype, ctypes.c_char_p)((name, lib))
+
+
+def _entry(name):
+    if not _fast:
+        _pkg.load()
+    return _fast[name]
 
 
 @dataclass
@@ -70,14 +90,17 @@ class KVCache:
     def num_pages(self) -> int:
         return self.pages.shape[0]
 
-    def args(self) -> KvCacheArgs:
+    def args(self):
+        """The fields of hqq_kv_cache, checked."""
         t = self.pages
-        _pkg._need(t, "pages", _torch().uint8)
-        need = _page_bytes(self.num_kv_heads, self.head_dim, self.nbits, self.group_size, self.page_size)
+        fmt = (self.num_kv_heads, self.head_dim, self.nbits, self.group_size, self.page_size)
+        if t.dtype is not _torch().uint8:
+            raise ValueError("pages must be torch.uint8, got %s" % t.dtype)
+        _pkg._placed(t, "pages")
+        need = _sizes.get(fmt) or _page_bytes(*fmt)
         if need and (t.dim() < 2 or t.numel() != t.shape[0] * need):
             raise ValueError("pages must be [num_pages, ...] of %d bytes a page, got %s" % (need, tuple(t.shape)))
-        return KvCacheArgs(t.data_ptr(), t.shape[0], self.num_kv_heads, self.head_dim, self.nbits, self.group_size,
-                           self.page_size)
+        return (t.data_ptr(), t.shape[0]) + fmt
 
 
 _sizes = {}
@@ -89,38 +112,65 @@ def _page_bytes(*fmt) -> int:
     return _sizes[fmt]
 
 
-def _torch():
-    import torch
-    return torch
-
-
+_modules = {}
 _codes = {}
 
 
-def _dtype_code(dtype) -> int:
-    if not _codes:
-        t = _torch()
+def _torch():
+    t = _modules.get("torch")
+    if t is None:
+        import torch as t
+        _modules["torch"] = t
         _codes.update({t.float16: HQQ_KV_F16, t.bfloat16: HQQ_KV_BF16})
-    if dtype not in _codes:
+    return t
+
+
+def _dtype_code(dtype) -> int:
+    code = _codes.get(dtype)
+    if code is None:
         raise ValueError("dtype must be torch.float16 or torch.bfloat16, got %s" % dtype)
-    return _codes[dtype]
+    return code
 
 
 def _strides(t, name, heads, dim):
     """Token and head strides of a [tokens, heads, dim] tensor (channels contiguous)."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError("%s must be [tokens, %d, %d], got %s" % (name, heads, dim, tuple(t.shape)))
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError("%s must be [tokens, %d, %d], got %s" % (name, heads, dim, tuple(shape)))
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA (HIP) tensor" % name)
-    s = t.stride()
-    if s[2] != 1 or s[0] % 8 or s[1] % 8 or t.data_ptr() % 16:
+    token, head, channel = t.stride()
+    if channel != 1 or token % 8 or head % 8 or t.data_ptr() % 16:
         raise ValueError("%s needs contiguous channels, strides that are multiples of 8 elements and 16-byte alignment "
-                         "(got strides %s); pass %s.contiguous()" % (name, s, name))
-    return s[0], s[1]
+                         "(got strides %s); pass %s.contiguous()" % (name, t.stride(), name))
+    return token, head
 
 
-def _stream(stream):
-    return (stream if stream is not None else _torch().cuda.current_stream()).cuda_stream
+def _indices(t, name, dtype, dim):
+    """Checks an index tensor (slots, lengths, offsets)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch tensor" % name)
+    if t.dtype is not dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.dim() != dim:
+        raise ValueError("%s must have %d dimension%s, got %s" % (name, dim, "" if dim == 1 else "s", tuple(t.shape)))
+
+
+def _stream(stream, t):
+    """The given stream's handle, or the current one's of the tensor's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _empty(stream, *shapes_like):
+    """New tensors on the stream the kernels run on (see _on): (shape, dtype, device) each."""
+    torch = _torch()
+    if stream is None:
+        return [torch.empty(s, dtype=d, device=v) for s, d, v in shapes_like]
+    with _pkg._on(stream):
+        return [torch.empty(s, dtype=d, device=v) for s, d, v in shapes_like]
 
 
 def hqq_kv_page_bytes(num_kv_heads: int, head_dim: int, nbits: int = 4, group_size: int = 64,
@@ -133,7 +183,7 @@ def hqq_kv_cache(num_pages: int, num_kv_heads: int, head_dim: int, nbits: int = 
                  page_size: int = 64, device="cuda") -> KVCache:
     """Allocates the pages of one layer's cache (contents undefined: a token is written before it is
     read)."""
-    nbytes = _page_bytes(num_kv_heads, head_dim, nbits, group_size, page_size)
+    nbytes = _pkg.load().hqq_kv_page_bytes(num_kv_heads, head_dim, nbits, group_size, page_size)
     if nbytes == 0:
         raise _pkg.HQQError(_pkg.HQQ_ERR_UNSUPPORTED, _pkg.last_error())
     pages = _torch().empty((num_pages, nbytes), dtype=_torch().uint8, device=device)
@@ -145,24 +195,26 @@ def hqq_kv_write(cache: KVCache, k, v, slots, echo: bool = False, stream=None):
     the cache's `slots` (int64 [n], distinct; slots outside the cache are skipped).  With `echo`
     returns (k, v) as the values the cache now stands for, else None."""
     torch = _torch()
-    _pkg._need(slots, "slots", torch.int64, device=False)
-    if v.dtype != k.dtype:
-        raise ValueError("k and v must have one dtype, got %s and %s" % (k.dtype, v.dtype))
-    code = _dtype_code(k.dtype)
-    n = k.shape[0]
-    if slots.dim() != 1 or slots.shape[0] != n or v.shape[0] != n:
+    _indices(slots, "slots", torch.int64, 1)
+    dtype, n = k.dtype, k.shape[0]
+    if v.dtype is not dtype:
+        raise ValueError("k and v must have one dtype, got %s and %s" % (dtype, v.dtype))
+    code = _dtype_code(dtype)
+    if slots.shape[0] != n or v.shape[0] != n:
         raise ValueError("k, v and slots must have the same number of tokens")
     kt, kh = _strides(k, "k", cache.num_kv_heads, cache.head_dim)
     vt, vh = _strides(v, "v", cache.num_kv_heads, cache.head_dim)
     _pkg._placed(slots, "slots")
-    ke = ve = None
+    out = None
     if echo:
-        with _pkg._on(stream):
-            ke, ve = (torch.empty(k.shape, dtype=k.dtype, device=k.device) for _ in range(2))
-    a = KvWriteArgs(cache.args(), code, k.data_ptr(), v.data_ptr(), n, kt, kh, vt, vh, slots.data_ptr(),
-                    ke.data_ptr() if echo else None, ve.data_ptr() if echo else None, _stream(stream))
-    _pkg._check(_pkg.load().hqq_kv_write(a))
-    return (ke, ve) if echo else None
+        like = (k.shape, dtype, k.device)
+        out = tuple(_empty(stream, like, like))
+    status = _entry("hqq_kv_write")(_WRITE.pack(
+        *cache.args(), code, k.data_ptr(), v.data_ptr(), n, kt, kh, vt, vh, slots.data_ptr(),
+        out[0].data_ptr() if echo else 0, out[1].data_ptr() if echo else 0, _stream(stream, k)))
+    if status:
+        _pkg._check(status)
+    return out
 
 
 def hqq_kv_read(cache: KVCache, slots, dtype=None, out=None, stream=None):
@@ -170,74 +222,79 @@ def hqq_kv_read(cache: KVCache, slots, dtype=None, out=None, stream=None):
     cache's `slots` (int64 [n]) stand for; zeros for a slot outside the cache.  `out` = (k, v) takes
     them instead of new tensors."""
     torch = _torch()
-    _pkg._need(slots, "slots", torch.int64)
-    if slots.dim() != 1:
-        raise ValueError("slots must be [n]")
+    _indices(slots, "slots", torch.int64, 1)
+    _pkg._placed(slots, "slots")
     shape = (slots.shape[0], cache.num_kv_heads, cache.head_dim)
     if out is None:
-        code = _dtype_code(dtype or torch.float16)
-        with _pkg._on(stream):
-            out = tuple(torch.empty(shape, dtype=dtype or torch.float16, device=slots.device) for _ in range(2))
+        dtype = dtype or torch.float16
+        code = _dtype_code(dtype)
+        like = (shape, dtype, slots.device)
+        out = tuple(_empty(stream, like, like))
     else:
         code = _dtype_code(out[0].dtype)
         for t, name in zip(out, ("k", "v")):
             _pkg._need(t, name, out[0].dtype, shape=shape)
-    a = KvReadArgs(cache.args(), code, slots.shape[0], slots.data_ptr(), out[0].data_ptr(), out[1].data_ptr(),
-                   _stream(stream))
-    _pkg._check(_pkg.load().hqq_kv_read(a))
+    status = _entry("hqq_kv_read")(_READ.pack(*cache.args(), code, shape[0], slots.data_ptr(), out[0].data_ptr(),
+                                              out[1].data_ptr(), _stream(stream, slots)))
+    if status:
+        _pkg._check(status)
     return out
 
 
 def _attention(entry, cache, q, page_table, seq_lens, scale, cu_q, max_q, max_len, causal, prefix_table, prefix_len,
                out, return_lse, workspace, stream):
     torch = _torch()
-    code = _dtype_code(q.dtype)
-    if q.dim() != 3 or q.shape[2] != cache.head_dim:
-        raise ValueError("q must be [total_q, heads, %d], got %s" % (cache.head_dim, tuple(q.shape)))
-    total_q, heads = q.shape[0], q.shape[1]
-    qt, qh = _strides(q, "q", heads, cache.head_dim)
-    _pkg._need(seq_lens, "seq_lens", torch.int32)
-    _pkg._need(page_table, "page_table", torch.int32, device=False)
-    if not page_table.is_cuda or page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table must be a CUDA (HIP) tensor [num_seqs, pages], each row contiguous")
+    dtype = q.dtype
+    code = _dtype_code(dtype)
+    dim = cache.head_dim
+    if q.dim() != 3 or q.shape[2] != dim:
+        raise ValueError("q must be [total_q, heads, %d], got %s" % (dim, tuple(q.shape)))
+    total_q, heads, _ = q.shape
+    qt, qh = _strides(q, "q", heads, dim)
+    _indices(seq_lens, "seq_lens", torch.int32, 1)
+    _indices(page_table, "page_table", torch.int32, 2)
+    _pkg._placed(seq_lens, "seq_lens")
     seqs, cols = page_table.shape
-    if seq_lens.dim() != 1 or seq_lens.shape[0] != seqs:
+    row, col = page_table.stride()
+    if not page_table.is_cuda or (col != 1 and cols > 1):
+        raise ValueError("page_table must be a CUDA (HIP) tensor [num_seqs, pages], each row contiguous")
+    if seq_lens.shape[0] != seqs:
         raise ValueError("seq_lens must be [num_seqs] = [%d], got %s" % (seqs, tuple(seq_lens.shape)))
     if cu_q is not None:
-        _pkg._need(cu_q, "cu_q", torch.int32)
-        if cu_q.dim() != 1 or cu_q.shape[0] != seqs + 1:
+        _indices(cu_q, "cu_q", torch.int32, 1)
+        _pkg._placed(cu_q, "cu_q")
+        if cu_q.shape[0] != seqs + 1:
             raise ValueError("cu_q must be [num_seqs + 1]")
         if max_q is None:
             max_q = total_q
     if prefix_len:
-        _pkg._need(prefix_table, "prefix_table", torch.int32)
-        if prefix_len < 0 or prefix_table.numel() * cache.page_size < prefix_len:
-            raise ValueError("prefix_table holds %d pages, too few for %d tokens" % (prefix_table.numel(), prefix_len))
-    if scale is None:
-        scale = cache.head_dim ** -0.5
-    lse = None
-    with _pkg._on(stream):
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        else:
-            _pkg._need(out, "out", q.dtype, shape=q.shape)
-        if return_lse:
-            lse = torch.empty((total_q, heads), dtype=torch.float32, device=q.device)
-        a = KvAttentionArgs(cache.args(), code, q.data_ptr(), total_q, qt, qh, heads, seqs,
-                            None if cu_q is None else cu_q.data_ptr(), max_q or 0, page_table.data_ptr(),
-                            max(page_table.stride(0), cols), cols, seq_lens.data_ptr(),
-                            cols * cache.page_size if max_len is None else min(max_len, cols * cache.page_size),
-                            1 if causal else 0, scale, prefix_table.data_ptr() if prefix_len else None, prefix_len,
-                            out.data_ptr(), lse.data_ptr() if return_lse else None, None, 0, _stream(stream))
-        lib = _pkg.load()
-        need = lib.hqq_kv_attention_workspace_bytes(a)
-        if need and workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    if workspace is not None:
+        _indices(prefix_table, "prefix_table", torch.int32, 1)
+        _pkg._placed(prefix_table, "prefix_table")
+        if prefix_len < 0 or prefix_table.shape[0] * cache.page_size < prefix_len:
+            raise ValueError("prefix_table holds %d pages, too few for %d tokens" % (prefix_table.shape[0], prefix_len))
+    most = cols * cache.page_size
+    if out is None:
+        out, = _empty(stream, (q.shape, dtype, q.device))
+    else:
+        _pkg._need(out, "out", dtype, shape=q.shape)
+    lse = _empty(stream, ((total_q, heads), torch.float32, q.device))[0] if return_lse else None
+    head = (*cache.args(), code, q.data_ptr(), total_q, qt, qh, heads, seqs, 0 if cu_q is None else cu_q.data_ptr(),
+            max_q or 0, page_table.data_ptr(), row if row > cols else cols, cols, seq_lens.data_ptr(),
+            most if max_len is None or max_len > most else max_len, 1 if causal else 0,
+            dim ** -0.5 if scale is None else scale, prefix_table.data_ptr() if prefix_len else 0, prefix_len,
+            out.data_ptr(), 0 if lse is None else lse.data_ptr())
+    handle = _stream(stream, q)
+    if workspace is None:
+        need = _entry("hqq_kv_attention_workspace_bytes")(_ATTENTION.pack(*head, 0, 0, handle))
+        if need:
+            workspace, = _empty(stream, ((need,), torch.uint8, q.device))
+    else:
         _pkg._need(workspace, "workspace", torch.uint8)
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    _pkg._check(getattr(lib, entry)(a))
-    return (out, lse) if return_lse else out
+        need = workspace.numel()
+    status = _entry(entry)(_ATTENTION.pack(*head, workspace.data_ptr() if need else 0, need, handle))
+    if status:
+        _pkg._check(status)
+    return out if lse is None else (out, lse)
 
 
 def hqq_kv_attention(cache: KVCache, q, page_table, seq_lens, scale=None, cu_q=None, max_q=None, max_len=None,
