@@ -56,15 +56,18 @@ struct StepV {
   u32x4 m[2];
 };
 
-// A step's registers and the page ids of the step they hold and of the next one they will hold.
-struct Ids {
-  int id[2];
+// Where a step's two tiles lie: their pages' blocks, and bit t set where tile t has no keys (past the end, or no such
+// page; some tokens of page 0 are loaded then, unused).
+struct Place {
+  const uint8_t* base[2];
+  uint32_t bad;
 };
+// A step's registers, and the places of the step they hold and of the next one they will hold.
 template <int D, int BITS, int NG>
 struct Stage {
   StepK<D, BITS, NG> k;
   StepV<D, BITS> v;
-  Ids now, then;
+  Place now, then;
 };
 
 template <int N>
@@ -139,7 +142,7 @@ __global__ __launch_bounds__(SPLIT ? 256 : 512, SPLIT ? stream_waves(D, GS, NT) 
   const int page = 1 << a.f.page_shift;
 
   // ---- the block's share, and where it begins
-  KeyList list = a.first_list ? a.list[1] : a.list[0];
+  KeyList list = SPLIT && a.first_list ? a.list[1] : a.list[0];
   Share share{0, 0};
   uint32_t u = 0, u_end = 0, u_begin = 0, pair = 0, x0 = 0, pairs = 0;  // pairs: in front of this one
   int seq = 0;
@@ -229,39 +232,48 @@ __global__ __launch_bounds__(SPLIT ? 256 : 512, SPLIT ? stream_waves(D, GS, NT) 
   const int first_t = __builtin_amdgcn_readfirstlane(row0 / a.per);
   const int end_min = list.causal ? len - tq + first_t + 1 : len;  // keys below it are seen by every row
 
-  // ---- the wave's first keys are on their way while the queries are prepared
+  // ---- queries, page ids and the wave's first keys are on their way before any of them is waited for
+  u32x4 qw[NT][G::kMf];
+  int rt[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int r = row0 + 16 * t + n;
+    rt[t] = r < rows ? r / a.per : -1;
+    const int token = max(rt[t], 0), head = r < rows ? r - token * a.per : 0;
+    const uint16_t* p =
+        reinterpret_cast<const uint16_t*>(a.q) + (int64_t)(q0 + token) * a.q_ts + (int64_t)(hk * a.per + head) * a.q_hs + 8 * h;
+#pragma unroll
+    for (int i = 0; i < G::kMf; ++i) qw[t][i] = *reinterpret_cast<const u32x4*>(p + 32 * i);
+  }
   uint32_t k_off = n * G::kRow + h * (G::kRow / 4);
   uint32_t v_off = page * G::kRow + (h * 16 + n) * (4 * G::kUnit);
   uint32_t km_off = 2 * page * G::kRow + 16 * h;
   uint32_t vm_off = km_off + 4 * page * (NG + (n * (D / 16)) / GS);
   const int32_t* table = list.table + (int64_t)seq * list.table_stride;
 
-  // page ids of a step's two tiles (-1: past the end, or no such page), loaded a step before the codes
-  auto page_ids = [&](int key0) {
-    Ids x;
+  const int last_page = max(list.table_cols - 1, 0);  // (a table without columns: any readable entry)
+  auto place_of = [&](int key0) {
+    Place x;
+    x.bad = 0;
 #pragma unroll
     for (int t = 0; t < (PAIR ? 1 : 2); ++t) {
       // (the entry is loaded before the length that says whether it counts has arrived)
       const int key = key0 + 16 * t;
-      const int id = list.table_cols > 0 ? entry(table, min(key >> a.f.page_shift, list.table_cols - 1)) : -1;
-      x.id[t] = key < ke && (uint32_t)id < a.f.num_pages ? id : -1;
+      const uint32_t id = entry(table, min(key >> a.f.page_shift, last_page));
+      const bool ok = key < ke && id < a.f.num_pages;
+      x.bad |= ok ? 0u : (PAIR ? 3u : 1u << t);
+      x.base[t] = a.f.pages + (uint64_t)(ok ? id : 0) * (uint64_t)a.f.page_bytes + hk * a.f.block_bytes;
     }
-    if (PAIR) x.id[1] = x.id[0];
+    if (PAIR) x.base[1] = x.base[0], x.bad |= key0 + 16 < ke ? 0u : 2u;
     return x;
   };
-  auto tile_at = [&](int key, int id, int* off) {
-    *off = key & (page - 1);
-    return (const uint8_t*)a.f.pages + (uint64_t)(uint32_t)max(id, 0) * (uint64_t)a.f.page_bytes + hk * a.f.block_bytes;
-  };
-  auto fetch_k = [&](int key0, Ids x, StepK<D, BITS, NG>& s) {
+  auto fetch_k = [&](int key0, const Place& x, StepK<D, BITS, NG>& s) {
     // (opaque per step, so that the lane's 32-bit offset stays one next to the wave's 64-bit address)
     asm volatile("" : "+v"(k_off), "+v"(km_off));
-    int off;
-    const uint8_t* base = tile_at(key0, x.id[0], &off);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if (!PAIR && t) base = tile_at(key0 + 16, x.id[1], &off);
-      const int more = PAIR ? 16 * t : 0;
+      const uint8_t* base = x.base[t];
+      const int off = (PAIR ? key0 : key0 + 16 * t) & (page - 1), more = PAIR ? 16 * t : 0;
       load_words(base + off * G::kRow + k_off + more * G::kRow, s.c[t]);
 #pragma unroll
       for (int g = 0; g < NG; ++g)
@@ -269,14 +281,12 @@ __global__ __launch_bounds__(SPLIT ? 256 : 512, SPLIT ? stream_waves(D, GS, NT) 
             __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(base + (off + g * page) * 4 + km_off + more * 4));
     }
   };
-  auto fetch_v = [&](int key0, Ids x, StepV<D, BITS>& s) {
+  auto fetch_v = [&](int key0, const Place& x, StepV<D, BITS>& s) {
     asm volatile("" : "+v"(v_off), "+v"(vm_off));
-    int off;
-    const uint8_t* base = tile_at(key0, x.id[0], &off);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      if (!PAIR && t) base = tile_at(key0 + 16, x.id[1], &off);
-      const int more = PAIR ? 16 * t : 0;
+      const uint8_t* base = x.base[t];
+      const int off = (PAIR ? key0 : key0 + 16 * t) & (page - 1), more = PAIR ? 16 * t : 0;
       load_words(base + off * G::kRow + v_off + more * G::kRow, s.c[t]);
       s.m[t] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(base + off * 4 + vm_off + more * 4));
     }
@@ -285,14 +295,15 @@ __global__ __launch_bounds__(SPLIT ? 256 : 512, SPLIT ? stream_waves(D, GS, NT) 
   Stage<D, BITS, NG> stage[SETS];
 #pragma unroll
   for (int i = 0; i < SETS; ++i) {
+    stage[i].now = place_of(first + i * kStride);
+    stage[i].then = place_of(first + (SETS + i) * kStride);
+  }
+#pragma unroll
+  for (int i = 0; i < SETS; ++i) {
+    // (without keys here: some tokens of page 0, unused)
     const int key0 = first + i * kStride;
-    stage[i].now = stage[i].then = Ids{{-1, -1}};
-    if (key0 < ke) {
-      stage[i].now = page_ids(key0);
-      stage[i].then = page_ids(key0 + SETS * kStride);
-      fetch_k(key0, stage[i].now, stage[i].k);
-      fetch_v(key0, stage[i].now, stage[i].v);
-    }
+    fetch_k(key0, stage[i].now, stage[i].k);
+    fetch_v(key0, stage[i].now, stage[i].v);
   }
 
   // ---- queries: rows in fp16 with a power of two of their own, sums per group
@@ -301,51 +312,60 @@ __global__ __launch_bounds__(SPLIT ? 256 : 512, SPLIT ? stream_waves(D, GS, NT) 
   int lim[NT];  // last key the lane's row sees
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    const int r = row0 + 16 * t + n;
-    const bool there = r < rows;
-    const int rt = (there ? r : row0) / a.per, rg = (there ? r : row0) % a.per;
-    const int64_t at = (int64_t)(q0 + rt) * a.q_ts + (int64_t)(hk * a.per + rg) * a.q_hs;
-    u32x4 w[G::kMf];
-    float top = 0.f;
+    const bool there = rt[t] >= 0;
+    u32x4(&w)[G::kMf] = qw[t];
+    // the row's largest value by its bits (their order is that of the magnitudes, in either type)
+    u16x2 most = {0, 0};
 #pragma unroll
     for (int i = 0; i < G::kMf; ++i) {
-      w[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.q) + at + 32 * i + 8 * h);
       if (!there) w[i] = u32x4{0, 0, 0, 0};
-    }
 #pragma unroll
-    for (int i = 0; i < G::kMf; ++i) {
-      float x[8];
-      floats8(w[i], a.dtype, x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
+      for (int j = 0; j < 4; ++j) most = __builtin_elementwise_max(most, as_u16x2(w[i][j] & 0x7fff7fffu));
     }
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    // the row's largest value to [2^14, 2^15): q / 16 keeps fp16's full precision for 2^13 below it
+    uint32_t top = max((uint32_t)most.x, (uint32_t)most.y);
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+    // 2^e takes it to [2^14, 2^15) (fp16 rows: e up to 15): q / 16 then keeps fp16's precision for 2^13
+    // below it, and a bfloat16 row of any size keeps its bits
     int e = 0;
-    if (top > 0.f && top < INFINITY) e = 14 - (int)((__builtin_bit_cast(uint32_t, top) >> 23) & 255) + 127;
-    e = min(e, 100);
-    cs[t] = ldexpf(a.scale_log2, 24 - e);
+    if (a.dtype == HQQ_KV_BF16) {
+      const int x = top >> 7;
+      if (x != 0 && x != 255) e = min(14 + 127 - x, 100);
 #pragma unroll
-    for (int g = 0; g < NG; ++g) sq[t][g] = 0.f;
+      for (int i = 0; i < G::kMf; ++i) {
+        float x8[8];
+        floats8<true>(w[i], x8);
 #pragma unroll
-    for (int i = 0; i < G::kMf; ++i) {
-      float x[8];
-      floats8(w[i], a.dtype, x);
+        for (int j = 0; j < 8; ++j) qf[t][i][j] = (_Float16)ldexpf(x8[j], BITS == 4 && (j & 2) ? e - 4 : e);
+      }
+    } else {
+      const int x = top >> 10;
+      if (top != 0 && x != 31) e = min(14 + 15 - x, 15);
+      const _Float16 up = (_Float16)ldexpf(1.f, e), up4 = (_Float16)ldexpf(1.f, BITS == 4 ? e - 4 : e);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float y = ldexpf(x[j], e);
-        sq[t][i * 32 / GS] += y;
-        qf[t][i][j] = (_Float16)(BITS == 4 && (j & 2) ? y * 0.0625f : y);
+      for (int i = 0; i < G::kMf; ++i) {
+        u32x4 y;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = as_u32(as_h2(w[i][j]) * (j & 1 ? h2{up4, up4} : h2{up, up}));
+        qf[t][i] = __builtin_bit_cast(h8, y);
       }
     }
+    cs[t] = ldexpf(a.scale_log2, 24 - e);
+    const h2 one = {(_Float16)1.f, (_Float16)1.f}, back = {(_Float16)16.f, (_Float16)16.f};
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-      sq[t][g] += __shfl_xor(sq[t][g], 16);
-      sq[t][g] += __shfl_xor(sq[t][g], 32);
-      sq[t][g] *= 0x1p-24f;  // the scale of the codes' products
+      float sum = 0.f;
+#pragma unroll
+      for (int i = g * GS / 32; i < (g + 1) * GS / 32; ++i) {
+        const u32x4 y = __builtin_bit_cast(u32x4, qf[t][i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum = __builtin_amdgcn_fdot2(as_h2(y[j]), BITS == 4 && (j & 1) ? back : one, sum, false);
+      }
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      sq[t][g] = sum * 0x1p-24f;  // the scale of the codes' products
     }
-    lim[t] = there ? (list.causal ? min(len - 1, len - tq + rt) : len - 1) : -1;
+    lim[t] = there ? (list.causal ? min(len - 1, len - tq + rt[t]) : len - 1) : -1;
   }
 
   // ---- the stream
@@ -369,7 +389,7 @@ __global__ __launch_bounds__(SPLIT ? 256 : 512, SPLIT ? stream_waves(D, GS, NT) 
   auto step = [&](int key0, Stage<D, BITS, NG>& g) {
     StepK<D, BITS, NG>& sk = g.k;
     StepV<D, BITS>& sv = g.v;
-    const uint32_t bad = (g.now.id[0] < 0 ? 1u : 0u) | (g.now.id[1] < 0 ? 2u : 0u);
+    const uint32_t bad = g.now.bad;
     // scores
     float p[NT][8];
 #pragma unroll
@@ -526,7 +546,7 @@ __global__ __launch_bounds__(SPLIT ? 256 : 512, SPLIT ? stream_waves(D, GS, NT) 
     }
     if (more) fetch_v(key0 + SETS * kStride, g.then, sv);
     g.now = g.then;
-    g.then = page_ids(key0 + 2 * SETS * kStride);
+    g.then = place_of(key0 + 2 * SETS * kStride);
   };
   for (int key0 = first; key0 < ke; key0 += SETS * kStride) {
 #pragma unroll
