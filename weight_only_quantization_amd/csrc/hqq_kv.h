@@ -96,6 +96,7 @@ hipError_t launch_kv_tile(const AttnArgs& a, int which, int D, int bits, int gs,
 hipError_t launch_kv_join(const AttnArgs& a, int D, int nt_own, int nt_prefix, hipStream_t st);
 
 constexpr int kUnitKeys = 128;  // keys of the stream's unit of work: a step of each of a block's four waves
+constexpr uint32_t kStartUnits = 3;  // units that beginning a (sequence, row tile, KV head) counts for
 
 constexpr float kNoKey = -1e30f;  // running maximum before any key (finite: differences of two stay numbers)
 

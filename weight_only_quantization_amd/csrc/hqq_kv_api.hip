@@ -65,7 +65,14 @@ struct Plan {
   size_t workspace;
 };
 
-int row_kernel(int64_t rows) { return rows <= 16 ? kStream16 : rows <= 64 ? kStream32 : kTile; }
+// `lists` times that many rows (KV heads times sequences).  17 to 64 rows take 32 a block, which reads the keys for
+// twice the rows, unless blocks of 16 are no more than the CUs: then those end sooner (16 sequences of 2001
+// keys, 5 tokens, 32 heads on 8: 19.6 us with 16 rows, 22.7 with 32; 12 tokens: 35 and 24).  More rows
+// take tiles (24 tokens there: 45 us, 47 streamed).
+int row_kernel(int64_t rows, int64_t lists) {
+  if (rows > 64) return kTile;
+  return rows <= 16 || (rows + 15) / 16 * lists <= 256 ? kStream16 : kStream32;
+}
 int nt_of(int kind) { return kind == kStream16 ? 1 : 2; }
 int64_t row_tiles(int64_t rows, int kind) {
   const int64_t of = kind == kStream16 ? 16 : kind == kStream32 ? 32 : 256;
@@ -85,14 +92,14 @@ void split_keys(KeyList* l, int64_t blocks) {
 }
 
 // Longest own keys that one block streams for a pair; longer ones are shared out over the blocks.
-constexpr int64_t kWholeKeys = 4096;
+constexpr int64_t kWholeKeys = 2048;
 
 // Blocks of a stream launch: what fills the GPU, but at least two units each.
 int stream_grid(const Plan& p, const hqq_kv_cache& c, int first, int lists) {
   int64_t units = 0;
   for (int i = first; i < first + lists; ++i) {
     const KeyList& l = p.a.list[i];
-    const int64_t keys = l.max_len > 0 ? (l.max_len + hqq::kv::kUnitKeys - 1) / hqq::kv::kUnitKeys : 1;
+    const int64_t keys = hqq::kv::kStartUnits + (l.max_len + hqq::kv::kUnitKeys - 1) / hqq::kv::kUnitKeys;
     units += keys * l.num_seqs * p.a.f.hkv * row_tiles((int64_t)l.max_q * p.a.per, p.kind[i]);
   }
   const int64_t most = hqq::kv::stream_blocks(c.head_dim, c.group_size, nt_of(p.kind[first]));
@@ -168,9 +175,9 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
   for (int i = 0; i < (a.joined ? 2 : 1); ++i) {
     KeyList& l = a.list[i];
     const int64_t rows = (int64_t)l.max_q * a.per;
-    p->kind[i] = row_kernel(rows);
+    p->kind[i] = row_kernel(rows, (int64_t)f.hkv * l.num_seqs);
     const int64_t tiles = row_tiles(rows, p->kind[i]), pairs = tiles * f.hkv * l.num_seqs;
-    KV_NEED(tiles <= 65535 && pairs * (l.max_len / hqq::kv::kUnitKeys + 1) <= (int64_t(1) << 30), HQQ_ERR_UNSUPPORTED,
+    KV_NEED(tiles <= 65535 && pairs * (l.max_len / hqq::kv::kUnitKeys + hqq::kv::kStartUnits + 1) <= (int64_t(1) << 30), HQQ_ERR_UNSUPPORTED,
             "too many query rows and keys in a call");
     if (p->kind[i] == kTile) {
       l.tiled = 1;
@@ -180,7 +187,7 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
       const int64_t most = 16 * nt_of(p->kind[i]);
       l.cap = (int)(rows < most ? rows : most);
       // (own keys and a prefix that streams alike take one launch of shares)
-      const bool alone = !a.joined || row_kernel(x->total_q * a.per) != p->kind[0];
+      const bool alone = !a.joined || row_kernel(x->total_q * a.per, f.hkv) != p->kind[0];
       if (i == 0 && alone && l.max_len <= kWholeKeys) {
         l.tiled = l.nsplit = 1;
       } else {

@@ -121,8 +121,9 @@ template <int NT>
 __device__ __forceinline__ uint32_t tiles_of(const AttnArgs& a, int tq) {
   return (uint32_t)(tq * a.per + 16 * NT - 1) / (16 * NT);
 }
-// (a sequence without keys has one unit: its rows are written all the same)
-__device__ __forceinline__ uint32_t units_of(int len) { return max(1u, (uint32_t)(len + kUnitKeys - 1) / kUnitKeys); }
+// A pair's units: kStartUnits without keys for what it costs to begin one (queries, page table, first
+// loads, joining the waves: about as long as three units), then those of its keys.
+__device__ __forceinline__ uint32_t units_of(int len) { return kStartUnits + (uint32_t)(len + kUnitKeys - 1) / kUnitKeys; }
 
 // PAIR: pages of at least 32 tokens, so a step's two tiles share a page (one lookup, one address).
 // SPLIT: the shares above, four waves a block.  Else a block takes a whole pair with eight waves: what short
@@ -147,18 +148,36 @@ __global__ __launch_bounds__(SPLIT ? 256 : 512, SPLIT ? stream_waves(D, GS, NT) 
   uint32_t u = 0, u_end = 0, u_begin = 0, pair = 0, x0 = 0, pairs = 0;  // pairs: in front of this one
   int seq = 0;
   if (SPLIT) {
-  auto weight = [&](const KeyList& l, int seq) -> uint32_t {
-    const Sequence s = sequence_of<false>(a, l, seq);
-    return units_of(s.len) * tiles_of<NT>(a, s.tq) * a.f.hkv;
+  // units and pairs up to and with each lane's sequence, 64 sequences at a time
+  struct Scan {
+    uint32_t units, pairs, own_units, own_pairs;
   };
-  uint32_t total = 0;
-  for (int li = a.first_list; li < a.first_list + a.lists; ++li) {
-    const KeyList l = li ? a.list[1] : a.list[0];
-    for (int s0 = 0; s0 < l.num_seqs; s0 += 64) {
-      uint32_t w = s0 + lane < l.num_seqs ? weight(l, s0 + lane) : 0;
+  auto scan = [&](const KeyList& l, int s0) {
+    Scan x{0, 0, 0, 0};
+    if (s0 + lane < l.num_seqs) {
+      const Sequence s = sequence_of<false>(a, l, s0 + lane);
+      x.own_pairs = tiles_of<NT>(a, s.tq) * a.f.hkv;
+      x.own_units = units_of(s.len) * x.own_pairs;
+    }
+    x.units = x.own_units, x.pairs = x.own_pairs;
+    if (l.num_seqs > 1) {
 #pragma unroll
-      for (int i = 1; i < 64; i <<= 1) w += __shfl_xor(w, i);
-      total += w;
+      for (int i = 1; i < 64; i <<= 1) {
+        const uint32_t y = __shfl_up(x.units, i), z = __shfl_up(x.pairs, i);
+        if (lane >= i) x.units += y, x.pairs += z;
+      }
+    } else {
+      x.units = __shfl(x.units, 0), x.pairs = __shfl(x.pairs, 0);
+    }
+    return x;
+  };
+  const int last = a.first_list + a.lists - 1;
+  const Scan first_scan = scan(list, 0);
+  uint32_t total = __shfl(first_scan.units, 63);
+  if (list.num_seqs > 64 || a.lists > 1) {
+    for (int li = a.first_list; li <= last; ++li) {
+      const KeyList l = li ? a.list[1] : a.list[0];
+      for (int s0 = li == a.first_list ? 64 : 0; s0 < l.num_seqs; s0 += 64) total += __shfl(scan(l, s0).units, 63);
     }
   }
   total = __builtin_amdgcn_readfirstlane(total);
@@ -170,34 +189,21 @@ __global__ __launch_bounds__(SPLIT ? 256 : 512, SPLIT ? stream_waves(D, GS, NT) 
   u_end = share.begin(blockIdx.x + 1);
   int li = a.first_list;
   uint32_t before = 0;  // units in front of the sequence
-  for (bool found = false; !found;) {
-    const KeyList l = li ? a.list[1] : a.list[0];
-    for (int s0 = 0; s0 < l.num_seqs && !found; s0 += 64) {
-      uint32_t w = 0, p = 0;
-      if (s0 + lane < l.num_seqs) {
-        const Sequence s = sequence_of<false>(a, l, s0 + lane);
-        p = tiles_of<NT>(a, s.tq) * a.f.hkv;
-        w = units_of(s.len) * p;
-      }
-      uint32_t wi = w, pi = p;
-#pragma unroll
-      for (int i = 1; i < 64; i <<= 1) {
-        const uint32_t x = __shfl_up(wi, i), y = __shfl_up(pi, i);
-        if (lane >= i) wi += x, pi += y;
-      }
-      const uint64_t past = __ballot(before + wi > u);
-      if (past) {
-        const int at = __builtin_ctzll(past);
-        seq = s0 + at;
-        before += __shfl(wi - w, at);
-        pairs += __shfl(pi - p, at);
-        found = true;
-      } else {
-        before += __shfl(wi, 63);
-        pairs += __shfl(pi, 63);
-      }
+  Scan x = first_scan;
+  for (int s0 = 0;;) {
+    const uint64_t past = __ballot(before + x.units > u);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      seq = s0 + at;
+      before += __shfl(x.units - x.own_units, at);
+      pairs += __shfl(x.pairs - x.own_pairs, at);
+      break;
     }
-    if (!found) ++li;
+    before += __shfl(x.units, 63);
+    pairs += __shfl(x.pairs, 63);
+    s0 += 64;
+    if (s0 >= (li ? a.list[1].num_seqs : a.list[0].num_seqs)) ++li, s0 = 0;
+    x = scan(li ? a.list[1] : a.list[0], s0);
   }
   seq = __builtin_amdgcn_readfirstlane(seq);
   before = __builtin_amdgcn_readfirstlane(before);
@@ -227,8 +233,8 @@ __global__ __launch_bounds__(SPLIT ? 256 : 512, SPLIT ? stream_waves(D, GS, NT) 
   const int row0 = tile * 16 * NT;
   const int last_t = __builtin_amdgcn_readfirstlane((min(row0 + 16 * NT, rows) - 1) / a.per);
   const int end_all = list.causal ? min(len, max(0, len - tq + last_t + 1)) : len;
-  const int kb = x0 * kUnitKeys;
-  const int ke = min((int)x1 * kUnitKeys, end_all);
+  const int kb = max((int)x0 - (int)kStartUnits, 0) * kUnitKeys;
+  const int ke = min(max((int)x1 - (int)kStartUnits, 0) * kUnitKeys, end_all);
   const int first_t = __builtin_amdgcn_readfirstlane(row0 / a.per);
   const int end_min = list.causal ? len - tq + first_t + 1 : len;  // keys below it are seen by every row
 
