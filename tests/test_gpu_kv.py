@@ -275,6 +275,25 @@ def test_value_ranges(bits, vscale):
             check(torch, o, lse, s.expect(), s.dt, tiles=t > 16, what="vscale %g" % vscale)
 
 
+@pytest.mark.parametrize("bits", [4, 8])
+def test_largest_values(bits):
+    """Keys and values at the largest fp16 number: what their groups stand for may lie past it."""
+    hq, torch = lib()
+    for t in (1, 40):
+        f = kp.Fmt(1, 128, bits, 64, 32)
+        rng = np.random.default_rng(25)
+        s = Scene(hq, torch, f, [150], [t], 2, "float16", seed=22, qscale=2e-5)
+        x = [np.clip(3e4 * rng.normal(size=(150, 1, 128)), -65504, 65504).astype(np.float32) for _ in "kv"]
+        for y in x:
+            y[::3, 0, ::5], y[1::3, 0, ::7] = 65504, -65504
+        slots = np.array([int(s.table[0, j // 32]) * 32 + j % 32 for j in range(150)], np.int64)
+        k, v = (kp.to(y, s.dt) for y in x)
+        ke, ve = hq.hqq_kv_write(s.cache, k.cuda(), v.cuda(), torch.from_numpy(slots).cuda(), echo=True)
+        s.kv[0] = [kp.quantise(kp.as_f32(y), bits, 64) for y in (k, v)]
+        o, lse = attend(hq, torch, s)
+        check(torch, o, lse, s.expect(), s.dt, tiles=t > 16, what="largest, %d tokens" % t)
+
+
 @pytest.mark.parametrize("qscale", [0.0, 1e-7, 30.0, 500.0])
 def test_query_ranges(qscale):
     """Flat, ordinary and one-key softmaxes; a query row of NaN touches no other row."""

@@ -3,12 +3,18 @@
 // Prompts' chunks, and a prefix under all the rows of a batch: the keys of a tile are dequantised once
 // for 256 rows, k = fp16(m + c s) with one rounding, into LDS, and both products run on the matrix unit:
 //   S^T[key][row] = K Q^T,  o^T[channel][row] += V^T P^T,
-// so a lane's scores (16 of one row) are its operand of the second product as they are: V^T is kept
-// in LDS with its keys in that order.
-// Eight waves, 32 rows each; all of them unpack 1/8 of the next tile while they work on this one (two
+// so a lane's scores (16 of one row to 32 keys) are its operand of the second product as they are: V^T is
+// kept in LDS with its keys in that order.  p is rounded to fp16; all sums are fp32.
+// Eight waves, 32 rows each; all of them unpack 1/8 of the next tile next to this one's products (two
 // buffers of K and V, one barrier a tile).  Codes, step and floor become values in packed fp16:
 // (1024 + c) - 1024 is exact, fma(c, s, m) rounds once.
 // Softmax as in the stream kernel: one pass, fp32, the maximum raised only when a score passes it by 2^5.
+//
+// 2048 tokens on 8192 keys, 32 heads on 8, 4 bits: 240 Gflop in 320-350 us, 0.69-0.75 Pflop/s; a library
+// product of two 8192 x 8192 fp16 matrices reaches 1.18.  Per 32 x 32 scores a wave needs 512 cycles of
+// the matrix unit and about 630 of the vector unit (16 exponentials take 256); with K and V from LDS and
+// their unpacking it takes about 1600 of its SIMD, without either 920.  Tried without gain: operands read from LDS
+// a phase ahead, 64 rows a wave with one wave a SIMD (480 us), wave priorities around the products.
 #include "hqq_kv.h"
 
 namespace hqq {
@@ -67,6 +73,10 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, h = lane >> 5;
+  // fp16 results past the largest number stay there (MODE.FP16_OVFL): a group that reaches +-65504 may stand for
+  // a little more than fp16 holds
+  __builtin_amdgcn_s_setreg(1 | 23 << 6, 1);
+
   // Grid: KV head and sequence (x), row tile (y), key split (z).  Blocks go round the eight XCDs in order
   // of x, so the pairs are turned by tile and split: the parts of one long sequence spread over
   // all XCDs.  The tiles with the most keys under a causal rule start first.
@@ -229,31 +239,41 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
   float mref = kNoKey, l = 0.f;
 
+  // 64 keys at a time: two chains of products and of weights side by side
   auto attend = [&](int key0, const u32x4* kt, const u32x4* vt, bool holes) {
 #pragma unroll 1
-    for (int sub = 0; sub < kKeys / 32; ++sub) {
+    for (int sub = 0; sub < kKeys / 32; sub += 2) {
       const int first = key0 + 32 * sub;
       if (first >= w_end) return;
-      f32x16 s;
+      f32x16 s[2];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) s[i] = 0.f;
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int i = 0; i < KS; ++i) {
-        const h8 kf = __builtin_bit_cast(h8, kt[k_chunk<D>(32 * sub + n, 2 * i + h)]);
-        s = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[i], s, 0, 0, 0);
-      }
-      if (holes | (first + 32 > w_min) | (first + 32 > ke)) {
+        for (int i = 0; i < 16; ++i) s[c][i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int key = first + 8 * (i >> 2) + 4 * h + (i & 3);
-          bool on = key <= lim && key < ke;
-          if (holes && on) on = (uint32_t)table[key >> a.f.page_shift] < a.f.num_pages;
-          s[i] = on ? s[i] : -INFINITY;
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const h8 kf = __builtin_bit_cast(h8, kt[k_chunk<D>(32 * (sub + c) + n, 2 * i + h)]);
+          s[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[i], s[c], 0, 0, 0);
         }
-      }
-      float top = s[0];
+      if (holes | (first + 64 > w_min) | (first + 64 > ke)) {
 #pragma unroll
-      for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int key = first + 32 * c + 8 * (i >> 2) + 4 * h + (i & 3);
+            bool on = key <= lim && key < ke;
+            if (holes) {
+              const int id = table[min(key >> a.f.page_shift, max(list.table_cols - 1, 0))];
+              on = on && (uint32_t)id < a.f.num_pages;
+            }
+            s[c][i] = on ? s[c][i] : -INFINITY;
+          }
+      }
+      float top = s[0][0];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(fmaxf(top, s[0][i]), s[1][i]);
       top *= cs;
       if (__any(top > mref + 5.f)) {
         top = fmaxf(top, __shfl_xor(top, 32));
@@ -264,45 +284,59 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] *= f;
       }
-      float sum = 0.f;
-      h8 pf[2];
+      float sum[2] = {0.f, 0.f};
+      h8 pf[2][2];
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const f32x2 e = {exp2_(fmaf(s[i], cs, -mref)), exp2_(fmaf(s[i + 1], cs, -mref))};
-        sum += e[0] + e[1];
-        const h2 p = __builtin_convertvector(e, h2);
-        pf[i >> 3][i & 7] = p.x, pf[i >> 3][(i & 7) + 1] = p.y;
-      }
-      l += sum;
+      for (int i = 0; i < 16; i += 2)
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const h8 vf = __builtin_bit_cast(h8, vt[v_chunk(32 * d + n, 4 * sub + 2 * t + h)]);
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[t], o[d], 0, 0, 0);
+        for (int c = 0; c < 2; ++c) {
+          const f32x2 e = {exp2_(fmaf(s[c][i], cs, -mref)), exp2_(fmaf(s[c][i + 1], cs, -mref))};
+          sum[c] += e[0] + e[1];
+          const h2 p = __builtin_convertvector(e, h2);
+          pf[c][i >> 3][i & 7] = p.x, pf[c][i >> 3][(i & 7) + 1] = p.y;
         }
+      l += sum[0] + sum[1];
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            const h8 vf = __builtin_bit_cast(h8, vt[v_chunk(32 * d + n, 4 * (sub + c) + 2 * t + h)]);
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[c][t], o[d], 0, 0, 0);
+          }
     }
   };
 
   if (kb < ke) {
     Raw<D, BITS, NG> raw;
     int id_k = page_id(kb + ik), id_v = page_id(kb + iv);
-    bool holes = __syncthreads_or((id_k < 0 && kb + ik < ke) ? 1 : 0);
-    fetch(kb, id_k, id_v, raw);
-    id_k = page_id(kb + kKeys + ik), id_v = page_id(kb + kKeys + iv);
+    int bad = id_k < 0 && kb + ik < ke;
+    auto load = [&](int key0) {  // the codes of the tile at key0, and the page ids of the one after it
+      if (key0 < ke) fetch(key0, id_k, id_v, raw);
+      bad = id_k < 0 && key0 + ik < ke;
+      id_k = page_id(key0 + kKeys + ik), id_v = page_id(key0 + kKeys + iv);
+    };
+    load(kb);
+    bool holes = __syncthreads_or(bad);
     unpack(raw, sh_k[0], sh_v[0]);
+    load(kb + kKeys);
     int buf = 0;
+    // The second wave of each SIMD unpacks before its products and the first one after them, so that one's matrix
+    // instructions meet the other's vector instructions.
+    const bool early = wave >= kWaves / 2;
     for (int key0 = kb; key0 < ke; key0 += kKeys) {
-      const int next = key0 + kKeys;
-      const bool more = next < ke;
-      const int bad = id_k < 0 && next + ik < ke;
-      if (more) {
-        fetch(next, id_k, id_v, raw);
-        id_k = page_id(next + kKeys + ik), id_v = page_id(next + kKeys + iv);
-      }
+      const bool more = key0 + kKeys < ke;
       const bool next_holes = __syncthreads_or(bad);  // this tile is written; the other buffer is free
+      if (more && early) {
+        unpack(raw, sh_k[buf ^ 1], sh_v[buf ^ 1]);
+        load(key0 + 2 * kKeys);
+      }
       attend(key0, sh_k[buf], sh_v[buf], holes);
-      if (more) unpack(raw, sh_k[buf ^ 1], sh_v[buf ^ 1]);
+      if (more && !early) {
+        unpack(raw, sh_k[buf ^ 1], sh_v[buf ^ 1]);
+        load(key0 + 2 * kKeys);
+      }
       holes = next_holes;
       buf ^= 1;
     }

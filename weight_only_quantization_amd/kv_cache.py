@@ -94,13 +94,16 @@ class KVCache:
         """The fields of hqq_kv_cache, checked."""
         t = self.pages
         fmt = (self.num_kv_heads, self.head_dim, self.nbits, self.group_size, self.page_size)
+        need = _sizes.get(fmt)
+        if need is None:
+            need = _page_bytes(*fmt)
+        shape = t.shape
         if t.dtype is not _torch().uint8:
             raise ValueError("pages must be torch.uint8, got %s" % t.dtype)
         _pkg._placed(t, "pages")
-        need = _sizes.get(fmt) or _page_bytes(*fmt)
-        if need and (t.dim() < 2 or t.numel() != t.shape[0] * need):
-            raise ValueError("pages must be [num_pages, ...] of %d bytes a page, got %s" % (need, tuple(t.shape)))
-        return (t.data_ptr(), t.shape[0]) + fmt
+        if need and (len(shape) < 2 or t.numel() != shape[0] * need):
+            raise ValueError("pages must be [num_pages, ...] of %d bytes a page, got %s" % (need, tuple(shape)))
+        return (t.data_ptr(), shape[0]) + fmt
 
 
 _sizes = {}
@@ -164,13 +167,19 @@ def _stream(stream, t):
     return _torch()._C._cuda_getCurrentRawStream(t.get_device())
 
 
-def _empty(stream, *shapes_like):
-    """New tensors on the stream the kernels run on (see _on): (shape, dtype, device) each."""
-    torch = _torch()
+def _empty(stream, shape, dtype, near):
+    """A new tensor on the device of `near`, on the stream the kernels run on (see _on)."""
     if stream is None:
-        return [torch.empty(s, dtype=d, device=v) for s, d, v in shapes_like]
+        return near.new_empty(shape, dtype=dtype)
     with _pkg._on(stream):
-        return [torch.empty(s, dtype=d, device=v) for s, d, v in shapes_like]
+        return near.new_empty(shape, dtype=dtype)
+
+
+def _like(stream, t):
+    """A new contiguous tensor of t's shape and type (torch.empty_like is the faster call where t is contiguous)."""
+    if stream is None and t.is_contiguous():
+        return _torch().empty_like(t)
+    return _empty(stream, t.shape, t.dtype, t)
 
 
 def hqq_kv_page_bytes(num_kv_heads: int, head_dim: int, nbits: int = 4, group_size: int = 64,
@@ -207,8 +216,8 @@ def hqq_kv_write(cache: KVCache, k, v, slots, echo: bool = False, stream=None):
     _pkg._placed(slots, "slots")
     out = None
     if echo:
-        like = (k.shape, dtype, k.device)
-        out = tuple(_empty(stream, like, like))
+        first = _like(stream, k)
+        out = (first, _like(stream, first))
     status = _entry("hqq_kv_write")(_WRITE.pack(
         *cache.args(), code, k.data_ptr(), v.data_ptr(), n, kt, kh, vt, vh, slots.data_ptr(),
         out[0].data_ptr() if echo else 0, out[1].data_ptr() if echo else 0, _stream(stream, k)))
@@ -228,8 +237,8 @@ def hqq_kv_read(cache: KVCache, slots, dtype=None, out=None, stream=None):
     if out is None:
         dtype = dtype or torch.float16
         code = _dtype_code(dtype)
-        like = (shape, dtype, slots.device)
-        out = tuple(_empty(stream, like, like))
+        first = _empty(stream, shape, dtype, slots)
+        out = (first, _like(stream, first))
     else:
         code = _dtype_code(out[0].dtype)
         for t, name in zip(out, ("k", "v")):
@@ -274,10 +283,10 @@ def _attention(entry, cache, q, page_table, seq_lens, scale, cu_q, max_q, max_le
             raise ValueError("prefix_table holds %d pages, too few for %d tokens" % (prefix_table.shape[0], prefix_len))
     most = cols * cache.page_size
     if out is None:
-        out, = _empty(stream, (q.shape, dtype, q.device))
+        out = _like(stream, q)
     else:
         _pkg._need(out, "out", dtype, shape=q.shape)
-    lse = _empty(stream, ((total_q, heads), torch.float32, q.device))[0] if return_lse else None
+    lse = _empty(stream, (total_q, heads), torch.float32, q) if return_lse else None
     head = (*cache.args(), code, q.data_ptr(), total_q, qt, qh, heads, seqs, 0 if cu_q is None else cu_q.data_ptr(),
             max_q or 0, page_table.data_ptr(), row if row > cols else cols, cols, seq_lens.data_ptr(),
             most if max_len is None or max_len > most else max_len, 1 if causal else 0,
@@ -287,7 +296,7 @@ def _attention(entry, cache, q, page_table, seq_lens, scale, cu_q, max_q, max_le
     if workspace is None:
         need = _entry("hqq_kv_attention_workspace_bytes")(_ATTENTION.pack(*head, 0, 0, handle))
         if need:
-            workspace, = _empty(stream, ((need,), torch.uint8, q.device))
+            workspace = _empty(stream, need, torch.uint8, q)
     else:
         _pkg._need(workspace, "workspace", torch.uint8)
         need = workspace.numel()
