@@ -275,6 +275,34 @@ def test_value_ranges(bits, vscale):
             check(torch, o, lse, s.expect(), s.dt, tiles=t > 16, what="vscale %g" % vscale)
 
 
+@pytest.mark.parametrize("qscale", [1e3, 6e4])
+def test_scores_past_fp32_units(qscale):
+    """Scores of 1e7 to 1e10, where a unit of fp32 is as large as many powers of two of a weight: every row is
+    finite, and the value of one of the keys whose scores are the largest to fp32."""
+    hq, torch = lib()
+    for t in (1, 40):
+        f = kp.Fmt(1, 128, 8, 64, 32)
+        s = Scene(hq, torch, f, [300], [t], 2, "float16", seed=27, qscale=1.0)
+        x = (np.random.default_rng(28).choice([-1.0, 1.0], size=(300, 1, 128)) * 3e4).astype(np.float32)
+        slots = np.array([int(s.table[0, j // 32]) * 32 + j % 32 for j in range(300)], np.int64)
+        k = kp.to(x, s.dt)
+        v = kp.to(np.arange(300)[:, None, None] + np.zeros((300, 1, 128)), torch.float32).to(s.dt)
+        hq.hqq_kv_write(s.cache, k.cuda(), v.cuda(), torch.from_numpy(slots).cuda())
+        s.kv[0] = [kp.quantise(kp.as_f32(y), 8, 64) for y in (k, v)]
+        s.q = (s.q.float().clamp(-1, 1) * qscale).to(s.dt)
+        o, lse = attend(hq, torch, s)
+        assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+        kk, _, _, _ = s.dense(0)
+        for i in range(t):
+            for h in range(2):
+                sc = s.scale * (kk[:, 0] @ s.q[i, h].double().numpy())
+                sc[300 - t + i + 1:] = -np.inf
+                near = np.flatnonzero(sc >= sc.max() - 2.0 ** -10 * np.abs(sc).max())
+                got = float(o[i, h, 0])
+                assert near.min() - 0.51 <= got <= near.max() + 0.51, (t, i, h, got, near)
+                assert abs(float(lse[i, h]) - sc.max()) <= 2.0 ** -10 * np.abs(sc[sc > -np.inf]).max()
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 def test_largest_values(bits):
     """Keys and values at the largest fp16 number: what their groups stand for may lie past it."""

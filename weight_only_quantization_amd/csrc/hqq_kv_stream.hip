@@ -383,10 +383,10 @@ __global__ __launch_bounds__(SPLIT ? 256 : 512, SPLIT ? stream_waves(D, GS, NT) 
   float zero;  // (opaque: a fused step and floor instead of a conversion and a product)
   asm("v_mov_b32 %0, 0" : "=v"(zero));
   f32x4 o[NT][G::kVm], fl[NT];  // channels (4h + i) * (D/16) + j; floors' sums of those units
-  float mref[NT], l[NT];
+  float mref[NT], l[NT];  // running maximum (of the scores before cs) and sum
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    mref[t] = kNoKey, l[t] = 0.f;
+    mref[t] = kNoKey / fmaxf(cs[t], 1.f), l[t] = 0.f;
     fl[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < G::kVm; ++j) o[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -484,24 +484,33 @@ __global__ __launch_bounds__(SPLIT ? 256 : 512, SPLIT ? stream_waves(D, GS, NT) 
       float top = p[t][0];
 #pragma unroll
       for (int c = 1; c < 8; ++c) top = fmaxf(top, p[t][c]);
-      top *= cs[t];
-      if (__any(top > mref[t] + slack)) {
+      if (__any((top - mref[t]) * cs[t] > slack)) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         const float next = fmaxf(mref[t], top);
-        const float f = exp2_(mref[t] - next);
+        const float f = exp2_((mref[t] - next) * cs[t]);
         mref[t] = next;
         l[t] *= f;
 #pragma unroll
         for (int j = 0; j < G::kVm; ++j) o[t][j] *= f;
         fl[t] *= f;
       }
+      // exponents: one fused operation, whose constant's rounding is nothing until scores of 2^20; from there on the
+      // difference first, so that the largest score's is 0 and none passes the largest number (a row without a key so
+      // far, or of NaN, does not count)
+      const float c0 = fmaf(-mref[t], cs[t], lift);
+      if (__any(fabsf(c0) > 0x1p20f && mref[t] > kNoKey / 1e17f)) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) p[t][c] = fmaf(p[t][c] - mref[t], cs[t], lift);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) p[t][c] = fmaf(p[t][c], cs[t], c0);
+      }
       float sum = 0.f;
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
-        const float e = exp2_(fmaf(p[t][c], cs[t], lift - mref[t]));
-        sum += e;
-        p[t][c] = e;
+        p[t][c] = exp2_(p[t][c]);
+        sum += p[t][c];
       }
       l[t] = fmaf(sum, drop, l[t]);
 #pragma unroll
@@ -572,6 +581,7 @@ __global__ __launch_bounds__(SPLIT ? 256 : 512, SPLIT ? stream_waves(D, GS, NT) 
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
+    mref[t] *= cs[t];  // in units of the exponent from here on
     l[t] += __shfl_xor(l[t], 16);
     l[t] += __shfl_xor(l[t], 32);
     if (h == 0) sh_m[wave][16 * t + n] = mref[t], sh_l[wave][16 * t + n] = l[t];

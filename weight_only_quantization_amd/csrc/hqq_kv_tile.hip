@@ -237,7 +237,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
   for (int d = 0; d < DT; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
-  float mref = kNoKey, l = 0.f;
+  float mref = kNoKey / fmaxf(cs, 1.f), l = 0.f;  // running maximum (of the scores before cs) and sum
 
   // 64 keys at a time: two chains of products and of weights side by side
   auto attend = [&](int key0, const u32x4* kt, const u32x4* vt, bool holes) {
@@ -274,15 +274,27 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
       float top = s[0][0];
 #pragma unroll
       for (int i = 0; i < 16; ++i) top = fmaxf(fmaxf(top, s[0][i]), s[1][i]);
-      top *= cs;
-      if (__any(top > mref + 5.f)) {
+      if (__any((top - mref) * cs > 5.f)) {
         top = fmaxf(top, __shfl_xor(top, 32));
         const float next = fmaxf(mref, top);
-        const float f = exp2_(mref - next);
+        const float f = exp2_((mref - next) * cs);
         mref = next;
         l *= f;
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] *= f;
+      }
+      // (exponents as in the stream kernel)
+      const float c0 = -mref * cs;
+      if (__any(fabsf(c0) > 0x1p20f && mref > kNoKey / 1e17f)) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[c][i] = (s[c][i] - mref) * cs;
+      } else {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) s[c][i] = fmaf(s[c][i], cs, c0);
       }
       float sum[2] = {0.f, 0.f};
       h8 pf[2][2];
@@ -290,7 +302,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
       for (int i = 0; i < 16; i += 2)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const f32x2 e = {exp2_(fmaf(s[c][i], cs, -mref)), exp2_(fmaf(s[c][i + 1], cs, -mref))};
+          const f32x2 e = {exp2_(s[c][i]), exp2_(s[c][i + 1])};
           sum[c] += e[0] + e[1];
           const h2 p = __builtin_convertvector(e, h2);
           pf[c][i >> 3][i & 7] = p.x, pf[c][i >> 3][(i & 7) + 1] = p.y;
@@ -343,6 +355,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
   }
 
   // ---- output: channels 32 d + 8 (i / 4) + 4 h + i % 4 of the lane's row
+  mref *= cs;  // in units of the exponent from here on
   l += __shfl_xor(l, 32);
   if (!there) return;
   const int64_t at = (int64_t)(q0 + rt) * a.hq + hk * a.per + rg;
