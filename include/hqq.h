@@ -473,7 +473,7 @@ int hqq_kv_read(const hqq_kv_read_args* args);
  *   cu_q       in  int32 [num_seqs + 1] (device): sequence b has the query tokens cu_q[b] .. cu_q[b+1]-1, at
  *              most max_q of them; NULL: total_q / num_seqs tokens each (which must divide).  Tokens
  *              of no sequence, or of one whose range leaves the tensor or exceeds max_q, have undefined outputs.
- *   page_table in  int32 [num_seqs, table_cols] (device), rows table_stride apart: a sequence's pages in order.
+ *   page_table in  int32 [num_seqs, table_cols] (device), rows table_stride apart (0: one row for all): a sequence's pages in order.
  *              Tokens on a page outside the cache (-1, say) are masked out.
  *   seq_lens   in  int32 [num_seqs] (device): cached tokens of each sequence, its query tokens included;
  *              0 for none.  Limited to max_len (host; a bound the caller knows) and to the table.

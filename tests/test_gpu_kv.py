@@ -388,6 +388,23 @@ def test_query_strides_and_repeats():
     assert none.shape == (0, 8, 128)
 
 
+def test_page_table_strides():
+    """Page tables as columns of a wider one, and one row for all sequences."""
+    hq, torch = lib()
+    f = kp.Fmt(2, 128, 4, 64, 32)
+    s = Scene(hq, torch, f, [100, 100, 64], [1, 1, 1], 4, "float16", seed=43)
+    lens = torch.tensor(s.lens, dtype=torch.int32, device="cuda")
+    q, t = s.q.cuda(), torch.from_numpy(s.table).cuda()
+    want = hq.hqq_kv_attention(s.cache, q, t, lens)
+    wide = torch.full((3, 11), -1, dtype=torch.int32, device="cuda")
+    wide[:, 2:2 + t.shape[1]] = t
+    assert torch.equal(hq.hqq_kv_attention(s.cache, q, wide[:, 2:2 + t.shape[1]], lens), want)
+    one = hq.hqq_kv_attention(s.cache, q, t[:1].expand(3, -1), lens)
+    assert torch.equal(one, hq.hqq_kv_attention(s.cache, q, t[:1].repeat(3, 1), lens)) and torch.equal(one[0], want[0])
+    with pytest.raises(ValueError, match="row contiguous"):
+        hq.hqq_kv_attention(s.cache, q, t.t().contiguous().t(), lens)
+
+
 def test_cache_past_32_bits():
     """Pages whose bytes lie past 2^32: written, read and attended at their own place."""
     hq, torch = lib()

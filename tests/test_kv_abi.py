@@ -89,7 +89,7 @@ def test_read_refused(lib, kw):
     (dict(dtype=7), BAD), (dict(total_q=-1), BAD), (dict(total_q=5), BAD), (dict(num_seqs=0), BAD), (dict(num_q_heads=7), BAD),
     (dict(num_q_heads=0), BAD), (dict(cu_q=FAKE, max_q=5), BAD), (dict(cu_q=FAKE, max_q=-1), BAD), (dict(max_len=-1), BAD),
     (dict(max_len=1 << 31), BAD), (dict(prefix_len=-1), BAD), (dict(prefix_len=3), BAD), (dict(prefix_table=FAKE), BAD),
-    (dict(table_cols=-1), BAD), (dict(table_cols=1 << 26, table_stride=1 << 26), BAD), (dict(table_stride=99), BAD), (dict(causal=2), BAD),
+    (dict(table_cols=-1), BAD), (dict(table_cols=1 << 26, table_stride=1 << 26), BAD), (dict(table_stride=-1), BAD), (dict(causal=2), BAD),
     (dict(scale=0.0), BAD), (dict(scale=-1.0), BAD), (dict(scale=float("inf")), BAD), (dict(scale=float("nan")), BAD),
     (dict(q=None), BAD), (dict(q=FAKE + 2), BAD), (dict(out=None), BAD), (dict(q_token_stride=1025), BAD),
     (dict(q_head_stride=-128), BAD), (dict(seq_lens=None), BAD), (dict(page_table=None), BAD), (dict(workspace=None), WS),

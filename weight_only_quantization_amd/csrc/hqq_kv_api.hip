@@ -132,7 +132,7 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
   KV_NEED(x->prefix_len >= 0 && x->prefix_len <= INT32_MAX - 256, HQQ_ERR_INVALID_ARGUMENT, "prefix_len out of range");
   KV_NEED(x->table_cols >= 0 && x->table_cols * (int64_t)c.page_size <= INT32_MAX, HQQ_ERR_INVALID_ARGUMENT,
           "table_cols out of range");
-  KV_NEED(x->table_stride >= x->table_cols, HQQ_ERR_INVALID_ARGUMENT, "table_stride is smaller than table_cols");
+  KV_NEED(x->table_stride >= 0, HQQ_ERR_INVALID_ARGUMENT, "table_stride must not be negative");
   KV_NEED(x->causal == 0 || x->causal == 1, HQQ_ERR_INVALID_ARGUMENT, "causal must be 0 or 1");
   KV_NEED(x->scale > 0.f && x->scale <= 3.0e38f, HQQ_ERR_INVALID_ARGUMENT, "scale must be finite and positive");
 

@@ -99,7 +99,7 @@ constexpr int stream_waves(int D, int GS, int NT) {
   return D == 64 || D / GS <= 2 ? 2 : 1;
 }
 
-// Steps whose registers a wave of a whole pair holds (256 registers a lane there).
+// Steps whose registers a wave of an eight-wave block holds (256 registers a lane there).
 constexpr int whole_sets(int D, int BITS, int GS, int NT) {
   return D == 64 || (BITS == 4 ? NT == 1 || D / GS <= 2 : NT == 1 && D / GS <= 2) ? 2 : 1;
 }
@@ -126,15 +126,18 @@ __device__ __forceinline__ uint32_t tiles_of(const AttnArgs& a, int tq) {
 __device__ __forceinline__ uint32_t units_of(int len) { return kStartUnits + (uint32_t)(len + kUnitKeys - 1) / kUnitKeys; }
 
 // PAIR: pages of at least 32 tokens, so a step's two tiles share a page (one lookup, one address).
-// SPLIT: the shares above, four waves a block.  Else a block takes a whole pair with eight waves: what short
+// MODE: kShares as above, four waves a block; or a block takes a whole pair with eight waves or with four: what short
 // sequences want, with no schedule to work out and nothing to join.
-template <int D, int BITS, int GS, int NT, bool PAIR, bool SPLIT>
-__global__ __launch_bounds__(SPLIT ? 256 : 512, SPLIT ? stream_waves(D, GS, NT) : 2) void k_kv_stream(AttnArgs a) {
+enum { kShares, kWhole8, kWhole4 };
+template <int D, int BITS, int GS, int NT, bool PAIR, int MODE>
+__global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : stream_waves(D, GS, NT)) void k_kv_stream(
+    AttnArgs a) {
+  constexpr bool SPLIT = MODE == kShares;
   using G = Geo<D, BITS>;
   constexpr int NG = D / GS;
   constexpr int kLdsRow = D + 4;
-  constexpr int W = SPLIT ? 4 : 8;  // waves
-  constexpr int SETS = SPLIT ? 1 : whole_sets(D, BITS, GS, NT), kStride = 32 * W;  // steps whose registers are held; keys of a block's step
+  constexpr int W = MODE == kWhole8 ? 8 : 4;  // waves
+  constexpr int SETS = MODE == kWhole8 ? whole_sets(D, BITS, GS, NT) : 1, kStride = 32 * W;  // steps whose registers are held; keys of a block's step
   __shared__ __attribute__((aligned(16))) float sh_o[W][16][kLdsRow];
   __shared__ float sh_m[W][16 * NT], sh_l[W][16 * NT];
 
@@ -782,11 +785,17 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int nt_own, int nt_
 template <int D, int BITS, int GS, int NT, bool PAIR>
 void stream_nt(const AttnArgs& a, hipStream_t st) {
   if (a.blocks) {
-    k_kv_stream<D, BITS, GS, NT, PAIR, true><<<a.blocks, 256, 0, st>>>(a);
+    k_kv_stream<D, BITS, GS, NT, PAIR, kShares><<<a.blocks, 256, 0, st>>>(a);
   } else {
     const KeyList& l = a.list[a.first_list];
     const int tiles = (int)(((int64_t)l.max_q * a.per + 16 * NT - 1) / (16 * NT));
-    k_kv_stream<D, BITS, GS, NT, PAIR, false><<<dim3(a.f.hkv * l.num_seqs, tiles), 512, 0, st>>>(a);
+    const dim3 grid(a.f.hkv * l.num_seqs, tiles);
+    // A CU holds one block of eight waves; more blocks than CUs would take it in turns, blocks of four run side by side
+    // (64 sequences of 1000 keys, 64 heads on 8: 23.5 us with eight waves, 18.9 with four).
+    if ((int64_t)grid.x * tiles <= 256)
+      k_kv_stream<D, BITS, GS, NT, PAIR, kWhole8><<<grid, 512, 0, st>>>(a);
+    else
+      k_kv_stream<D, BITS, GS, NT, PAIR, kWhole4><<<grid, 256, 0, st>>>(a);
   }
 }
 

@@ -288,7 +288,7 @@ def _attention(entry, cache, q, page_table, seq_lens, scale, cu_q, max_q, max_le
         _pkg._need(out, "out", dtype, shape=q.shape)
     lse = _empty(stream, (total_q, heads), torch.float32, q) if return_lse else None
     head = (*cache.args(), code, q.data_ptr(), total_q, qt, qh, heads, seqs, 0 if cu_q is None else cu_q.data_ptr(),
-            max_q or 0, page_table.data_ptr(), row if row > cols else cols, cols, seq_lens.data_ptr(),
+            max_q or 0, page_table.data_ptr(), row, cols, seq_lens.data_ptr(),
             most if max_len is None or max_len > most else max_len, 1 if causal else 0,
             dim ** -0.5 if scale is None else scale, prefix_table.data_ptr() if prefix_len else 0, prefix_len,
             out.data_ptr(), 0 if lse is None else lse.data_ptr())
@@ -313,8 +313,9 @@ def hqq_kv_attention(cache: KVCache, q, page_table, seq_lens, scale=None, cu_q=N
     page_table int32 [num_seqs, pages] and seq_lens int32 [num_seqs] (cached tokens, the query tokens
     included) are device tensors; cu_q int32 [num_seqs + 1] gives each sequence's range of query tokens (at
     most max_q; equal shares without it).  max_len bounds seq_lens for the launch (the table's
-    length by default: pass the true bound, the split of the keys goes by it).  scale defaults to
-    head_dim ** -0.5.  Returns out [total_q, heads, head_dim], with return_lse also the fp32 log-sum-exp [total_q,
+    length by default; pass the true bound: up to 2048 keys take a shorter path).  One call's sequences run by the
+    longest one's number of query tokens, so decode steps and prompts' chunks are better called apart.  scale
+    defaults to head_dim ** -0.5.  Returns out [total_q, heads, head_dim], with return_lse also the fp32 log-sum-exp [total_q,
     heads].  A row that sees no key is 0 (-inf)."""
     return _attention("hqq_kv_attention", cache, q, page_table, seq_lens, scale, cu_q, max_q, max_len, causal, None, 0,
                       out, return_lse, workspace, stream)
