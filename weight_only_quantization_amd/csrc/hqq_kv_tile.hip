@@ -10,11 +10,14 @@
 // (1024 + c) - 1024 is exact, fma(c, s, m) rounds once.
 // Softmax as in the stream kernel: one pass, fp32, the maximum raised only when a score passes it by 2^5.
 //
-// 2048 tokens on 8192 keys, 32 heads on 8, 4 bits: 240 Gflop in 320-350 us, 0.69-0.75 Pflop/s; a library
+// 2048 tokens on 8192 keys, 32 heads on 8, 4 bits: 240 Gflop in 300-320 us, 0.75-0.80 Pflop/s; a library
 // product of two 8192 x 8192 fp16 matrices reaches 1.18.  Per 32 x 32 scores a wave needs 512 cycles of
-// the matrix unit and about 630 of the vector unit (16 exponentials take 256); with K and V from LDS and
-// their unpacking it takes about 1600 of its SIMD, without either 920.  Tried without gain: operands read from LDS
-// a phase ahead, 64 rows a wave with one wave a SIMD (480 us), wave priorities around the products.
+// the matrix unit and about 600 of the vector unit (16 exponentials take 256); with K and V from LDS and
+// their unpacking it takes about 1500 of its SIMD, without either 920: the two waves of a SIMD overlap only in part.
+// Padded rows against swizzled ones (an address a read less) 330 -> 312 us, the tile's two halves
+// unrolled and each half's values multiplied while the next half's weights are worked out -> 300-310.  Tried without
+// gain: operands read from LDS a phase ahead, 64 rows a wave with one wave a SIMD (480 us), wave
+// priorities around the products, a prescribed alternation of matrix and vector instructions.
 #include "hqq_kv.h"
 
 namespace hqq {
@@ -46,13 +49,13 @@ constexpr uint32_t pair_sel(int t, int b) {
   return 0x0c000c00u | sy << 16 | sx;
 }
 
-// 16-byte chunk of a row of K (D halves) and of V^T (128 halves), swizzled so that 16 lanes reading one
-// chunk column, and the unpacking writes, spread over all banks.
+// LDS: rows of K (a key's D halves) and of V^T (a channel's 128 keys), 16 bytes of padding each, so that 16
+// lanes reading one 16-byte column, and the unpacking writes, spread over all banks, and every read of a phase is
+// one lane address with a constant offset.  V^T's row x is channel (D/16) (x % 16) + x / 16: the 16 units written at
+// once are neighbours, and a lane of the output holds whole units.
 template <int D>
-__device__ __forceinline__ int k_chunk(int key, int c) {
-  return D == 128 ? key * 16 + (c ^ (key & 15)) : key * 8 + (c ^ ((key >> 1) & 7));
-}
-__device__ __forceinline__ int v_chunk(int d, int c) { return d * 16 + (c ^ ((d ^ (d >> 3)) & 15)); }
+constexpr int kRowK = 2 * D + 16;
+constexpr int kRowV = 2 * kKeys + 16;
 
 template <int D, int BITS, int NG>
 struct Raw {
@@ -68,8 +71,8 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
   constexpr int NG = D / GS, U = D * BITS / 128;
   constexpr int kRow = D * BITS / 8;
   constexpr int KS = D / 16, DT = D / 32;  // MFMA steps of a score, channel tiles of the output
-  __shared__ __attribute__((aligned(16))) u32x4 sh_k[2][kKeys * D / 8];
-  __shared__ __attribute__((aligned(16))) u32x4 sh_v[2][kKeys * D / 8];
+  __shared__ __attribute__((aligned(16))) uint8_t sh_k[2][kKeys * kRowK<D>];
+  __shared__ __attribute__((aligned(16))) uint8_t sh_v[2][D * kRowV];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, h = lane >> 5;
@@ -187,7 +190,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
   asm("v_mov_b32 %0, 0x64006400" : "=v"(or1024));
   asm("v_mov_b32 %0, 0x54005400" : "=v"(or64));
   const h2 n1024 = {(_Float16)-1024.f, (_Float16)-1024.f}, n64 = {(_Float16)-64.f, (_Float16)-64.f};
-  auto unpack = [&](Raw<D, BITS, NG>& s, u32x4* to_k, u32x4* to_v) {
+  auto unpack = [&](Raw<D, BITS, NG>& s, uint8_t* to_k, uint8_t* to_v) {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       const uint32_t mm = s.km[i * 32 / GS];
@@ -206,7 +209,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
           w[j] = as_u32(__builtin_elementwise_fma(as_h2(c) + n1024, st, fm));
         }
       }
-      to_k[k_chunk<D>(ik, 4 * i + (tid & 3))] = w;
+      *reinterpret_cast<u32x4*>(to_k + ik * kRowK<D> + (4 * i + (tid & 3)) * 16) = w;
     }
     h2 st[2], fm[2];
 #pragma unroll
@@ -226,9 +229,10 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
         lo[i] = as_u32(__builtin_elementwise_fma(as_h2(BITS == 4 ? (c & m_lo) | or1024 : c | or1024) + n1024, st[i], fm[i]));
         if (BITS == 4) hi[i] = as_u32(__builtin_elementwise_fma(as_h2((c & m_hi) | or64) + n64, st[i], fm[i]));
       }
-      const int d = unit * (D / 16) + (BITS == 4 ? 2 * b : b);
-      reinterpret_cast<u32x2*>(to_v)[2 * v_chunk(d, chunk) + half] = lo;
-      if (BITS == 4) reinterpret_cast<u32x2*>(to_v)[2 * v_chunk(d + 1, chunk) + half] = hi;
+      const int j = BITS == 4 ? 2 * b : b;  // channel of the unit
+      uint8_t* at = to_v + (16 * j + unit) * kRowV + chunk * 16 + half * 8;
+      *reinterpret_cast<u32x2*>(at) = lo;
+      if (BITS == 4) *reinterpret_cast<u32x2*>(at + 16 * kRowV) = hi;
     }
   };
 
@@ -240,8 +244,10 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
   float mref = kNoKey / fmaxf(cs, 1.f), l = 0.f;  // running maximum (of the scores before cs) and sum
 
   // 64 keys at a time: two chains of products and of weights side by side
-  auto attend = [&](int key0, const u32x4* kt, const u32x4* vt, bool holes) {
-#pragma unroll 1
+  auto attend = [&](int key0, const uint8_t* kt, const uint8_t* vt, bool holes) {
+    const uint8_t* kl = kt + n * kRowK<D> + h * 16;
+    const uint8_t* vl = vt + n * kRowV + h * 16;
+#pragma unroll
     for (int sub = 0; sub < kKeys / 32; sub += 2) {
       const int first = key0 + 32 * sub;
       if (first >= w_end) return;
@@ -254,7 +260,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
       for (int i = 0; i < KS; ++i)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const h8 kf = __builtin_bit_cast(h8, kt[k_chunk<D>(32 * (sub + c) + n, 2 * i + h)]);
+          const h8 kf = *reinterpret_cast<const h8*>(kl + 32 * (sub + c) * kRowK<D> + 32 * i);
           s[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[i], s[c], 0, 0, 0);
         }
       if (holes | (first + 64 > w_min) | (first + 64 > ke)) {
@@ -296,27 +302,26 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) s[c][i] = fmaf(s[c][i], cs, c0);
       }
-      float sum[2] = {0.f, 0.f};
-      h8 pf[2][2];
+      float sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; i += 2)
+      for (int c = 0; c < 2; ++c) {
+        h8 pf[2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int i = 0; i < 16; i += 2) {
           const f32x2 e = {exp2_(s[c][i]), exp2_(s[c][i + 1])};
-          sum[c] += e[0] + e[1];
+          sum += e[0] + e[1];
           const h2 p = __builtin_convertvector(e, h2);
-          pf[c][i >> 3][i & 7] = p.x, pf[c][i >> 3][(i & 7) + 1] = p.y;
+          pf[i >> 3][i & 7] = p.x, pf[i >> 3][(i & 7) + 1] = p.y;
         }
-      l += sum[0] + sum[1];
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int d = 0; d < DT; ++d) {
-            const h8 vf = __builtin_bit_cast(h8, vt[v_chunk(32 * d + n, 4 * (sub + c) + 2 * t + h)]);
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[c][t], o[d], 0, 0, 0);
+            const h8 vf = *reinterpret_cast<const h8*>(vl + 32 * d * kRowV + (4 * (sub + c) + 2 * t) * 16);
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, pf[t], o[d], 0, 0, 0);
           }
+      }
+      l += sum;
     }
   };
 
@@ -354,7 +359,8 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
     }
   }
 
-  // ---- output: channels 32 d + 8 (i / 4) + 4 h + i % 4 of the lane's row
+  // ---- output: row x = 32 d + 8 a + 4 h + c of the tile's channels is element 4 a + c of o[d]; the lane holds the
+  // units 8 (a % 2) + 4 h + c whole, channel 2 d + a / 2 of each
   mref *= cs;  // in units of the exponent from here on
   l += __shfl_xor(l, 32);
   if (!there) return;
@@ -364,25 +370,26 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
     if (h == 0) a.part_ml[part] = float2{mref, l};
     if (l != 0.f)
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
+      for (int u = 0; u < 8; ++u) {
+        const int e = (u >> 2) * 4 + (u & 3);  // 4 (a % 2) + c
+        float* to = a.part_o + part * D + (8 * (u >> 2) + 4 * h + (u & 3)) * (D / 16);
 #pragma unroll
-        for (int i = 0; i < 16; i += 4)
-          *reinterpret_cast<f32x4*>(a.part_o + part * D + 32 * d + 2 * i + 4 * h) =
-              f32x4{o[d][i], o[d][i + 1], o[d][i + 2], o[d][i + 3]};
+        for (int d = 0; d < DT; d += 2)
+          *reinterpret_cast<f32x4*>(to + 2 * d) = f32x4{o[d][e], o[d][e + 8], o[d + 1][e], o[d + 1][e + 8]};
+      }
   } else {
     const float inv = l != 0.f ? 1.0f / l : 0.f;
-    uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + at * D + 4 * h;
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+    for (int u = 0; u < 8; ++u) {
+      const int e = (u >> 2) * 4 + (u & 3);
+      uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + at * D + (8 * (u >> 2) + 4 * h + (u & 3)) * (D / 16);
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        u32x2 w;
-        if (a.dtype == HQQ_KV_BF16)
-          w = u32x2{pack2<true>(o[d][i] * inv, o[d][i + 1] * inv), pack2<true>(o[d][i + 2] * inv, o[d][i + 3] * inv)};
-        else
-          w = u32x2{pack2<false>(o[d][i] * inv, o[d][i + 1] * inv), pack2<false>(o[d][i + 2] * inv, o[d][i + 3] * inv)};
-        *reinterpret_cast<u32x2*>(to + 32 * d + 2 * i) = w;
+      for (int d = 0; d < DT; d += 2) {
+        const float y0 = o[d][e] * inv, y1 = o[d][e + 8] * inv, y2 = o[d + 1][e] * inv, y3 = o[d + 1][e + 8] * inv;
+        *reinterpret_cast<u32x2*>(to + 2 * d) = a.dtype == HQQ_KV_BF16 ? u32x2{pack2<true>(y0, y1), pack2<true>(y2, y3)}
+                                                                     : u32x2{pack2<false>(y0, y1), pack2<false>(y2, y3)};
       }
+    }
     if (a.lse && h == 0) a.lse[at] = l != 0.f ? (mref + __log2f(l)) * 0.69314718056f : -INFINITY;
   }
 }

@@ -100,10 +100,11 @@ class KVCache:
         shape = t.shape
         if t.dtype is not _torch().uint8:
             raise ValueError("pages must be torch.uint8, got %s" % t.dtype)
-        _pkg._placed(t, "pages")
+        if not (t.is_cuda and t.is_contiguous()):
+            _pkg._placed(t, "pages")
         if need and (len(shape) < 2 or t.numel() != shape[0] * need):
             raise ValueError("pages must be [num_pages, ...] of %d bytes a page, got %s" % (need, tuple(shape)))
-        return (t.data_ptr(), shape[0]) + fmt
+        return (t.data_ptr(), shape[0], *fmt)
 
 
 _sizes = {}
@@ -129,6 +130,7 @@ def _torch():
 
 
 def _dtype_code(dtype) -> int:
+    _torch()
     code = _codes.get(dtype)
     if code is None:
         raise ValueError("dtype must be torch.float16 or torch.bfloat16, got %s" % dtype)
@@ -150,14 +152,20 @@ def _strides(t, name, heads, dim):
 
 
 def _indices(t, name, dtype, dim):
-    """Checks an index tensor (slots, lengths, offsets)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    """Checks the values of an index tensor (slots, lengths, offsets; its place last, by _there) and returns its shape."""
+    if not isinstance(t, _torch().Tensor):
         raise TypeError("%s must be a torch tensor" % name)
+    shape = t.shape
     if t.dtype is not dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if t.dim() != dim:
-        raise ValueError("%s must have %d dimension%s, got %s" % (name, dim, "" if dim == 1 else "s", tuple(t.shape)))
+    if len(shape) != dim:
+        raise ValueError("%s must have %d dimension%s, got %s" % (name, dim, "" if dim == 1 else "s", tuple(shape)))
+    return shape
+
+
+def _there(t, name):
+    if not (t.is_cuda and t.is_contiguous()):
+        _pkg._placed(t, name)
 
 
 def _stream(stream, t):
@@ -203,17 +211,19 @@ def hqq_kv_write(cache: KVCache, k, v, slots, echo: bool = False, stream=None):
     """Quantises k, v [n, num_kv_heads, head_dim] (fp16 or bf16; token and head strides allowed) into
     the cache's `slots` (int64 [n], distinct; slots outside the cache are skipped).  With `echo`
     returns (k, v) as the values the cache now stands for, else None."""
-    torch = _torch()
-    _indices(slots, "slots", torch.int64, 1)
+    count, = _indices(slots, "slots", _torch().int64, 1)
     dtype, n = k.dtype, k.shape[0]
     if v.dtype is not dtype:
         raise ValueError("k and v must have one dtype, got %s and %s" % (dtype, v.dtype))
-    code = _dtype_code(dtype)
-    if slots.shape[0] != n or v.shape[0] != n:
+    code = _codes.get(dtype)
+    if code is None:
+        code = _dtype_code(dtype)
+    if v.shape[0] != n or count != n:
         raise ValueError("k, v and slots must have the same number of tokens")
-    kt, kh = _strides(k, "k", cache.num_kv_heads, cache.head_dim)
-    vt, vh = _strides(v, "v", cache.num_kv_heads, cache.head_dim)
-    _pkg._placed(slots, "slots")
+    heads, dim = cache.num_kv_heads, cache.head_dim
+    kt, kh = _strides(k, "k", heads, dim)
+    vt, vh = _strides(v, "v", heads, dim)
+    _there(slots, "slots")
     out = None
     if echo:
         first = _like(stream, k)
@@ -231,9 +241,8 @@ def hqq_kv_read(cache: KVCache, slots, dtype=None, out=None, stream=None):
     cache's `slots` (int64 [n]) stand for; zeros for a slot outside the cache.  `out` = (k, v) takes
     them instead of new tensors."""
     torch = _torch()
-    _indices(slots, "slots", torch.int64, 1)
-    _pkg._placed(slots, "slots")
-    shape = (slots.shape[0], cache.num_kv_heads, cache.head_dim)
+    shape = (*_indices(slots, "slots", torch.int64, 1), cache.num_kv_heads, cache.head_dim)
+    _there(slots, "slots")
     if out is None:
         dtype = dtype or torch.float16
         code = _dtype_code(dtype)
@@ -250,64 +259,8 @@ def hqq_kv_read(cache: KVCache, slots, dtype=None, out=None, stream=None):
     return out
 
 
-def _attention(entry, cache, q, page_table, seq_lens, scale, cu_q, max_q, max_len, causal, prefix_table, prefix_len,
-               out, return_lse, workspace, stream):
-    torch = _torch()
-    dtype = q.dtype
-    code = _dtype_code(dtype)
-    dim = cache.head_dim
-    if q.dim() != 3 or q.shape[2] != dim:
-        raise ValueError("q must be [total_q, heads, %d], got %s" % (dim, tuple(q.shape)))
-    total_q, heads, _ = q.shape
-    qt, qh = _strides(q, "q", heads, dim)
-    _indices(seq_lens, "seq_lens", torch.int32, 1)
-    _indices(page_table, "page_table", torch.int32, 2)
-    _pkg._placed(seq_lens, "seq_lens")
-    seqs, cols = page_table.shape
-    row, col = page_table.stride()
-    if not page_table.is_cuda or (col != 1 and cols > 1):
-        raise ValueError("page_table must be a CUDA (HIP) tensor [num_seqs, pages], each row contiguous")
-    if seq_lens.shape[0] != seqs:
-        raise ValueError("seq_lens must be [num_seqs] = [%d], got %s" % (seqs, tuple(seq_lens.shape)))
-    if cu_q is not None:
-        _indices(cu_q, "cu_q", torch.int32, 1)
-        _pkg._placed(cu_q, "cu_q")
-        if cu_q.shape[0] != seqs + 1:
-            raise ValueError("cu_q must be [num_seqs + 1]")
-        if max_q is None:
-            max_q = total_q
-    if prefix_len:
-        _indices(prefix_table, "prefix_table", torch.int32, 1)
-        _pkg._placed(prefix_table, "prefix_table")
-        if prefix_len < 0 or prefix_table.shape[0] * cache.page_size < prefix_len:
-            raise ValueError("prefix_table holds %d pages, too few for %d tokens" % (prefix_table.shape[0], prefix_len))
-    most = cols * cache.page_size
-    if out is None:
-        out = _like(stream, q)
-    else:
-        _pkg._need(out, "out", dtype, shape=q.shape)
-    lse = _empty(stream, (total_q, heads), torch.float32, q) if return_lse else None
-    head = (*cache.args(), code, q.data_ptr(), total_q, qt, qh, heads, seqs, 0 if cu_q is None else cu_q.data_ptr(),
-            max_q or 0, page_table.data_ptr(), row, cols, seq_lens.data_ptr(),
-            most if max_len is None or max_len > most else max_len, 1 if causal else 0,
-            dim ** -0.5 if scale is None else scale, prefix_table.data_ptr() if prefix_len else 0, prefix_len,
-            out.data_ptr(), 0 if lse is None else lse.data_ptr())
-    handle = _stream(stream, q)
-    if workspace is None:
-        need = _entry("hqq_kv_attention_workspace_bytes")(_ATTENTION.pack(*head, 0, 0, handle))
-        if need:
-            workspace = _empty(stream, need, torch.uint8, q)
-    else:
-        _pkg._need(workspace, "workspace", torch.uint8)
-        need = workspace.numel()
-    status = _entry(entry)(_ATTENTION.pack(*head, workspace.data_ptr() if need else 0, need, handle))
-    if status:
-        _pkg._check(status)
-    return out if lse is None else (out, lse)
-
-
 def hqq_kv_attention(cache: KVCache, q, page_table, seq_lens, scale=None, cu_q=None, max_q=None, max_len=None,
-                     causal: bool = True, out=None, return_lse: bool = False, workspace=None, stream=None):
+                     causal: bool = True, out=None, return_lse: bool = False, workspace=None, stream=None, _prefix=None):
     """Attention of query tokens q [total_q, heads, head_dim] over their sequences' cached tokens.
 
     page_table int32 [num_seqs, pages] and seq_lens int32 [num_seqs] (cached tokens, the query tokens
@@ -317,8 +270,63 @@ def hqq_kv_attention(cache: KVCache, q, page_table, seq_lens, scale=None, cu_q=N
     longest one's number of query tokens, so decode steps and prompts' chunks are better called apart.  scale
     defaults to head_dim ** -0.5.  Returns out [total_q, heads, head_dim], with return_lse also the fp32 log-sum-exp [total_q,
     heads].  A row that sees no key is 0 (-inf)."""
-    return _attention("hqq_kv_attention", cache, q, page_table, seq_lens, scale, cu_q, max_q, max_len, causal, None, 0,
-                      out, return_lse, workspace, stream)
+    torch = _torch()
+    dtype, dim, shape = q.dtype, cache.head_dim, q.shape
+    code = _codes.get(dtype)
+    if code is None:
+        code = _dtype_code(dtype)
+    if len(shape) != 3 or shape[2] != dim:
+        raise ValueError("q must be [total_q, heads, %d], got %s" % (dim, tuple(shape)))
+    total_q, heads, _ = shape
+    qt, qh = _strides(q, "q", heads, dim)
+    lens, = _indices(seq_lens, "seq_lens", torch.int32, 1)
+    seqs, cols = _indices(page_table, "page_table", torch.int32, 2)
+    _there(seq_lens, "seq_lens")
+    row, col = page_table.stride()
+    if not page_table.is_cuda or (col != 1 and cols > 1):
+        raise ValueError("page_table must be a CUDA (HIP) tensor [num_seqs, pages], each row contiguous")
+    if lens != seqs:
+        raise ValueError("seq_lens must be [num_seqs] = [%d], got [%d]" % (seqs, lens))
+    if cu_q is not None:
+        if _indices(cu_q, "cu_q", torch.int32, 1)[0] != seqs + 1:
+            raise ValueError("cu_q must be [num_seqs + 1]")
+        _there(cu_q, "cu_q")
+        if max_q is None:
+            max_q = total_q
+    entry, prefix_at, prefix_len = "hqq_kv_attention", 0, 0
+    if _prefix is not None:
+        entry = "hqq_kv_attention_shared"
+        table, prefix_len = _prefix
+        if prefix_len:
+            pages, = _indices(table, "prefix_table", torch.int32, 1)
+            _there(table, "prefix_table")
+            if prefix_len < 0 or pages * cache.page_size < prefix_len:
+                raise ValueError("prefix_table holds %d pages, too few for %d tokens" % (pages, prefix_len))
+            prefix_at = table.data_ptr()
+    most = cols * cache.page_size
+    if out is None:
+        out = _like(stream, q)
+    else:
+        _pkg._need(out, "out", dtype, shape=shape)
+    lse = _empty(stream, (total_q, heads), torch.float32, q) if return_lse else None
+    handle = _stream(stream, q)
+    head = (*cache.args(), code, q.data_ptr(), total_q, qt, qh, heads, seqs, 0 if cu_q is None else cu_q.data_ptr(),
+            max_q or 0, page_table.data_ptr(), row, cols, seq_lens.data_ptr(),
+            most if max_len is None or max_len > most else max_len, 1 if causal else 0,
+            dim ** -0.5 if scale is None else scale, prefix_at, prefix_len, out.data_ptr(), 0 if lse is None else lse.data_ptr())
+    at = need = 0
+    if workspace is None:
+        need = _entry("hqq_kv_attention_workspace_bytes")(_ATTENTION.pack(*head, 0, 0, handle))
+        if need:
+            workspace = _empty(stream, need, torch.uint8, q)
+            at = workspace.data_ptr()
+    else:
+        _pkg._need(workspace, "workspace", torch.uint8)
+        at, need = workspace.data_ptr(), workspace.numel()
+    status = _entry(entry)(_ATTENTION.pack(*head, at, need, handle))
+    if status:
+        _pkg._check(status)
+    return out if lse is None else (out, lse)
 
 
 def hqq_kv_attention_shared(cache: KVCache, q, prefix_table, prefix_len: int, page_table, seq_lens, scale=None,
@@ -327,5 +335,5 @@ def hqq_kv_attention_shared(cache: KVCache, q, prefix_table, prefix_len: int, pa
     """hqq_kv_attention for sequences that share their first prefix_len tokens, kept once on the pages
     prefix_table (int32, device): every row sees the whole prefix, then its own sequence's cached tokens
     (page_table, seq_lens: without the prefix).  The prefix is read once for all rows together."""
-    return _attention("hqq_kv_attention_shared", cache, q, page_table, seq_lens, scale, cu_q, max_q, max_len, causal,
-                      prefix_table, prefix_len, out, return_lse, workspace, stream)
+    return hqq_kv_attention(cache, q, page_table, seq_lens, scale, cu_q, max_q, max_len, causal, out, return_lse,
+                            workspace, stream, (prefix_table, prefix_len))
