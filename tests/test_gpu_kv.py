@@ -405,6 +405,17 @@ def test_page_table_strides():
         hq.hqq_kv_attention(s.cache, q, t.t().contiguous().t(), lens)
 
 
+def test_page_table_without_columns():
+    """No columns of a wide table: no key, whatever the lengths say, and nothing read at the rows' distance."""
+    hq, torch = lib()
+    f = kp.Fmt(2, 128, 4, 64, 32)
+    s = Scene(hq, torch, f, [100] * 9, [2] * 9, 4, "float16", seed=47)
+    wide = torch.full((9, 1 << 12), -1, dtype=torch.int32, device="cuda")
+    lens = torch.tensor(s.lens, dtype=torch.int32, device="cuda")
+    o, lse = hq.hqq_kv_attention(s.cache, s.q.cuda(), wide[:, :0], lens, return_lse=True)
+    assert not o.any() and (lse == -math.inf).all()
+
+
 def test_cache_past_32_bits():
     """Pages whose bytes lie past 2^32: written, read and attended at their own place."""
     hq, torch = lib()

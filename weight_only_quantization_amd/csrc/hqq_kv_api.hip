@@ -151,8 +151,9 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
   a.lse = x->lse;
   a.joined = x->prefix_len > 0;
   KeyList& own = a.list[0];
-  own.table = x->table_cols ? x->page_table : x->seq_lens;  // (readable; no key is on a table without columns)
-  own.table_stride = x->table_stride;
+  // (no key is on a table without columns, but its first entry is loaded before the length is there: any readable one)
+  own.table = x->table_cols ? x->page_table : x->seq_lens;
+  own.table_stride = x->table_cols ? x->table_stride : 0;
   own.table_cols = (int)x->table_cols;
   own.lens = x->seq_lens;
   own.max_len = (int)x->max_len;
