@@ -10,12 +10,12 @@
 // (1024 + c) - 1024 is exact, fma(c, s, m) rounds once.
 // Softmax as in the stream kernel: one pass, fp32, the maximum raised only when a score passes it by 2^5.
 //
-// 2048 tokens on 8192 keys, 32 heads on 8, 4 bits: 240 Gflop in 300-320 us, 0.75-0.80 Pflop/s; a library
+// 2048 tokens on 8192 keys, 32 heads on 8, 4 bits: 240 Gflop in 285 us among such calls (304-316 in a trace), 0.84 Pflop/s; a library
 // product of two 8192 x 8192 fp16 matrices reaches 1.18.  Per 32 x 32 scores a wave needs 512 cycles of
 // the matrix unit and about 600 of the vector unit (16 exponentials take 256); with K and V from LDS and
 // their unpacking it takes about 1500 of its SIMD, without either 920: the two waves of a SIMD overlap only in part.
 // Padded rows against swizzled ones (an address a read less) 330 -> 312 us, the tile's two halves
-// unrolled and each half's values multiplied while the next half's weights are worked out -> 300-310.  Tried without
+// unrolled and each half's values multiplied while the next half's weights are worked out -> 285-310.  Tried without
 // gain: operands read from LDS a phase ahead, 64 rows a wave with one wave a SIMD (480 us), wave
 // priorities around the products, a prescribed alternation of matrix and vector instructions.
 #include "hqq_kv.h"
