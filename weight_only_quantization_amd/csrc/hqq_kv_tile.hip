@@ -114,7 +114,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
 
   // ---- queries
   h8 qf[KS];
-  float cs;
+  float cs, odd = 0.f;  // odd: NaN where the row's query is not finite
   int lim;
   const int r = w_row0 + n;
   const bool there = r < rows;
@@ -133,9 +133,15 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
       float x[8];
       floats8(w[i], a.dtype, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]));
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j])), odd = fmaf(x[j], 0.f, odd);
     }
     top = fmaxf(top, __shfl_xor(top, 32));
+    odd += __shfl_xor(odd, 32);
+    if (odd != odd) {
+      top = 0.f;
+#pragma unroll
+      for (int i = 0; i < KS; ++i) w[i] = u32x4{0, 0, 0, 0};
+    }
     // the row's largest value to [2^14, 2^15): bfloat16 rows of any size keep their bits in fp16
     int e = 0;
     if (top > 0.f && top < INFINITY) e = 14 - (int)((__builtin_bit_cast(uint32_t, top) >> 23) & 255) + 127;
@@ -282,7 +288,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
       for (int i = 0; i < 16; ++i) top = fmaxf(fmaxf(top, s[0][i]), s[1][i]);
       if (__any((top - mref) * cs > 5.f)) {
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float next = fmaxf(mref, top);
+        const float next = (top - mref) * cs > 5.f ? top : mref;  // (each row by its own scores alone)
         const float f = exp2_((mref - next) * cs);
         mref = next;
         l *= f;
@@ -363,6 +369,9 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
   // units 8 (a % 2) + 4 h + c whole, channel 2 d + a / 2 of each
   mref *= cs;  // in units of the exponent from here on
   l += __shfl_xor(l, 32);
+  // a query with an infinity or NaN gives NaN wherever it sees a key (it entered the products as 0: the fp16 mode above
+  // does not hand a NaN on)
+  if (l != 0.f) l += odd;
   if (!there) return;
   const int64_t at = (int64_t)(q0 + rt) * a.hq + hk * a.per + rg;
   if (partial) {
@@ -386,8 +395,10 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
 #pragma unroll
       for (int d = 0; d < DT; d += 2) {
         const float y0 = o[d][e] * inv, y1 = o[d][e + 8] * inv, y2 = o[d + 1][e] * inv, y3 = o[d + 1][e + 8] * inv;
-        *reinterpret_cast<u32x2*>(to + 2 * d) = a.dtype == HQQ_KV_BF16 ? u32x2{pack2<true>(y0, y1), pack2<true>(y2, y3)}
-                                                                     : u32x2{pack2<false>(y0, y1), pack2<false>(y2, y3)};
+        u32x2 w = a.dtype == HQQ_KV_BF16 ? u32x2{pack2<true>(y0, y1), pack2<true>(y2, y3)}
+                                         : u32x2{pack2<false>(y0, y1), pack2<false>(y2, y3)};
+        if (l != l) w = u32x2{0x7fff7fffu, 0x7fff7fffu};
+        *reinterpret_cast<u32x2*>(to + 2 * d) = w;
       }
     }
     if (a.lse && h == 0) a.lse[at] = l != 0.f ? (mref + __log2f(l)) * 0.69314718056f : -INFINITY;
