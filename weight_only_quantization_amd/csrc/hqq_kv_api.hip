@@ -65,12 +65,17 @@ struct Plan {
   size_t workspace;
 };
 
-// `lists` times that many rows (KV heads times sequences).  17 to 64 rows take 32 a block, which reads the keys for
-// twice the rows, unless blocks of 16 are no more than the CUs: then those end sooner (16 sequences of 2001
-// keys, 5 tokens, 32 heads on 8: 19.6 us with 16 rows, 22.7 with 32; 12 tokens: 35 and 24).  More rows
-// take tiles (24 tokens there: 45 us, 47 streamed).
-int row_kernel(int64_t rows, int64_t lists) {
-  if (rows > 64) return kTile;
+// `lists` times that many rows (KV heads times sequences) over `keys` keys.  17 rows and more take 32 a block, which
+// reads the keys for twice the rows, unless blocks of 16 are no more than the CUs: then those end sooner (16
+// sequences of 2001 keys, 5 tokens, 32 heads on 8: 19.6 us with 16 rows, 22.7 with 32; 12 tokens: 35 and 24).
+// More than 64 rows take tiles where there is work enough: a block of tiles takes 10 us to begin and end and 5 us
+// per 128 keys, while streams spread few keys over more and shorter blocks.  Time of the call streamed and in tiles by the
+// millions of pairs of a row and a key of a KV head: 0.36 (298 rows, 306 keys) 13 and 24 us, 3.0 (1290 rows) 14 and 28, 6.9
+// (1856 rows) 13 and 27, 8.4 (105 rows, 9991 keys) 27 and 28, 9.1 to 12 from 24 and 39 to 55 and 40 by type and
+// keys, 23 (375 rows, 1954 keys) 91 and 62, 33 (1024 rows) 76 and 46.
+constexpr int64_t kStreamWork = int64_t(1) << 23, kStreamRows = 1 << 16;  // (rows: the grid's bound, 65535 row tiles)
+int row_kernel(int64_t rows, int64_t lists, int64_t keys) {
+  if (rows > 64 && (rows > kStreamRows || (keys > 0 ? keys : 1) * lists > kStreamWork / rows)) return kTile;
   return rows <= 16 || (rows + 15) / 16 * lists <= 256 ? kStream16 : kStream32;
 }
 int nt_of(int kind) { return kind == kStream16 ? 1 : 2; }
@@ -176,7 +181,7 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
   for (int i = 0; i < (a.joined ? 2 : 1); ++i) {
     KeyList& l = a.list[i];
     const int64_t rows = (int64_t)l.max_q * a.per;
-    p->kind[i] = row_kernel(rows, (int64_t)f.hkv * l.num_seqs);
+    p->kind[i] = row_kernel(rows, (int64_t)f.hkv * l.num_seqs, l.max_len);
     const int64_t tiles = row_tiles(rows, p->kind[i]), pairs = tiles * f.hkv * l.num_seqs;
     KV_NEED(tiles <= 65535 && pairs * (l.max_len / hqq::kv::kUnitKeys + hqq::kv::kStartUnits + 1) <= (int64_t(1) << 30), HQQ_ERR_UNSUPPORTED,
             "too many query rows and keys in a call");
@@ -188,7 +193,7 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
       const int64_t most = 16 * nt_of(p->kind[i]);
       l.cap = (int)(rows < most ? rows : most);
       // (own keys and a prefix that streams alike take one launch of shares)
-      const bool alone = !a.joined || row_kernel(x->total_q * a.per, f.hkv) != p->kind[0];
+      const bool alone = !a.joined || row_kernel(x->total_q * a.per, f.hkv, x->prefix_len) != p->kind[0];
       if (i == 0 && alone && l.max_len <= kWholeKeys) {
         l.tiled = l.nsplit = 1;
       } else {
