@@ -70,16 +70,22 @@ struct Stage {
   Place now, then;
 };
 
-template <int N>
+// ONCE: past the caches, for keys that one block alone reads (the mode kSharesOnce below).
+template <bool ONCE, typename T>
+__device__ __forceinline__ T load(const uint8_t* p) {
+  const T* from = reinterpret_cast<const T*>(p);
+  return ONCE ? __builtin_nontemporal_load(from) : *from;
+}
+template <bool ONCE, int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
   if (N % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
-      const u32x4 t = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p) + i);
+      const u32x4 t = load<ONCE, u32x4>(p + 16 * i);
       w[4 * i] = t[0], w[4 * i + 1] = t[1], w[4 * i + 2] = t[2], w[4 * i + 3] = t[3];
     }
   } else {
-    const u32x2 t = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+    const u32x2 t = load<ONCE, u32x2>(p);
     w[0] = t[0], w[1] = t[1];
   }
 }
@@ -128,11 +134,14 @@ __device__ __forceinline__ uint32_t units_of(int len) { return kStartUnits + (ui
 // PAIR: pages of at least 32 tokens, so a step's two tiles share a page (one lookup, one address).
 // MODE: kShares as above, four waves a block; or a block takes a whole pair with eight waves or with four: what short
 // sequences want, with no schedule to work out and nothing to join.
-enum { kShares, kWhole8, kWhole4 };
+// kSharesOnce: shares of pairs whose rows are one tile each, so that no other block reads the keys: their loads pass the
+// caches by (16 sequences of 16384-32768 keys, 64 heads on 8: 88 us, 95 with ordinary loads; where several tiles of rows read the
+// keys the caches serve the later ones: 104 rows on 5834 keys in 8 bits 27 us, 34 past the caches).
+enum { kShares, kSharesOnce, kWhole8, kWhole4 };
 template <int D, int BITS, int GS, int NT, bool PAIR, int MODE>
 __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : stream_waves(D, GS, NT)) void k_kv_stream(
     AttnArgs a) {
-  constexpr bool SPLIT = MODE == kShares;
+  constexpr bool ONCE = MODE == kSharesOnce, SPLIT = ONCE || MODE == kShares;
   using G = Geo<D, BITS>;
   constexpr int NG = D / GS;
   constexpr int kLdsRow = D + 4;
@@ -283,11 +292,10 @@ __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : 
     for (int t = 0; t < 2; ++t) {
       const uint8_t* base = x.base[t];
       const int off = (PAIR ? key0 : key0 + 16 * t) & (page - 1), more = PAIR ? 16 * t : 0;
-      load_words(base + off * G::kRow + k_off + more * G::kRow, s.c[t]);
+      load_words<ONCE>(base + off * G::kRow + k_off + more * G::kRow, s.c[t]);
 #pragma unroll
       for (int g = 0; g < NG; ++g)
-        s.m[t][g] =
-            __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(base + (off + g * page) * 4 + km_off + more * 4));
+        s.m[t][g] = load<ONCE, u32x4>(base + (off + g * page) * 4 + km_off + more * 4);
     }
   };
   auto fetch_v = [&](int key0, const Place& x, StepV<D, BITS>& s) {
@@ -296,8 +304,8 @@ __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : 
     for (int t = 0; t < 2; ++t) {
       const uint8_t* base = x.base[t];
       const int off = (PAIR ? key0 : key0 + 16 * t) & (page - 1), more = PAIR ? 16 * t : 0;
-      load_words(base + off * G::kRow + v_off + more * G::kRow, s.c[t]);
-      s.m[t] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(base + off * 4 + vm_off + more * 4));
+      load_words<ONCE>(base + off * G::kRow + v_off + more * G::kRow, s.c[t]);
+      s.m[t] = load<ONCE, u32x4>(base + off * 4 + vm_off + more * 4);
     }
   };
   const int first = kb + 32 * wave;
@@ -784,11 +792,15 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int nt_own, int nt_
 
 template <int D, int BITS, int GS, int NT, bool PAIR>
 void stream_nt(const AttnArgs& a, hipStream_t st) {
+  auto tiles_in = [&](const KeyList& l) { return (int)(((int64_t)l.max_q * a.per + 16 * NT - 1) / (16 * NT)); };
+  const KeyList& l = a.list[a.first_list];
+  const int tiles = tiles_in(l);
   if (a.blocks) {
-    k_kv_stream<D, BITS, GS, NT, PAIR, kShares><<<a.blocks, 256, 0, st>>>(a);
+    if (tiles == 1 && (a.lists == 1 || tiles_in(a.list[1]) == 1))
+      k_kv_stream<D, BITS, GS, NT, PAIR, kSharesOnce><<<a.blocks, 256, 0, st>>>(a);
+    else
+      k_kv_stream<D, BITS, GS, NT, PAIR, kShares><<<a.blocks, 256, 0, st>>>(a);
   } else {
-    const KeyList& l = a.list[a.first_list];
-    const int tiles = (int)(((int64_t)l.max_q * a.per + 16 * NT - 1) / (16 * NT));
     const dim3 grid(a.f.hkv * l.num_seqs, tiles);
     // A CU holds one block of eight waves; more blocks than CUs would take it in turns, blocks of four run side by side
     // (64 sequences of 1000 keys, 64 heads on 8: 23.5 us with eight waves, 18.9 with four).
