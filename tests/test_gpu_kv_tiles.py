@@ -1,6 +1,6 @@
 """Attention of many rows in tiles, at the sizes and values where it can go wrong.
 
-Calls of more than 64 rows a KV head run in tiles from 2^23 pairs of a row and a key (of every KV head and sequence) on,
+Calls of more than 64 rows a KV head run in tiles from 3 * 2^23 pairs of a row and a key (of every KV head and sequence) on,
 counted with the host's bound on the lengths.  `attend` here widens the page table with columns that lie past every length, so
 that short sequences take that way too; bounds and scenes are those of tests/test_gpu_kv.py."""
 import numpy as np
@@ -12,7 +12,7 @@ from tests.gpu_common import say
 
 pytestmark = pytest.mark.gpu
 
-WORK = 1 << 23
+WORK = 3 << 23
 plain_attend = base.attend
 
 
@@ -82,7 +82,7 @@ def test_ragged_queries_and_missing_pages():
 
 
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
-@pytest.mark.parametrize("hkv,n", [(2, 200), (16, 1700)])
+@pytest.mark.parametrize("hkv,n", [(2, 200), (16, 5000)])
 def test_rows_that_are_not_finite(dtype, hkv, n):
     """A query row with NaN or an infinity is NaN where it sees a key, 0 where it sees none, and touches no other row;
     with the keys of a pair in one block and split."""
@@ -100,7 +100,7 @@ def test_rows_that_are_not_finite(dtype, hkv, n):
     assert torch.equal(o2, o) and torch.equal(lse2, lse)
 
 
-@pytest.mark.parametrize("t,per,n", [(300, 8, 901), (97, 16, 1430)])
+@pytest.mark.parametrize("t,per,n", [(300, 8, 2701), (97, 16, 4130)])
 def test_key_splits(t, per, n):
     """Sequences long enough by themselves; their keys are split among the blocks and joined."""
     hq, torch = base.lib()
@@ -115,8 +115,8 @@ def test_key_splits(t, per, n):
 def test_shared_prefix():
     """A prefix in tiles, the own keys streamed."""
     hq, torch = base.lib()
-    s = base.Scene(hq, torch, kp.Fmt(8, 64, 4, 32, 64), [7, 0, 130, 55, 3, 64, 1, 90, 20], [3] * 9, 8, "bfloat16", prefix=5001, seed=9)
-    assert 27 * 8 * 8 * 5001 > WORK
+    s = base.Scene(hq, torch, kp.Fmt(8, 64, 4, 32, 64), [7, 0, 130, 55, 3, 64, 1, 90, 20], [3] * 9, 8, "bfloat16", prefix=15001, seed=9)
+    assert 27 * 8 * 8 * 15001 > WORK
     o, lse = plain_attend(hq, torch, s, shared=True)
     base.check(torch, o, lse, s.expect(), s.dt, tiles=True, what="shared")
 
