@@ -476,7 +476,8 @@ int hqq_kv_read(const hqq_kv_read_args* args);
  *   page_table in  int32 [num_seqs, table_cols] (device), rows table_stride apart (0: one row for all): a sequence's pages in order.
  *              Tokens on a page outside the cache (-1, say) are masked out.
  *   seq_lens   in  int32 [num_seqs] (device): cached tokens of each sequence, its query tokens included;
- *              0 for none.  Limited to max_len (host; a bound the caller knows) and to the table.
+ *              0 for none.  Limited to max_len (host; a bound the caller knows, at most 2^31 - 2^16 - 1, as prefix_len) and
+ *              to the table.
  *   causal     1: query token t of T stands at position seq_len - T + t and sees the keys up to it; 0: all.
  *   scale      finite, > 0.
  *   out        out [total_q, num_q_heads, head_dim] contiguous of dtype.  A row that sees no key is 0.

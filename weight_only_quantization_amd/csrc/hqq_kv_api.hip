@@ -54,6 +54,10 @@ int check_cache(const hqq_kv_cache& c, Format* f) {
 
 bool known_type(int dtype) { return dtype == HQQ_KV_F16 || dtype == HQQ_KV_BF16; }
 
+// Most keys of a list.  The kernels count keys in 32 bits and look ahead of the last one: four steps of 256 keys in
+// the stream, two tiles of 128 in the tiles, whose splits end up to 256 * 128 keys past it.
+constexpr int64_t kMostKeys = INT32_MAX - (1 << 16);
+
 // One attention call: its kernels' arguments, the row kernel of each list, the workspace.
 enum { kStream16, kStream32, kTile };  // the stream with 16 or 32 rows a block, or tiles of 256 rows
 
@@ -134,8 +138,8 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
   KV_NEED(x->cu_q || x->num_seqs == 0 || x->total_q % x->num_seqs == 0, HQQ_ERR_INVALID_ARGUMENT,
           "without cu_q total_q must be a multiple of num_seqs");
   KV_NEED(!x->cu_q || (x->max_q >= 0 && x->max_q <= x->total_q), HQQ_ERR_INVALID_ARGUMENT, "max_q must be 0 .. total_q");
-  KV_NEED(x->max_len >= 0 && x->max_len <= INT32_MAX - 256, HQQ_ERR_INVALID_ARGUMENT, "max_len out of range");
-  KV_NEED(x->prefix_len >= 0 && x->prefix_len <= INT32_MAX - 256, HQQ_ERR_INVALID_ARGUMENT, "prefix_len out of range");
+  KV_NEED(x->max_len >= 0 && x->max_len <= kMostKeys, HQQ_ERR_INVALID_ARGUMENT, "max_len out of range");
+  KV_NEED(x->prefix_len >= 0 && x->prefix_len <= kMostKeys, HQQ_ERR_INVALID_ARGUMENT, "prefix_len out of range");
   KV_NEED(x->table_cols >= 0 && x->table_cols * (int64_t)c.page_size <= INT32_MAX, HQQ_ERR_INVALID_ARGUMENT,
           "table_cols out of range");
   KV_NEED(x->table_stride >= 0, HQQ_ERR_INVALID_ARGUMENT, "table_stride must not be negative");
