@@ -2,7 +2,7 @@
 import pytest
 
 import weight_only_quantization_amd as hq
-from tests.test_kv_abi import BAD, FAKE, WS, attention, cache, lib  # noqa: F401
+from tests.test_kv_abi import BAD, FAKE, UNSUP, WS, attention, cache, lib  # noqa: F401
 
 MOST = (1 << 31) - (1 << 16) - 1
 
@@ -18,3 +18,13 @@ def test_key_counts_near_32_bits(lib, past):  # noqa: F811
     e = "hqq_kv_attention_shared"
     assert attention(lib, e, prefix_len=MOST, prefix_table=FAKE, **one) == WS
     assert attention(lib, e, prefix_len=MOST + past, prefix_table=FAKE, **one) == BAD and "prefix_len" in hq.last_error()
+
+
+def test_work_past_64_bits(lib):  # noqa: F811
+    """KV heads x sequences x row tiles x units of keys whose product wraps to a small number: refused, as the same
+    with fewer keys is."""
+    kw = dict(c=cache(num_kv_heads=4096, page_size=256), num_q_heads=4096, total_q=1 << 24, num_seqs=32768, cu_q=FAKE,
+              table_cols=1 << 22, table_stride=1 << 22)
+    for max_q, keys in ((1 << 23, 1 << 12), (1 << 23, ((1 << 22) - 4) * 128), (1 << 23, ((1 << 22) - 3) * 128)):
+        # 2^15 row tiles, 2^27 pairs of a head and a sequence, 2^22 units: 2^64
+        assert attention(lib, max_q=max_q, max_len=keys, **kw) == UNSUP, keys

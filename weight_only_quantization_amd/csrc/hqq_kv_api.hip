@@ -188,8 +188,9 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
     const int64_t rows = (int64_t)l.max_q * a.per;
     p->kind[i] = row_kernel(rows, (int64_t)f.hkv * l.num_seqs, l.max_len);
     const int64_t tiles = row_tiles(rows, p->kind[i]), pairs = tiles * f.hkv * l.num_seqs;
-    KV_NEED(tiles <= 65535 && pairs * (l.max_len / hqq::kv::kUnitKeys + hqq::kv::kStartUnits + 1) <= (int64_t(1) << 30), HQQ_ERR_UNSUPPORTED,
-            "too many query rows and keys in a call");
+    // (pairs times units may pass 64 bits)
+    KV_NEED(tiles <= 65535 && pairs <= (int64_t(1) << 30) / (l.max_len / hqq::kv::kUnitKeys + hqq::kv::kStartUnits + 1),
+            HQQ_ERR_UNSUPPORTED, "too many query rows and keys in a call");
     if (p->kind[i] == kTile) {
       l.tiled = 1;
       split_keys(&l, pairs);
