@@ -434,7 +434,8 @@ size_t hqq_kv_page_bytes(int num_kv_heads, int head_dim, int nbits, int group_si
  *   k_echo, v_echo  out (both or neither) [n, num_kv_heads, head_dim] contiguous of dtype: the values
  *              the cache stands for (also of skipped tokens), rounded once: what a prompt's own attention
  *              takes to see the keys that later steps will see.
- * n = 0 does nothing.
+ * n = 0 does nothing.  One call takes fewer than 2^32 groups of 8 channels (n * num_kv_heads * head_dim / 8); more
+ * return HQQ_ERR_UNSUPPORTED, also from hqq_kv_read.
  */
 typedef struct hqq_kv_write_args {
   hqq_kv_cache cache;

@@ -2,7 +2,7 @@
 import pytest
 
 import weight_only_quantization_amd as hq
-from tests.test_kv_abi import BAD, FAKE, UNSUP, WS, attention, cache, lib  # noqa: F401
+from tests.test_kv_abi import BAD, FAKE, UNSUP, WS, attention, cache, lib, read, write  # noqa: F401
 
 MOST = (1 << 31) - (1 << 16) - 1
 
@@ -28,3 +28,17 @@ def test_work_past_64_bits(lib):  # noqa: F811
     for max_q, keys in ((1 << 23, 1 << 12), (1 << 23, ((1 << 22) - 4) * 128), (1 << 23, ((1 << 22) - 3) * 128)):
         # 2^15 row tiles, 2^27 pairs of a head and a sequence, 2^22 units: 2^64
         assert attention(lib, max_q=max_q, max_len=keys, **kw) == UNSUP, keys
+
+
+def test_launches_past_32_bits(lib):  # noqa: F811
+    """Calls with a launch of 2^32 threads or more in a dimension: refused before any kernel of the call runs."""
+    for call in (write, read):
+        assert call(lib, n=(1 << 28) - 4) == UNSUP and "tokens" in hq.last_error()              # 2 heads of 16 octets: 2^33
+        assert call(lib, n=1 << 28, c=cache(head_dim=64, num_kv_heads=2)) == UNSUP
+    many = dict(c=cache(num_kv_heads=1024), num_q_heads=1024, total_q=16384, num_seqs=16384, max_len=128)
+    assert attention(lib, **many) == UNSUP and "sequences" in hq.last_error()                   # 2^24 blocks
+    e = "hqq_kv_attention_shared"
+    rows = dict(num_q_heads=64, c=cache(num_kv_heads=64), total_q=1 << 20, num_seqs=1 << 10, max_len=128, prefix_table=FAKE)
+    assert attention(lib, e, prefix_len=128, **rows) == UNSUP and "query rows" in hq.last_error()  # a join of 2^26 rows
+    rows["total_q"] -= 1 << 10
+    assert attention(lib, e, prefix_len=128, **rows) == WS

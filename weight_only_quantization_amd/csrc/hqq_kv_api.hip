@@ -52,6 +52,9 @@ int check_cache(const hqq_kv_cache& c, Format* f) {
   return HQQ_OK;
 }
 
+// A launch dimension takes fewer than 2^32 threads.
+constexpr int64_t kThreads = (int64_t(1) << 32) - 512;
+
 bool known_type(int dtype) { return dtype == HQQ_KV_F16 || dtype == HQQ_KV_BF16; }
 
 // Most keys of a list.  The kernels count keys in 32 bits and look ahead of the last one: four steps of 256 keys in
@@ -207,6 +210,9 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
       }
     }
   }
+  // (blocks of 512 threads per KV head and sequence; four rows a block of 256 in the join)
+  KV_NEED((int64_t)f.hkv * x->num_seqs <= kThreads / 512 && (!p->join || x->total_q * a.hq <= kThreads / 64),
+          HQQ_ERR_UNSUPPORTED, "too many sequences or query rows in a call");
   if (!p->join) return HQQ_OK;
   // the lists' partial results, one after the other; the streams' segment lists behind them
   for (int i = 0; i < (a.joined ? 2 : 1); ++i) {
@@ -291,6 +297,8 @@ int hqq_kv_write(const hqq_kv_write_args* x) {
   if (st != HQQ_OK) return st;
   KV_NEED(known_type(x->dtype), HQQ_ERR_INVALID_ARGUMENT, "dtype must be HQQ_KV_F16 or HQQ_KV_BF16");
   KV_NEED(x->n >= 0 && x->n <= (int64_t(1) << 30) / x->cache.num_kv_heads, HQQ_ERR_INVALID_ARGUMENT, "n out of range");
+  KV_NEED((x->n + 3) * x->cache.num_kv_heads * (x->cache.head_dim / 8) <= kThreads, HQQ_ERR_UNSUPPORTED,
+          "too many tokens in a call");
   KV_NEED(!x->k_echo == !x->v_echo, HQQ_ERR_INVALID_ARGUMENT, "k_echo and v_echo go together");
   if (x->n == 0) return HQQ_OK;
   KV_NEED(x->k && x->v && x->slots, HQQ_ERR_INVALID_ARGUMENT, "k, v and slots must not be NULL");
@@ -315,6 +323,8 @@ int hqq_kv_read(const hqq_kv_read_args* x) {
   if (st != HQQ_OK) return st;
   KV_NEED(known_type(x->dtype), HQQ_ERR_INVALID_ARGUMENT, "dtype must be HQQ_KV_F16 or HQQ_KV_BF16");
   KV_NEED(x->n >= 0 && x->n <= (int64_t(1) << 30) / x->cache.num_kv_heads, HQQ_ERR_INVALID_ARGUMENT, "n out of range");
+  KV_NEED((x->n + 3) * x->cache.num_kv_heads * (x->cache.head_dim / 8) <= kThreads, HQQ_ERR_UNSUPPORTED,
+          "too many tokens in a call");
   if (x->n == 0) return HQQ_OK;
   KV_NEED(x->k && x->v && x->slots, HQQ_ERR_INVALID_ARGUMENT, "k, v and slots must not be NULL");
   KV_NEED(aligned16(x->k) && aligned16(x->v) && reinterpret_cast<uintptr_t>(x->slots) % 8 == 0, HQQ_ERR_INVALID_ARGUMENT,
