@@ -400,7 +400,9 @@ int hqq_gemv(const void* packed, const void* delta_fp16, const void* zero_fp16, 
  * written entry is finite):
  *   floor = fp16(min x), step = fp16(max(max x - floor, 0) * (1 / (2^nbits - 1))),
  *   code = clip(rint((x - floor) * (1 / step)), 0, 2^nbits - 1)  (0 where step = 0),
- * and stands for floor + code * step.
+ * and stands for floor + code * step.  The top code of a group that reaches 65504 may stand for a little more (65566
+ * at most): finite here and in bfloat16, but from 65520 on infinite where it is rounded to fp16, as the read-back and the echo
+ * do; the attention's fp16 outputs are held to +-65504.
  * Block layout (D = head_dim, b = nbits; in order, without gaps):
  *   K codes     [page_size][h: 4][i: D/32][j: 8]: channel 32 i + 8 h + j of the token; for b = 4
  *               the nibbles 0..7 of the 32-bit word (h, i) hold j = 0, 2, 4, 6, 1, 3, 5, 7

@@ -142,6 +142,14 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return as_u32(__builtin_convertvector(s, h2));
 }
 
+// fp16 outputs: the top code of a group that reaches 65504 may stand for up to 65566 (its step is rounded), so a mean
+// of values is held to +-65504; NaN stays.
+__device__ __forceinline__ uint32_t pack2_held(float a, float b) {
+  a = a > 65504.f ? 65504.f : a < -65504.f ? -65504.f : a;
+  b = b > 65504.f ? 65504.f : b < -65504.f ? -65504.f : b;
+  return pack2<false>(a, b);
+}
+
 template <bool BF16>
 __device__ __forceinline__ u32x4 pack8(const float (&x)[8]) {
   u32x4 w;

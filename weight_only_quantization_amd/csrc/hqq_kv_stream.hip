@@ -650,7 +650,7 @@ __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : 
 #pragma unroll
           for (int i = 0; i < VEC; i += 2) {
             const float y0 = x[j][i] * inv, y1 = x[j][i + 1] * inv;
-            *reinterpret_cast<uint32_t*>(to + j * VEC + i) = a.dtype == HQQ_KV_BF16 ? pack2<true>(y0, y1) : pack2<false>(y0, y1);
+            *reinterpret_cast<uint32_t*>(to + j * VEC + i) = a.dtype == HQQ_KV_BF16 ? pack2<true>(y0, y1) : pack2_held(y0, y1);
           }
         }
         if (a.lse && d0 == 0) a.lse[at] = sum != 0.f ? (rm + __log2f(sum)) * 0.69314718056f : -INFINITY;
@@ -784,7 +784,7 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int nt_own, int nt_
     if (a.dtype == HQQ_KV_BF16)
       w = u32x2{pack2<true>(o[0] * inv, o[1] * inv), pack2<true>(o[2] * inv, o[3] * inv)};
     else
-      w = u32x2{pack2<false>(o[0] * inv, o[1] * inv), pack2<false>(o[2] * inv, o[3] * inv)};
+      w = u32x2{pack2_held(o[0] * inv, o[1] * inv), pack2_held(o[2] * inv, o[3] * inv)};
     *reinterpret_cast<u32x2*>(reinterpret_cast<uint16_t*>(a.out) + row * D + d) = w;
     if (a.lse && lane == 0) a.lse[row] = sum != 0.f ? (top + __log2f(sum)) * 0.69314718056f : -INFINITY;
   }
