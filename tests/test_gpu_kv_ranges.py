@@ -77,3 +77,43 @@ def test_values_past_the_largest_half(d, bits, g, dtype):
             # u |o| + 2^-9 A, A at most 65504 + 131072
             assert (np.abs(o - held) <= u * 65566 + 2.0 ** -9 * 196608).all(), (key, tiles)
             assert np.abs(lse.cpu().numpy()).max() == 0
+
+
+@pytest.mark.parametrize("where", ["low weight", "hidden", "other group", "other group, small floors"])
+@pytest.mark.parametrize("seqs", [1, 130])
+@pytest.mark.parametrize("d,bits,g,dtype", [(128, 4, 64, "float16"), (128, 8, 32, "bfloat16"), (64, 4, 32, "bfloat16"), (64, 8, 32, "float16"),
+                                            (128, 8, 64, "float16"), (128, 4, 32, "float16")])
+def test_small_values_next_to_large_ones(d, bits, g, dtype, seqs, where):
+    """Steps of 2 and more next to steps of 1e-4 and less: in other keys (of low weight, or hidden from some rows) and in
+    another group of the same keys.  24 rows take two tiles of 16, or where that is more blocks than the GPU runs at
+    once, one of 32 (130 sequences)."""
+    hq, torch = base.lib()
+    say("kv mixed values", d, bits, g, dtype, seqs, where)
+    rng = np.random.default_rng(d + bits + seqs)
+    n, t, per = 45, 3, 8
+    k, v = (rng.normal(size=(n, d)).astype(np.float32) for _ in "kv")
+    v *= 1e-3
+    if where in ("low weight", "hidden"):
+        at = 7 if where == "low weight" else n - 1
+        v[at] *= 1e6
+        if where == "low weight":
+            k[at] = -8
+    else:
+        v[:, :g] *= 1e6
+        if where.endswith("floors"):
+            v[:, g:] = np.abs(v[:, g:]) + 3e-4
+    cache, (ks, vs) = one_head(hq, torch, bits, k, v, g=g, dtype=dtype)
+    steps = kp.quantise(kp.as_f32(kp.to(v, getattr(torch, dtype)))[:, None], bits, g)[1]
+    assert steps.max() > 2 and steps.min() < 1e-3
+    q = kp.to((1 + 0.5 * rng.normal(size=(t, per, d))).astype(np.float32), getattr(torch, dtype))
+    o, lse = attend(hq, torch, cache, q.cuda().repeat(seqs, 1, 1), [n] * seqs)
+    see = np.arange(n)[None] <= (n - t + np.arange(t))[:, None]
+    code, step, floor = kp.quantise(kp.as_f32(kp.to(v, getattr(torch, dtype)))[:, None], bits, g)
+    mags = kp.stands_for(code, step, np.abs(floor)).astype(np.float64)
+    args = (kp.as_f32(q).astype(np.float64), ks[:, None])
+    want, wl, _, _ = kp.attend(*args, vs[:, None], see, d ** -0.5)
+    _, _, mag, _ = kp.attend(*args, mags, see, d ** -0.5)
+    u = 2.0 ** -11 if dtype == "float16" else 2.0 ** -8
+    got = o.double().cpu().numpy().reshape(seqs, t, per, d)
+    err = np.abs(got - want) / (u * np.abs(want) + 2.0 ** -9 * mag + 1e-7)
+    assert err.max() <= 1, (err.max(), np.unravel_index(err.argmax(), err.shape))

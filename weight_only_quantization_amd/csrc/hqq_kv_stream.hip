@@ -478,24 +478,13 @@ __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : 
       st[i] = as_h2(__builtin_amdgcn_perm(y, x, 0x05040100));
       fm[i] = as_h2(__builtin_amdgcn_perm(y, x, 0x07060302));
     }
-    // 1024 s passes fp16 for steps of 64 and more: with a step of 2 or more (bit 14 of its half) this step of
-    // the stream takes its values 2^-8 smaller (a 4-bit step is at most 8734) and its weights, then
-    // held to 1, 2^8 larger
-    const bool wide = __any((as_u32(st[0]) | as_u32(st[1]) | as_u32(st[2]) | as_u32(st[3])) & 0x40004000u);
-    float slack = 5.f, lift = 0.f, drop = 1.f;
-    if (wide) {
-      slack = 0.f, lift = 8.f, drop = 0x1p-8f;
-      const h2 vs = {(_Float16)0x1p-8f, (_Float16)0x1p-8f};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) st[i] *= vs, fm[i] *= vs;
-    }
     h8 pf[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       float top = p[t][0];
 #pragma unroll
       for (int c = 1; c < 8; ++c) top = fmaxf(top, p[t][c]);
-      if (__any((top - mref[t]) * cs[t] > slack)) {
+      if (__any((top - mref[t]) * cs[t] > 5.f)) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         const float next = fmaxf(mref[t], top);
@@ -509,10 +498,10 @@ __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : 
       // exponents: one fused operation, whose constant's rounding is nothing until scores of 2^20; from there on the
       // difference first, so that the largest score's is 0 and none passes the largest number (a row without a key so
       // far, or of NaN, does not count)
-      const float c0 = fmaf(-mref[t], cs[t], lift);
+      const float c0 = -mref[t] * cs[t];
       if (__any(fabsf(c0) > 0x1p20f && mref[t] > kNoKey / 1e17f)) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) p[t][c] = fmaf(p[t][c] - mref[t], cs[t], lift);
+        for (int c = 0; c < 8; ++c) p[t][c] = (p[t][c] - mref[t]) * cs[t];
       } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c) p[t][c] = fmaf(p[t][c], cs[t], c0);
@@ -523,7 +512,7 @@ __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : 
         p[t][c] = exp2_(p[t][c]);
         sum += p[t][c];
       }
-      l[t] = fmaf(sum, drop, l[t]);
+      l[t] += sum;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         const f32x2 e = {p[t][2 * c], p[t][2 * c + 1]};
@@ -531,34 +520,61 @@ __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : 
         pf[t][2 * c] = r.x, pf[t][2 * c + 1] = r.y;
       }
     }
-    h2 s1024[4], s64[4];
     u32x4 flw;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      flw[i] = as_u32(fm[i]);
-      s1024[i] = st[i] * h2{(_Float16)-1024.f, (_Float16)-1024.f};
-      if (BITS == 4) s64[i] = st[i] * h2{(_Float16)-64.f, (_Float16)-64.f};
-    }
+    for (int i = 0; i < 4; ++i) flw[i] = as_u32(fm[i]);
     const h8 ff = __builtin_bit_cast(h8, flw);
 #pragma unroll
     for (int t = 0; t < NT; ++t) fl[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ff, pf[t], fl[t], 0, 0, 0);
+    // values: dword i of operand b of the lane's units, from two tokens' words of codes, steps, and -1024 and -64 steps
+    auto value = [&](uint32_t wx, uint32_t wy, int b, int i, h2 s, h2 s1024, h2 s64, u32x4& lo, u32x4& hi) {
+      const uint32_t c = __builtin_amdgcn_perm(wy, wx, pair_sel<G::kUnit>(2 * (i & 1), b));
+      const h2 x = as_h2(BITS == 4 ? (c & mk.lo) | mk.or1024 : c | mk.or1024);
+      lo[i] = as_u32(__builtin_elementwise_fma(x, s, s1024));
+      if (BITS == 4) {
+        const h2 y = as_h2((c & mk.hi) | mk.or64);
+        hi[i] = as_u32(__builtin_elementwise_fma(y, s, s64));
+      }
+    };
+    auto word = [&](int b, int i, int t) { return sv.c[i >> 1][((2 * (i & 1) + t) * G::kUnit + b) / 4]; };
+    const h2 n1024 = {(_Float16)-1024.f, (_Float16)-1024.f}, n64 = {(_Float16)-64.f, (_Float16)-64.f};
+    // 1024 s passes fp16 for steps of 64 and more, and c s where a group is wider than it: entries whose step is 2 or
+    // more (bit 14 of its half) are taken by themselves, 2^-8 smaller, and then the others without them, so that these keep
+    // their bits.  Few steps of the stream have any: the way holds no registers (opaque operands: else the compiler works out in front
+    // what both ways share).
+    if (__any((as_u32(st[0]) | as_u32(st[1]) | as_u32(st[2]) | as_u32(st[3])) & 0x40004000u)) {
+#pragma unroll
+      for (int b = 0; b < G::kUnit; ++b) {
+        u32x4 lo, hi;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t wx = word(b, i, 0), wy = word(b, i, 1), s = as_u32(st[i]);
+          asm volatile("" : "+v"(wx), "+v"(wy), "+v"(s));
+          const h2 large = as_h2((s >> 14 & 0x00010001u) * 0xffffu & s) * h2{(_Float16)0x1p-8f, (_Float16)0x1p-8f};
+          value(wx, wy, b, i, large, large * n1024, large * n64, lo, hi);
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+          const int j = BITS == 4 ? 2 * b : b;
+          o[t][j] += 256.f * __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, lo), pf[t], none, 0, 0, 0);
+          if (BITS == 4) o[t][j + 1] += 256.f * __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, hi), pf[t], none, 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) st[i] = as_h2(as_u32(st[i]) & ~((as_u32(st[i]) >> 14 & 0x00010001u) * 0xffffu));
+    }
+    h2 s1024[4], s64[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s1024[i] = st[i] * n1024;
+      if (BITS == 4) s64[i] = st[i] * n64;
+    }
 #pragma unroll
     for (int b = 0; b < G::kUnit; ++b) {
       u32x4 lo, hi;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        constexpr int U = G::kUnit;
-        const int t0 = 2 * (i & 1);  // first token of the pair within the tile
-        const uint32_t(&v)[G::kVW] = sv.c[i >> 1];
-        const uint32_t wx = v[(t0 * U + b) / 4], wy = v[((t0 + 1) * U + b) / 4];
-        const uint32_t c = __builtin_amdgcn_perm(wy, wx, pair_sel<U>(t0, b));
-        const h2 x = as_h2(BITS == 4 ? (c & mk.lo) | mk.or1024 : c | mk.or1024);
-        lo[i] = as_u32(__builtin_elementwise_fma(x, st[i], s1024[i]));
-        if (BITS == 4) {
-          const h2 y = as_h2((c & mk.hi) | mk.or64);
-          hi[i] = as_u32(__builtin_elementwise_fma(y, st[i], s64[i]));
-        }
-      }
+      for (int i = 0; i < 4; ++i) value(word(b, i, 0), word(b, i, 1), b, i, st[i], s1024[i], s64[i], lo, hi);
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         if (BITS == 4) {
