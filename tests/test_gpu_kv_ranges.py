@@ -117,3 +117,37 @@ def test_small_values_next_to_large_ones(d, bits, g, dtype, seqs, where):
     got = o.double().cpu().numpy().reshape(seqs, t, per, d)
     err = np.abs(got - want) / (u * np.abs(want) + 2.0 ** -9 * mag + 1e-7)
     assert err.max() <= 1, (err.max(), np.unravel_index(err.argmax(), err.shape))
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("what,seqs,t,per,n", [("a block a pair", 1, 1, 1, 1024), ("rows of 32", 130, 3, 8, 1024),
+                                               ("shares", 300, 1, 1, 5120), ("shares of rows of 32", 130, 3, 8, 5120),
+                                               ("tiles, keys split", 2, 80, 16, 16384), ("tiles", 136, 80, 1, 5120)])
+def test_flat_tail_under_one_key(what, seqs, t, per, n, bits):
+    """One key whose weight is 2^25 times each other one's, and whose value is 0: the output is the others' part alone, and
+    A with it, so every one of them has to be there to 2^-9."""
+    hq, torch = base.lib()
+    say("kv flat tail", what, bits)
+    rng = np.random.default_rng(n + bits)
+    d, page = 64, 256
+    k = np.zeros((2 * page, d), np.float32)
+    v = (30 + 9 * rng.normal(size=(2 * page, d))).astype(np.float32)
+    k[5], v[5] = 2.175, 0               # score 17.4 for queries of ones
+    cache, (ks, vs) = one_head(hq, torch, bits, k, v, page=page)
+    order = np.r_[0, np.ones(n // page - 1, np.int64)]
+    rows = t * per
+    cols = max(len(order), TILE_WORK // (rows * seqs * page) + 1 if rows > 64 else 0)
+    table = torch.full((1, cols), -1, dtype=torch.int32)
+    table[0, :len(order)] = torch.from_numpy(order)
+    q = torch.ones(seqs * t, per, d, dtype=torch.float16, device="cuda")
+    o, lse = hq.hqq_kv_attention(cache, q, table.cuda().expand(seqs, -1), torch.full((seqs,), n, dtype=torch.int32, device="cuda"),
+                                 causal=False, return_lse=True)
+    at = (order[:, None] * page + np.arange(page)).reshape(-1)
+    see, one = np.ones((1, n), bool), np.ones((1, 1, d))
+    code, step, floor = kp.quantise(kp.as_f32(kp.to(v, torch.float16))[:, None], bits, 64)
+    mags = kp.stands_for(code, step, np.abs(floor)).astype(np.float64)
+    want, wl, _, _ = kp.attend(one, ks[at][:, None], vs[at][:, None], see, d ** -0.5)
+    _, _, mag, _ = kp.attend(one, ks[at][:, None], mags[at], see, d ** -0.5)
+    err = np.abs(o.double().cpu().numpy() - want) / (2.0 ** -11 * np.abs(want) + 2.0 ** -9 * mag + 1e-7)
+    assert err.max() <= 1, err.max()
+    assert np.abs(lse.double().cpu().numpy() - wl).max() <= 1e-5 * 20

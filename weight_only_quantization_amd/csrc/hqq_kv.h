@@ -98,6 +98,10 @@ hipError_t launch_kv_join(const AttnArgs& a, int D, int nt_own, int nt_prefix, h
 constexpr int kUnitKeys = 128;  // keys of the stream's unit of work: a step of each of a block's four waves
 constexpr uint32_t kStartUnits = 3;  // units that beginning a (sequence, row tile, KV head) counts for
 
+// Softmax weights are taken 2^kLift larger than exp(score - running maximum), in the sums too: a score passes the maximum by
+// 2^5 at most, so they stay under 2^15 in fp16, which then keeps 11 bits of weights down to 2^-24 of the maximum's and holds
+// some down to 2^-35 (without it 2^-14 and 2^-25: a long flat tail under one key counted in the sum but not in the products).
+constexpr float kLift = 10.f;
 constexpr float kNoKey = -1e30f;  // running maximum before any key (finite: differences of two stay numbers)
 
 // (by value: a bit cast of a vector's element in place takes the vector's first one)

@@ -14,7 +14,7 @@
 //   values  O^T[channel][row] += (c s)[channel][key] p[key][row]: a lane's 8 scores are its operand as
 //           they are (keys keep their order inside the step).  c s is one fp16 rounding,
 //           fma(1024 + c, s, -1024 s); the floors enter as one more product, sum_j p_j m_j.
-//           p is rounded to fp16 (2^-12 relative, independent per key).
+//           p is rounded to fp16 (2^-11 relative at most, from 2^-24 of the maximum's weight down 2^-35 of that; kLift).
 // Next keys are loaded as soon as this step's scores are done, the next values after this
 // step's product, each into the registers just read: few registers, so three waves a SIMD cover the
 // memory's latency (two with both steps' registers held: 3.2 TB/s at 16 sequences of 16384-32768 keys,
@@ -498,10 +498,10 @@ __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : 
       // exponents: one fused operation, whose constant's rounding is nothing until scores of 2^20; from there on the
       // difference first, so that the largest score's is 0 and none passes the largest number (a row without a key so
       // far, or of NaN, does not count)
-      const float c0 = -mref[t] * cs[t];
+      const float c0 = fmaf(-mref[t], cs[t], kLift);
       if (__any(fabsf(c0) > 0x1p20f && mref[t] > kNoKey / 1e17f)) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) p[t][c] = (p[t][c] - mref[t]) * cs[t];
+        for (int c = 0; c < 8; ++c) p[t][c] = fmaf(p[t][c] - mref[t], cs[t], kLift);
       } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c) p[t][c] = fmaf(p[t][c], cs[t], c0);
@@ -608,7 +608,7 @@ __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : 
   }
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    mref[t] *= cs[t];  // in units of the exponent from here on
+    mref[t] = fmaf(mref[t], cs[t], -kLift);  // what the weights are over, in units of the exponent, from here on
     l[t] += __shfl_xor(l[t], 16);
     l[t] += __shfl_xor(l[t], 32);
     if (h == 0) sh_m[wave][16 * t + n] = mref[t], sh_l[wave][16 * t + n] = l[t];

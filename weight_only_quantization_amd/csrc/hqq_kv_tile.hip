@@ -4,7 +4,7 @@
 // for 256 rows, k = fp16(m + c s) with one rounding, into LDS, and both products run on the matrix unit:
 //   S^T[key][row] = K Q^T,  o^T[channel][row] += V^T P^T,
 // so a lane's scores (16 of one row to 32 keys) are its operand of the second product as they are: V^T is
-// kept in LDS with its keys in that order.  p is rounded to fp16; all sums are fp32.
+// kept in LDS with its keys in that order.  p is rounded to fp16 (kLift); all sums are fp32.
 // Eight waves, 32 rows each; all of them unpack 1/8 of the next tile next to this one's products (two
 // buffers of K and V, one barrier a tile).  Codes, step and floor become values in packed fp16:
 // (1024 + c) - 1024 is exact, fma(c, s, m) rounds once.
@@ -296,12 +296,12 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
         for (int d = 0; d < DT; ++d) o[d] *= f;
       }
       // (exponents as in the stream kernel)
-      const float c0 = -mref * cs;
+      const float c0 = fmaf(-mref, cs, kLift);
       if (__any(fabsf(c0) > 0x1p20f && mref > kNoKey / 1e17f)) {
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) s[c][i] = (s[c][i] - mref) * cs;
+          for (int i = 0; i < 16; ++i) s[c][i] = fmaf(s[c][i] - mref, cs, kLift);
       } else {
 #pragma unroll
         for (int c = 0; c < 2; ++c)
@@ -367,7 +367,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
 
   // ---- output: row x = 32 d + 8 a + 4 h + c of the tile's channels is element 4 a + c of o[d]; the lane holds the
   // units 8 (a % 2) + 4 h + c whole, channel 2 d + a / 2 of each
-  mref *= cs;  // in units of the exponent from here on
+  mref = fmaf(mref, cs, -kLift);  // what the weights are over, in units of the exponent, from here on
   l += __shfl_xor(l, 32);
   // a query with an infinity or NaN gives NaN wherever it sees a key (it entered the products as 0: the fp16 mode above
   // does not hand a NaN on)
