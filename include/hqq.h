@@ -483,7 +483,8 @@ int hqq_kv_read(const hqq_kv_read_args* args);
  *              to the table.
  *   causal     1: query token t of T stands at position seq_len - T + t and sees the keys up to it; 0: all.
  *   scale      finite, > 0.
- *   out        out [total_q, num_q_heads, head_dim] contiguous of dtype.  A row that sees no key is 0.
+ *   out        out [total_q, num_q_heads, head_dim] contiguous of dtype.  A row that sees no key is 0; one
+ *              whose query holds NaN or an infinity is NaN where it sees any.
  *   lse        out (nullable) float [total_q, num_q_heads]: log of the sum of exp(scale * q.k); -inf for no key.
  *   workspace  at least hqq_kv_attention_workspace_bytes(args) bytes (may be 0), 16-byte aligned.
  * Scores, maximum, sums and the join of key ranges are fp32; a code enters its product exactly

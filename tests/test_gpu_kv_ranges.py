@@ -151,3 +151,31 @@ def test_flat_tail_under_one_key(what, seqs, t, per, n, bits):
     err = np.abs(o.double().cpu().numpy() - want) / (2.0 ** -11 * np.abs(want) + 2.0 ** -9 * mag + 1e-7)
     assert err.max() <= 1, err.max()
     assert np.abs(lse.double().cpu().numpy() - wl).max() <= 1e-5 * 20
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("bits", [4, 8])
+@pytest.mark.parametrize("seqs", [1, 130])
+def test_streamed_rows_that_are_not_finite(seqs, bits, dtype):
+    """A streamed query row with NaN or an infinity of either sign is NaN where it sees a key, 0 where it sees none, and touches no
+    other row: keys of either sign in the channel, with codes 0 and the largest."""
+    hq, torch = base.lib()
+    say("kv streamed infinities", seqs, bits, dtype)
+    rng = np.random.default_rng(5)
+    n, t, per, d = 3, 4, 8, 64
+    k, v = (rng.normal(size=(n, d)).astype(np.float32) for _ in "kv")
+    k[:, :32] = 2 + rng.uniform(size=(n, 32))       # floors and codes of one sign: every product with an infinity is infinite
+    k[:, 7] = 3.5
+    cache, _ = one_head(hq, torch, bits, k, v, g=32, dtype=dtype)
+    q = kp.to(rng.normal(size=(t, per, d)).astype(np.float32), getattr(torch, dtype)).cuda().repeat(seqs, 1, 1)
+    o, lse = attend(hq, torch, cache, q, [n] * seqs)
+    odd = q.clone()
+    for head, channel, x in ((0, 7, -math.inf), (1, 7, math.inf), (2, 7, math.nan), (3, 50, -math.inf), (4, 50, math.inf)):
+        odd[t - 1::t, head, channel] = x
+        odd[0::t, head, channel] = x                # (before the sequence's first key)
+    o2, lse2 = attend(hq, torch, cache, odd, [n] * seqs)
+    assert torch.isnan(o2[t - 1::t, :5]).all() and torch.isnan(lse2[t - 1::t, :5]).all()
+    assert not o2[0::t].any() and (lse2[0::t] == -math.inf).all()
+    for x, y in ((o2, o), (lse2, lse)):
+        x[t - 1::t, :5] = y[t - 1::t, :5]
+        assert torch.equal(x, y)

@@ -342,6 +342,9 @@ __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : 
     uint32_t top = max((uint32_t)most.x, (uint32_t)most.y);
     top = max(top, (uint32_t)__shfl_xor((int)top, 16));
     top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+    // a row with an infinity gives NaN wherever it sees a key, as one with NaN does (infinite products of one sign alone
+    // would look like a row without keys)
+    if (top >= (a.dtype == HQQ_KV_BF16 ? 0x7f80u : 0x7c00u)) w[0][0] = 0x7fff7fffu;
     // 2^e takes it to [2^14, 2^15) (fp16 rows: e up to 15): q / 16 then keeps fp16's precision for 2^13
     // below it, and a bfloat16 row of any size keeps its bits
     int e = 0;
