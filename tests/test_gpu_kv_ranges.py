@@ -179,3 +179,24 @@ def test_streamed_rows_that_are_not_finite(seqs, bits, dtype):
     for x, y in ((o2, o), (lse2, lse)):
         x[t - 1::t, :5] = y[t - 1::t, :5]
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("scale_of_others", [1e-2, 8.0, 3e4])
+@pytest.mark.parametrize("what,seqs,t,per", [("rows of 16", 1, 1, 8), ("rows of 32", 130, 3, 8), ("tiles", 2, 30, 8)])
+def test_rows_do_not_depend_on_their_neighbours(what, seqs, t, per, scale_of_others):
+    """Other queries in half of the rows (flat, peaked, or with scores past 2^20): the other half keeps its bits."""
+    hq, torch = base.lib()
+    say("kv neighbours", what, scale_of_others)
+    rng = np.random.default_rng(9)
+    n, d = 400, 128
+    k, v = (rng.normal(size=(n, d)).astype(np.float32) for _ in "kv")
+    cache, _ = one_head(hq, torch, 4, k * 30, v)
+    q = kp.to((0.05 * rng.normal(size=(seqs * t, per, d))).astype(np.float32), torch.float16).cuda()
+    o, lse = attend(hq, torch, cache, q, [n] * seqs, tiles=what == "tiles")
+    odd = q.clone()
+    odd[:, 1::2] = kp.to((scale_of_others * rng.normal(size=(seqs * t, per // 2, d))).astype(np.float32), torch.float16).cuda()
+    o2, lse2 = attend(hq, torch, cache, odd, [n] * seqs, tiles=what == "tiles")
+    finite = torch.isfinite(odd).all(-1)            # (the largest scale has infinite queries among them)
+    assert torch.equal(torch.isfinite(o2).all(-1), finite) and torch.equal(torch.isnan(o2).all(-1), ~finite)
+    assert not torch.equal(o2, o)
+    assert torch.equal(o2[:, ::2], o[:, ::2]) and torch.equal(lse2[:, ::2], lse[:, ::2])

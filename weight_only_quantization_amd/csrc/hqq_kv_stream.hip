@@ -490,7 +490,7 @@ __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : 
       if (__any((top - mref[t]) * cs[t] > 5.f)) {
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
-        const float next = fmaxf(mref[t], top);
+        const float next = (top - mref[t]) * cs[t] > 5.f ? top : mref[t];  // (each row by its own scores alone)
         const float f = exp2_((mref[t] - next) * cs[t]);
         mref[t] = next;
         l[t] *= f;
@@ -502,9 +502,10 @@ __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : 
       // difference first, so that the largest score's is 0 and none passes the largest number (a row without a key so
       // far, or of NaN, does not count)
       const float c0 = fmaf(-mref[t], cs[t], kLift);
-      if (__any(fabsf(c0) > 0x1p20f && mref[t] > kNoKey / 1e17f)) {
+      const bool far = fabsf(c0) > 0x1p20f && mref[t] > kNoKey / 1e17f;
+      if (__builtin_expect(__any(far), 0)) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) p[t][c] = fmaf(p[t][c] - mref[t], cs[t], kLift);
+        for (int c = 0; c < 8; ++c) p[t][c] = far ? fmaf(p[t][c] - mref[t], cs[t], kLift) : fmaf(p[t][c], cs[t], c0);
       } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c) p[t][c] = fmaf(p[t][c], cs[t], c0);

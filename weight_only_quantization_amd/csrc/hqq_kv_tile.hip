@@ -297,11 +297,13 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
       }
       // (exponents as in the stream kernel)
       const float c0 = fmaf(-mref, cs, kLift);
-      if (__any(fabsf(c0) > 0x1p20f && mref > kNoKey / 1e17f)) {
+      const bool far = fabsf(c0) > 0x1p20f && mref > kNoKey / 1e17f;
+      if (__builtin_expect(__any(far), 0)) {
+        const float less = far ? mref : 0.f, plus = far ? kLift : c0;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) s[c][i] = fmaf(s[c][i] - mref, cs, kLift);
+          for (int i = 0; i < 16; ++i) s[c][i] = fmaf(s[c][i] - less, cs, plus);
       } else {
 #pragma unroll
         for (int c = 0; c < 2; ++c)
