@@ -90,6 +90,10 @@ hipError_t launch_kv_read(const ReadArgs& a, int D, int bits, int gs, int dtype,
 // Rows of up to 16 * nt per block, streamed keys; nt 1 or 2.  stream_blocks: the grid that fills the GPU.
 int stream_blocks(int D, int gs, int nt);
 hipError_t launch_kv_stream(const AttnArgs& a, int D, int bits, int gs, int nt, hipStream_t st);
+// How the stream takes the lists of a launch: shares of the work for each block (loads through the caches, or past them), or a
+// block of eight or four waves a pair.
+enum StreamMode { kShares, kSharesOnce, kWhole8, kWhole4 };
+StreamMode stream_mode(const AttnArgs& a, int nt);
 // Tiles of 256 rows of list `which`.
 hipError_t launch_kv_tile(const AttnArgs& a, int which, int D, int bits, int gs, hipStream_t st);
 // Joins the partial results of every row; nt: of the stream's lists.
@@ -196,3 +200,8 @@ __device__ __forceinline__ uint8_t* slot_block(const Format& f, int64_t slot, in
 
 }  // namespace kv
 }  // namespace hqq
+
+// Which kernels a call of hqq_kv_attention(_shared) with these arguments launches, for the tests: per list (own keys, prefix)
+// the rows of a block (16, 32 or 256; 0 without the list), the stream's mode (hqq::kv::StreamMode; -1 in tiles) and the tiles' key
+// splits; then whether a join follows.  Nothing is read or launched.  Returns the call's status.
+extern "C" int hqq_kv_attention_way(const hqq_kv_attention_args* args, int32_t way[7]);

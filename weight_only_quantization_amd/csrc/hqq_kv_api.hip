@@ -235,6 +235,26 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
   return HQQ_OK;
 }
 
+// The launches in front of the join, in order; launch(i) with the arguments set for list i (and the ones after it that share the
+// launch).  Tiles of a prefix first (the longest work), then the streams: one launch where both lists stream alike.
+template <typename F>
+hipError_t each_launch(Plan* p, const hqq_kv_cache& c, F launch) {
+  AttnArgs& a = p->a;
+  const int lists = a.joined ? 2 : 1;
+  hipError_t e = hipSuccess;
+  for (int i = lists - 1; i >= 0 && e == hipSuccess; --i)
+    if (p->kind[i] == kTile) e = launch(i);
+  for (int i = 0; i < lists && e == hipSuccess; ++i) {
+    if (p->kind[i] == kTile) continue;
+    a.first_list = i;
+    a.lists = i == 0 && lists == 2 && !a.list[0].tiled && p->kind[1] == p->kind[0] ? 2 : 1;
+    a.blocks = a.list[i].tiled ? 0 : stream_grid(*p, c, i, a.lists);
+    e = launch(i);
+    i += a.lists - 1;
+  }
+  return e;
+}
+
 int run_attention(const hqq_kv_attention_args* x) {
   Plan p;
   const int st = plan_attention(x, false, &p);
@@ -264,19 +284,11 @@ int run_attention(const hqq_kv_attention_args* x) {
     }
   }
   hipStream_t stream = static_cast<hipStream_t>(x->stream);
-  const int D = c.head_dim, bits = c.nbits, gs = c.group_size, lists = a.joined ? 2 : 1;
-  hipError_t e = hipSuccess;
-  // tiles of a prefix first (the longest work), then the streams: one launch where both lists stream alike
-  for (int i = lists - 1; i >= 0 && e == hipSuccess; --i)
-    if (p.kind[i] == kTile) e = hqq::kv::launch_kv_tile(a, i, D, bits, gs, stream);
-  for (int i = 0; i < lists && e == hipSuccess; ++i) {
-    if (p.kind[i] == kTile) continue;
-    a.first_list = i;
-    a.lists = i == 0 && lists == 2 && !a.list[0].tiled && p.kind[1] == p.kind[0] ? 2 : 1;
-    a.blocks = a.list[i].tiled ? 0 : stream_grid(p, c, i, a.lists);
-    e = hqq::kv::launch_kv_stream(a, D, bits, gs, nt_of(p.kind[i]), stream);
-    i += a.lists - 1;
-  }
+  const int D = c.head_dim, bits = c.nbits, gs = c.group_size;
+  hipError_t e = each_launch(&p, c, [&](int i) {
+    return p.kind[i] == kTile ? hqq::kv::launch_kv_tile(a, i, D, bits, gs, stream)
+                              : hqq::kv::launch_kv_stream(a, D, bits, gs, nt_of(p.kind[i]), stream);
+  });
   if (e == hipSuccess && p.join) e = hqq::kv::launch_kv_join(a, D, nt_of(p.kind[0]), nt_of(p.kind[1]), stream);
   return device_status(e);
 }
@@ -350,6 +362,23 @@ int hqq_kv_attention(const hqq_kv_attention_args* x) {
 int hqq_kv_attention_shared(const hqq_kv_attention_args* x) {
   KV_NEED(x, HQQ_ERR_INVALID_ARGUMENT, "args must not be NULL");
   return run_attention(x);
+}
+
+int hqq_kv_attention_way(const hqq_kv_attention_args* x, int32_t way[7]) {
+  Plan p;
+  for (int i = 0; i < 7; ++i) way[i] = 0;
+  const int st = plan_attention(x, false, &p);
+  if (st != HQQ_OK || x->total_q == 0 || p.a.list[0].max_q == 0) return st;
+  (void)each_launch(&p, x->cache, [&](int i) {
+    for (int l = i; l < i + (p.kind[i] == kTile ? 1 : p.a.lists); ++l) {
+      way[3 * l] = p.kind[l] == kTile ? 256 : 16 * nt_of(p.kind[l]);
+      way[3 * l + 1] = p.kind[l] == kTile ? -1 : hqq::kv::stream_mode(p.a, nt_of(p.kind[l]));
+      way[3 * l + 2] = p.kind[l] == kTile ? p.a.list[l].nsplit : 1;
+    }
+    return hipSuccess;
+  });
+  way[6] = p.join;
+  return HQQ_OK;
 }
 
 }  // extern "C"

@@ -132,12 +132,11 @@ __device__ __forceinline__ uint32_t tiles_of(const AttnArgs& a, int tq) {
 __device__ __forceinline__ uint32_t units_of(int len) { return kStartUnits + (uint32_t)(len + kUnitKeys - 1) / kUnitKeys; }
 
 // PAIR: pages of at least 32 tokens, so a step's two tiles share a page (one lookup, one address).
-// MODE: kShares as above, four waves a block; or a block takes a whole pair with eight waves or with four: what short
+// MODE (StreamMode): shares as above, four waves a block; or a block takes a whole pair with eight waves or with four: what short
 // sequences want, with no schedule to work out and nothing to join.
 // kSharesOnce: shares of pairs whose rows are one tile each, so that no other block reads the keys: their loads pass the
 // caches by (16 sequences of 16384-32768 keys, 64 heads on 8: 88 us, 95 with ordinary loads; where several tiles of rows read the
 // keys the caches serve the later ones: 104 rows on 5834 keys in 8 bits 27 us, 34 past the caches).
-enum { kShares, kSharesOnce, kWhole8, kWhole4 };
 template <int D, int BITS, int GS, int NT, bool PAIR, int MODE>
 __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : stream_waves(D, GS, NT)) void k_kv_stream(
     AttnArgs a) {
@@ -810,24 +809,19 @@ __global__ __launch_bounds__(256) void k_kv_join(AttnArgs a, int nt_own, int nt_
   }
 }
 
+int tiles_in(const AttnArgs& a, const KeyList& l, int nt) {
+  return (int)(((int64_t)l.max_q * a.per + 16 * nt - 1) / (16 * nt));
+}
+
 template <int D, int BITS, int GS, int NT, bool PAIR>
 void stream_nt(const AttnArgs& a, hipStream_t st) {
-  auto tiles_in = [&](const KeyList& l) { return (int)(((int64_t)l.max_q * a.per + 16 * NT - 1) / (16 * NT)); };
   const KeyList& l = a.list[a.first_list];
-  const int tiles = tiles_in(l);
-  if (a.blocks) {
-    if (tiles == 1 && (a.lists == 1 || tiles_in(a.list[1]) == 1))
-      k_kv_stream<D, BITS, GS, NT, PAIR, kSharesOnce><<<a.blocks, 256, 0, st>>>(a);
-    else
-      k_kv_stream<D, BITS, GS, NT, PAIR, kShares><<<a.blocks, 256, 0, st>>>(a);
-  } else {
-    const dim3 grid(a.f.hkv * l.num_seqs, tiles);
-    // A CU holds one block of eight waves; more blocks than CUs would take it in turns, blocks of four run side by side
-    // (64 sequences of 1000 keys, 64 heads on 8: 23.5 us with eight waves, 18.9 with four).
-    if ((int64_t)grid.x * tiles <= 256)
-      k_kv_stream<D, BITS, GS, NT, PAIR, kWhole8><<<grid, 512, 0, st>>>(a);
-    else
-      k_kv_stream<D, BITS, GS, NT, PAIR, kWhole4><<<grid, 256, 0, st>>>(a);
+  const dim3 grid(a.f.hkv * l.num_seqs, tiles_in(a, l, NT));
+  switch (stream_mode(a, NT)) {
+    case kSharesOnce: k_kv_stream<D, BITS, GS, NT, PAIR, kSharesOnce><<<a.blocks, 256, 0, st>>>(a); break;
+    case kShares: k_kv_stream<D, BITS, GS, NT, PAIR, kShares><<<a.blocks, 256, 0, st>>>(a); break;
+    case kWhole8: k_kv_stream<D, BITS, GS, NT, PAIR, kWhole8><<<grid, 512, 0, st>>>(a); break;
+    case kWhole4: k_kv_stream<D, BITS, GS, NT, PAIR, kWhole4><<<grid, 256, 0, st>>>(a); break;
   }
 }
 
@@ -842,6 +836,15 @@ hipError_t stream_t(const AttnArgs& a, int nt, hipStream_t st) {
 }
 
 }  // namespace
+
+StreamMode stream_mode(const AttnArgs& a, int nt) {
+  const KeyList& l = a.list[a.first_list];
+  const int tiles = tiles_in(a, l, nt);
+  if (a.blocks) return tiles == 1 && (a.lists == 1 || tiles_in(a, a.list[1], nt) == 1) ? kSharesOnce : kShares;
+  // A CU holds one block of eight waves; more blocks than CUs would take it in turns, blocks of four run side by side
+  // (64 sequences of 1000 keys, 64 heads on 8: 23.5 us with eight waves, 18.9 with four).
+  return (int64_t)a.f.hkv * l.num_seqs * tiles <= 256 ? kWhole8 : kWhole4;
+}
 
 int stream_blocks(int D, int gs, int nt) { return 256 * stream_waves(D, gs, nt); }
 
