@@ -42,3 +42,13 @@ def test_launches_past_32_bits(lib):  # noqa: F811
     assert attention(lib, e, prefix_len=128, **rows) == UNSUP and "query rows" in hq.last_error()  # a join of 2^26 rows
     rows["total_q"] -= 1 << 10
     assert attention(lib, e, prefix_len=128, **rows) == WS
+
+
+@pytest.mark.parametrize("name", ["seq_lens", "page_table", "cu_q", "prefix_table", "lse"])
+def test_misaligned_words(lib, name):  # noqa: F811
+    """Lists of 32-bit words off their alignment: scalar loads would read others in their place."""
+    kw = dict(max_len=128, cu_q=FAKE, max_q=2, prefix_table=FAKE, prefix_len=64, lse=FAKE)
+    assert attention(lib, "hqq_kv_attention_shared", **kw) == WS
+    for off in (1, 2, 3):
+        kw[name] = FAKE + off
+        assert attention(lib, "hqq_kv_attention_shared", **kw) == BAD and "aligned" in hq.last_error()

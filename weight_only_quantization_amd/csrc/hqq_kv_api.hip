@@ -12,6 +12,7 @@ using hqq::kv::AttnArgs;
 using hqq::kv::Format;
 using hqq::kv::KeyList;
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int device_status(hipError_t e) {
@@ -269,6 +270,9 @@ int run_attention(const hqq_kv_attention_args* x) {
   KV_NEED(x->seq_lens, HQQ_ERR_INVALID_ARGUMENT, "seq_lens must not be NULL");
   KV_NEED(x->page_table || x->table_cols == 0, HQQ_ERR_INVALID_ARGUMENT, "page_table must not be NULL");
   KV_NEED(!a.joined || x->prefix_table, HQQ_ERR_INVALID_ARGUMENT, "prefix_table must not be NULL");
+  // (scalar loads drop the low address bits)
+  KV_NEED(aligned4(x->seq_lens) && aligned4(x->page_table) && aligned4(x->cu_q) && aligned4(x->prefix_table) && aligned4(x->lse),
+          HQQ_ERR_INVALID_ARGUMENT, "seq_lens, the page tables, cu_q and lse must be 4-byte aligned");
   if (p.workspace) {
     KV_NEED(x->workspace && x->workspace_bytes >= p.workspace, HQQ_ERR_WORKSPACE,
             "workspace missing or smaller than hqq_kv_attention_workspace_bytes");
