@@ -267,6 +267,15 @@ def size_of(hq, ways, torch, s, prefix):
     return sizes[-1]
 
 
+def test_bounds_past_the_call(ways):
+    """Bounds on query tokens and lengths that are larger than the call itself (a program's fixed ones) are bounds too."""
+    hq, torch = base.lib()
+    s = base.Scene(hq, torch, kp.Fmt(2, 128, 4, 64, 32), [40, 7, 90], [3, 1, 2], 4, "float16", seed=5)
+    o, lse = base.attend(hq, torch, s)
+    o2, lse2 = base.attend(hq, torch, s, max_q=64, max_len=1 << 20)
+    assert torch.equal(o2, o) and torch.equal(lse2, lse)
+
+
 def test_graph_of_shares(ways):
     """Shares with a join in a graph, lengths changed between replays: each against the eager call."""
     hq, torch = base.lib()

@@ -291,7 +291,7 @@ def hqq_kv_attention(cache: KVCache, q, page_table, seq_lens, scale=None, cu_q=N
         if _indices(cu_q, "cu_q", torch.int32, 1)[0] != seqs + 1:
             raise ValueError("cu_q must be [num_seqs + 1]")
         _there(cu_q, "cu_q")
-        if max_q is None:
+        if max_q is None or max_q > total_q:
             max_q = total_q
     entry, prefix_at, prefix_len = "hqq_kv_attention", 0, 0
     if _prefix is not None:
