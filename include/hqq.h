@@ -482,7 +482,7 @@ int hqq_kv_read(const hqq_kv_read_args* args);
  *              0 for none.  Limited to max_len (host; a bound the caller knows, at most 2^31 - 2^16 - 1, as prefix_len) and
  *              to the table.
  *   causal     1: query token t of T stands at position seq_len - T + t and sees the keys up to it; 0: all.
- *   scale      finite, > 0.
+ *   scale      finite, > 0; scale * q.k is taken to lie within +-1e30.
  *   out        out [total_q, num_q_heads, head_dim] contiguous of dtype.  A row that sees no key is 0; one
  *              whose query holds NaN or an infinity is NaN where it sees any.
  *   lse        out (nullable) float [total_q, num_q_heads]: log of the sum of exp(scale * q.k); -inf for no key.

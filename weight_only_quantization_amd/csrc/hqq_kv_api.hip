@@ -78,11 +78,12 @@ struct Plan {
 // sequences of 2001 keys, 5 tokens, 32 heads on 8: 19.6 us with 16 rows, 22.7 with 32; 12 tokens: 35 and 24).
 // More than 64 rows take tiles where there is work enough: a block of tiles takes 10 us to begin and end and 5 us
 // per 128 keys, while streams spread few keys over more and shorter blocks.  Time of the call streamed and in tiles by the
-// millions of pairs of a row and a key of a KV head: 0.36 (298 rows, 306 keys) 13 and 24 us, 3.0 (1290 rows) 14 and 28, 6.9
-// (1856 rows) 13 and 27, 12.5 (2160 rows, 721 keys) 19 and 34, 12.6 (70 rows, 5623 keys, 32 heads) 29 and 28, 17.5 (1180 rows on a
-// prefix of 3706) 42 and 52, 24 (6461 rows, 925 keys) 22 and 39; past that by the sizes: 31 (240 rows, 16379 keys)
-// 64 and 55, 38 (1414 rows, 3399 keys) 79 and 52, 36 (5516 rows) 40 and 59.
-constexpr int64_t kStreamWork = int64_t(3) << 23, kStreamRows = 1 << 16;  // (rows: the grid's bound, 65535 row tiles)
+// millions of pairs of a row and a key, over all KV heads and sequences: 0.36 (298 rows, 306 keys) 13 and 24 us, 3.0 (1290
+// rows) 14 and 28, 6.9 (1856 rows) 13 and 27, 12.5 (2160 rows, 721 keys) 19 and 34, 12.6 (70 rows, 5623 keys, 32 heads) 29 and 28,
+// 17.5 (1180 rows on a prefix of 3706) 42 and 52, 24 (6461 rows, 925 keys) 22 and 39.  Past the threshold it goes by the sizes, and
+// tiles are taken where streams were the faster too: 31 (240 rows, 16379 keys) 64 and 55, 38 (1414 rows, 3399 keys) 79 and 52, but
+// 36 (5516 rows) 40 and 59.  More than 2^16 rows take tiles whatever the keys (the threshold is at 384 keys there).
+constexpr int64_t kStreamWork = int64_t(3) << 23, kStreamRows = 1 << 16;
 int row_kernel(int64_t rows, int64_t lists, int64_t keys) {
   if (rows > 64 && (rows > kStreamRows || (keys > 0 ? keys : 1) * lists > kStreamWork / rows)) return kTile;
   return rows <= 16 || (rows + 15) / 16 * lists <= 256 ? kStream16 : kStream32;

@@ -3,23 +3,26 @@
 //   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q.k_j - max),  k = m + c s,  v = m + c s per group.
 //
 // A wave owns 16 * NT rows (the query tokens and heads that share a KV head) and walks its keys in
-// steps of 32, without LDS: the cache is stored so that each lane's wide loads are operands of the
+// steps of 32, registers only: the cache is stored so that each lane's wide loads are operands of the
 // matrix unit.
 //   scores  S^T[key][row] = sum_g s_jg (sum_{d in g} c_jd q_d) + m_jg (sum_{d in g} q_d): the codes go
 //           in exactly, as fp16 subnormals c 2^-24 (a mask of the word is the operand; the other
 //           nibble of a byte is 16 c, its q carries 1/16), step and floor apply to the fp32 sums.
-//   softmax one pass, running maximum and sum in fp32; a lane holds 8 keys of one row.  The maximum is
-//           raised (and the sums rescaled) only when a score passes it by 2^5, so the cross-lane
+//   softmax one pass, running maximum and sum in fp32; a lane holds 8 keys of one row.  A row's maximum is
+//           raised (and its sums rescaled) only when a score passes it by 2^5, so the cross-lane
 //           reduction is rare; the weights stay within fp16.
 //   values  O^T[channel][row] += (c s)[channel][key] p[key][row]: a lane's 8 scores are its operand as
 //           they are (keys keep their order inside the step).  c s is one fp16 rounding,
-//           fma(1024 + c, s, -1024 s); the floors enter as one more product, sum_j p_j m_j.
+//           fma(1024 + c, s, -1024 s), 2^-8 smaller for steps of 2 and more; the floors enter as one more product, sum_j p_j m_j.
 //           p is rounded to fp16 (2^-11 relative at most, from 2^-24 of the maximum's weight down 2^-35 of that; kLift).
+//           These two roundings are what the matrix unit's fp16 operands cost: 5.2e-4 to 5.8e-4 of the output (2-norm) with the fp16
+//           output's own 2.1e-4 (fp32 products run at a sixteenth of the rate).
 // Next keys are loaded as soon as this step's scores are done, the next values after this
 // step's product, each into the registers just read: few registers, so three waves a SIMD cover the
 // memory's latency (two with both steps' registers held: 3.2 TB/s at 16 sequences of 16384-32768 keys,
-// 64 heads on 8).  The four waves of a block take
-// every fourth step of the block's chunk and are joined through LDS; chunks are joined by k_join.
+// 64 heads on 8; so 5.9, of 455.6 MB by the counters, 1.004 of the bytes it cannot do without).  The four or eight waves of a block
+// take every fourth or eighth step of its keys and are joined through LDS; pairs that several blocks share, and both lists of
+// a shared call, are joined by k_kv_join.
 #include "hqq_kv.h"
 
 namespace hqq {

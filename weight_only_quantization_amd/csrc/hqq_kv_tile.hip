@@ -10,8 +10,9 @@
 // (1024 + c) - 1024 is exact, fma(c, s, m) rounds once.
 // Softmax as in the stream kernel: one pass, fp32, the maximum raised only when a score passes it by 2^5.
 //
-// 2048 tokens on 8192 keys, 32 heads on 8, 4 bits: 240 Gflop in 285-294 us among such calls (304-316 in a trace), 0.82-0.84 Pflop/s; a library
-// product of two 8192 x 8192 fp16 matrices reaches 1.18.  Per 32 x 32 scores a wave needs 512 cycles of
+// 2048 tokens on 8192 keys, 32 heads on 8, 4 bits: 240 Gflop in 280-298 us among such calls, by the card (303 in a trace), 0.81-0.86 Pflop/s; a
+// library product of two 8192 x 8192 fp16 matrices reaches 1.18.  Keys, values and weights in fp16 cost 6.9e-4 of the output (2-norm)
+// with the fp16 output's own 2.1e-4.  Per 32 x 32 scores a wave needs 512 cycles of
 // the matrix unit and about 600 of the vector unit (16 exponentials take 256); with K and V from LDS and
 // their unpacking it takes about 1500 of its SIMD, without either 920: the two waves of a SIMD overlap only in part.
 // Padded rows against swizzled ones (an address a read less) 330 -> 312 us, the tile's two halves
