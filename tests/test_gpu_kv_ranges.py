@@ -79,12 +79,13 @@ def test_values_past_the_largest_half(d, bits, g, dtype):
             assert np.abs(lse.cpu().numpy()).max() == 0
 
 
-@pytest.mark.parametrize("where", ["low weight", "hidden", "other group", "other group, small floors"])
+@pytest.mark.parametrize("where", ["low weight", "hidden", "other group", "other group, small floors", "huge, low weight",
+                                   "huge, other group"])
 @pytest.mark.parametrize("seqs", [1, 130])
 @pytest.mark.parametrize("d,bits,g,dtype", [(128, 4, 64, "float16"), (128, 8, 32, "bfloat16"), (64, 4, 32, "bfloat16"), (64, 8, 32, "float16"),
                                             (128, 8, 64, "float16"), (128, 4, 32, "float16")])
 def test_small_values_next_to_large_ones(d, bits, g, dtype, seqs, where):
-    """Steps of 2 and more next to steps of 1e-4 and less: in other keys (of low weight, or hidden from some rows) and in
+    """Steps of 2 to 5000 next to steps of 1e-4 and less: in other keys (of low weight, or hidden from some rows) and in
     another group of the same keys.  24 rows take two tiles of 16, or where that is more blocks than the GPU runs at
     once, one of 32 (130 sequences)."""
     hq, torch = base.lib()
@@ -93,18 +94,19 @@ def test_small_values_next_to_large_ones(d, bits, g, dtype, seqs, where):
     n, t, per = 45, 3, 8
     k, v = (rng.normal(size=(n, d)).astype(np.float32) for _ in "kv")
     v *= 1e-3
-    if where in ("low weight", "hidden"):
-        at = 7 if where == "low weight" else n - 1
-        v[at] *= 1e6
-        if where == "low weight":
+    large = 1e7 if where.startswith("huge") else 1e6     # (steps of 32 and more in 8 bits too)
+    if where.endswith("low weight") or where == "hidden":
+        at = n - 1 if where == "hidden" else 7
+        v[at] *= large
+        if where != "hidden":
             k[at] = -8
     else:
-        v[:, :g] *= 1e6
+        v[:, :g] *= large
         if where.endswith("floors"):
             v[:, g:] = np.abs(v[:, g:]) + 3e-4
     cache, (ks, vs) = one_head(hq, torch, bits, k, v, g=g, dtype=dtype)
     steps = kp.quantise(kp.as_f32(kp.to(v, getattr(torch, dtype)))[:, None], bits, g)[1]
-    assert steps.max() > 2 and steps.min() < 1e-3
+    assert steps.max() > (32 if large > 1e6 else 2) and steps.min() < 1e-3
     q = kp.to((1 + 0.5 * rng.normal(size=(t, per, d))).astype(np.float32), getattr(torch, dtype))
     o, lse = attend(hq, torch, cache, q.cuda().repeat(seqs, 1, 1), [n] * seqs)
     see = np.arange(n)[None] <= (n - t + np.arange(t))[:, None]

@@ -13,7 +13,7 @@
 //           reduction is rare; the weights stay within fp16.
 //   values  O^T[channel][row] += (c s)[channel][key] p[key][row]: a lane's 8 scores are its operand as
 //           they are (keys keep their order inside the step).  c s is one fp16 rounding,
-//           fma(1024 + c, s, -1024 s), 2^-8 smaller for steps of 2 and more; the floors enter as one more product, sum_j p_j m_j.
+//           fma(1024 + c, s, -1024 s), 2^-8 smaller for steps of 32 and more; the floors enter as one more product, sum_j p_j m_j.
 //           p is rounded to fp16 (2^-11 relative at most, from 2^-24 of the maximum's weight down 2^-35 of that; kLift).
 //           These two roundings are what the matrix unit's fp16 operands cost: 5.2e-4 to 5.8e-4 of the output (2-norm) with the fp16
 //           output's own 2.1e-4 (fp32 products run at a sixteenth of the rate).
@@ -544,11 +544,15 @@ __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : 
     };
     auto word = [&](int b, int i, int t) { return sv.c[i >> 1][((2 * (i & 1) + t) * G::kUnit + b) / 4]; };
     const h2 n1024 = {(_Float16)-1024.f, (_Float16)-1024.f}, n64 = {(_Float16)-64.f, (_Float16)-64.f};
-    // 1024 s passes fp16 for steps of 64 and more, and c s where a group is wider than it: entries whose step is 2 or
-    // more (bit 14 of its half) are taken by themselves, 2^-8 smaller, and then the others without them, so that these keep
-    // their bits.  Few steps of the stream have any: the way holds no registers (opaque operands: else the compiler works out in front
+    // 1024 s passes fp16 for steps of 64 and more, and c s where a group is wider than it: entries whose step is 32 or
+    // more (its half plus 0x3000 reaches the sign) are taken by themselves, 2^-8 smaller, and then the others without them, so that
+    // these keep their bits.  Groups that wide, 480 and more in 4 bits, are rare, and so is the way (where all are: 36 us for 25 at 32
+    // sequences of 65-4096 keys, 32 heads on 8); it holds no registers (opaque operands: else the compiler works out in front
     // what both ways share).
-    if (__any((as_u32(st[0]) | as_u32(st[1]) | as_u32(st[2]) | as_u32(st[3])) & 0x40004000u)) {
+    auto past = [](uint32_t s) { return (s + 0x30003000u) >> 15 & 0x00010001u; };
+    const u16x2 s01 = __builtin_elementwise_max(as_u16x2(as_u32(st[0])), as_u16x2(as_u32(st[1])));
+    const u16x2 s23 = __builtin_elementwise_max(as_u16x2(as_u32(st[2])), as_u16x2(as_u32(st[3])));
+    if (__any(past(__builtin_bit_cast(uint32_t, __builtin_elementwise_max(s01, s23))))) {
 #pragma unroll
       for (int b = 0; b < G::kUnit; ++b) {
         u32x4 lo, hi;
@@ -556,7 +560,7 @@ __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : 
         for (int i = 0; i < 4; ++i) {
           uint32_t wx = word(b, i, 0), wy = word(b, i, 1), s = as_u32(st[i]);
           asm volatile("" : "+v"(wx), "+v"(wy), "+v"(s));
-          const h2 large = as_h2((s >> 14 & 0x00010001u) * 0xffffu & s) * h2{(_Float16)0x1p-8f, (_Float16)0x1p-8f};
+          const h2 large = as_h2(past(s) * 0xffffu & s) * h2{(_Float16)0x1p-8f, (_Float16)0x1p-8f};
           value(wx, wy, b, i, large, large * n1024, large * n64, lo, hi);
         }
 #pragma unroll
@@ -568,7 +572,7 @@ __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : 
         }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) st[i] = as_h2(as_u32(st[i]) & ~((as_u32(st[i]) >> 14 & 0x00010001u) * 0xffffu));
+      for (int i = 0; i < 4; ++i) st[i] = as_h2(as_u32(st[i]) & ~(past(as_u32(st[i])) * 0xffffu));
     }
     h2 s1024[4], s64[4];
 #pragma unroll
