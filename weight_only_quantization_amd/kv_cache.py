@@ -210,7 +210,8 @@ def hqq_kv_cache(num_pages: int, num_kv_heads: int, head_dim: int, nbits: int = 
 def hqq_kv_write(cache: KVCache, k, v, slots, echo: bool = False, stream=None):
     """Quantises k, v [n, num_kv_heads, head_dim] (fp16 or bf16; token and head strides allowed) into
     the cache's `slots` (int64 [n], distinct; slots outside the cache are skipped).  With `echo`
-    returns (k, v) as the values the cache now stands for, else None."""
+    returns (k, v) as the values the cache now stands for, else None (rounded once: in fp16 the top of a group that
+    reaches 65504 may be infinite)."""
     count, = _indices(slots, "slots", _torch().int64, 1)
     dtype, n = k.dtype, k.shape[0]
     if v.dtype is not dtype:
