@@ -522,6 +522,223 @@ size_t hqq_kv_attention_workspace_bytes(const hqq_kv_attention_args* args);
 int hqq_kv_attention(const hqq_kv_attention_args* args);
 int hqq_kv_attention_shared(const hqq_kv_attention_args* args);
 
+/*
+ * Rotary positions (not part of the page's method; between the projections and the cache of a decode step).  Of each head the
+ * first rot_dim channels are pairs (x_a, x_b), turned by the angle theta = position * freqs[i] of pair i:
+ *   y_a = m (x_a cos theta - x_b sin theta),  y_b = m (x_b cos theta + x_a sin theta);  the other channels are copied.
+ * layout HQQ_ROPE_HALVES: pair i is the channels i and i + rot_dim / 2; HQQ_ROPE_INTERLEAVED: 2 i and 2 i + 1.
+ * Angles and rotation are 64-bit, the result is rounded (to fp32, then to the type).
+ */
+#define HQQ_ROPE_HALVES 0
+#define HQQ_ROPE_INTERLEAVED 1
+typedef struct hqq_rope_form {
+  const double* freqs; /* device [rot_dim / 2]: radians per position; 8-byte aligned */
+  int rot_dim;         /* a multiple of 16, at most the head's channels */
+  int layout;
+  double magnitude;    /* m, finite (1 without scaling) */
+} hqq_rope_form;
+
+/* Scalings of the frequencies f_i = base^(-2 i / rot_dim) for contexts longer than the trained one. */
+#define HQQ_ROPE_PLAIN 0  /* f_i */
+#define HQQ_ROPE_LINEAR 1 /* f_i / factor: positions are interpolated */
+#define HQQ_ROPE_BASE 2   /* f_i of base * factor^(rot_dim / (rot_dim - 2)): the slowest pair is slowed by the factor */
+#define HQQ_ROPE_BANDS 3  /* by how often a pair turns over original_len positions: kept from `fast` turns on, divided by factor
+                             up to `slow` turns, between them a ramp over the pair's index, from floor(i(fast)) to ceil(i(slow)) with i(n) =
+                             rot_dim ln(original_len / (2 pi n)) / (2 ln base); magnitude 0.1 ln(factor) + 1 */
+
+/*
+ * The frequencies of a form, on the host: freqs (host, rot_dim / 2 doubles) and *magnitude (nullable).  rot_dim a positive multiple
+ * of 16 (at most 1024), base > 1, factor >= 1, all finite; for HQQ_ROPE_BANDS original_len >= 1 and fast > slow > 0.
+ */
+int hqq_rope_frequencies(int rot_dim, double base, int scaling, double factor, double original_len, double fast, double slow,
+                         double* freqs, double* magnitude);
+
+/*
+ * Turns q and k (either may have 0 heads) of n tokens.
+ *   dtype      HQQ_KV_F16 or HQQ_KV_BF16; head_dim a multiple of 16, at most 1024.
+ *   backward   0; 1: the transposed rotation (sine with the other sign): dL/dx from dL/dy.
+ *   positions  in  int64 [n] (device, 8-byte aligned), any value within +-2^53.
+ *   q, q_out   [n, q_heads, head_dim], channels contiguous; token and head strides in elements (non-negative multiples of 8;
+ *              16-byte aligned pointers).  q_out may be q itself with the same strides; no other overlap, and no two heads of an output
+ *              on the same memory.  k, k_out likewise.
+ * n = 0 does nothing.  NaN and infinities stay within their pair.
+ */
+typedef struct hqq_rope_args {
+  hqq_rope_form form;
+  int dtype, head_dim, backward;
+  int64_t n;
+  const int64_t* positions;
+  const void* q;
+  int64_t q_token_stride, q_head_stride;
+  int q_heads;
+  void* q_out;
+  int64_t q_out_token_stride, q_out_head_stride;
+  const void* k;
+  int64_t k_token_stride, k_head_stride;
+  int k_heads;
+  void* k_out;
+  int64_t k_out_token_stride, k_out_head_stride;
+  void* stream;
+} hqq_rope_args;
+int hqq_rope(const hqq_rope_args* args);
+
+/*
+ * hqq_rope of q and k and hqq_kv_write of the turned keys and the values, in one launch: the same bits as the two calls (the turned
+ * key is rounded to dtype before it is quantised).
+ *   write      as for hqq_kv_write, k before the rotation; k_echo what the cache stands for, so turned.
+ *   form, positions, q, q_out  as for hqq_rope (head_dim the cache's; q_heads may be 0).
+ */
+typedef struct hqq_kv_write_rope_args {
+  hqq_kv_write_args write;
+  hqq_rope_form form;
+  const int64_t* positions;
+  const void* q;
+  int64_t q_token_stride, q_head_stride;
+  int q_heads;
+  void* q_out;
+  int64_t q_out_token_stride, q_out_head_stride;
+} hqq_kv_write_rope_args;
+int hqq_kv_write_rope(const hqq_kv_write_rope_args* args);
+
+/*
+ * A tree of drafted tokens per sequence, to be verified in one pass: each sequence's query tokens are its drafts, written to the
+ * cache as its last tokens (draft t of T at position seq_len - T + t); a draft sees all keys in front of the drafts, and itself and its
+ * ancestors.
+ *
+ * hqq_kv_tree_plan works out from the drafts' parents what the step needs:
+ *   parents    in  int32 [total_q]: index within the sequence of the draft that draft t follows, smaller than t; -1 (and any
+ *              other value) for a draft that follows the cached tokens directly.
+ *   num_seqs, cu_q, max_q, page_table, table_stride, table_cols, seq_lens  as for hqq_kv_attention (max_q at most 4096).
+ *   mask       out uint64 [total_q, mask_words]: bit j of row t (word j / 64) set where draft t sees draft j of its sequence;
+ *              mask_words 1 .. 64, 64 * mask_words >= max_q.
+ *   positions  out (nullable) int64 [total_q]: seq_len - T + depth, for the rotation: a draft directly behind the cached
+ *              tokens has depth 0.
+ *   slots      out (nullable) int64 [total_q]: where hqq_kv_write puts draft t, by its index; -1 without a page.
+ * Rows of tokens of no sequence are left as they are.
+ */
+typedef struct hqq_kv_tree_plan_args {
+  const int32_t* parents;
+  int64_t total_q, num_seqs;
+  const int32_t* cu_q;
+  int64_t max_q;
+  const int32_t* page_table;
+  int64_t table_stride, table_cols;
+  const int32_t* seq_lens;
+  int page_size;
+  uint64_t* mask;
+  int64_t mask_words;
+  int64_t* positions;
+  int64_t* slots;
+  void* stream;
+} hqq_kv_tree_plan_args;
+int hqq_kv_tree_plan(const hqq_kv_tree_plan_args* args);
+
+/*
+ * hqq_kv_attention (with prefix_len > 0 hqq_kv_attention_shared) for drafted trees: `causal` is not looked at; of the
+ * sequence's last T keys, T its query tokens, query token t sees those whose bit is set in row t of mask (device, 8-byte
+ * aligned, uint64 [total_q, mask_words]; mask_words 1 .. 64, 64 * mask_words >= max_q), and all keys in front of them.  The mask may be
+ * any (bits from T on are ignored); a row that sees no key is 0.  seq_len < T: the drafts in front of the first key do not exist.
+ * Workspace: hqq_kv_attention_tree_workspace_bytes(args).
+ */
+typedef struct hqq_kv_tree_args {
+  hqq_kv_attention_args attention;
+  const uint64_t* mask;
+  int64_t mask_words;
+} hqq_kv_tree_args;
+size_t hqq_kv_attention_tree_workspace_bytes(const hqq_kv_tree_args* args);
+int hqq_kv_attention_tree(const hqq_kv_tree_args* args);
+
+/*
+ * Moving what is cached, exactly as it is stored, in all layers of a model at once: layers of one format and number of pages,
+ * which share their page tables.  pages is a HOST array of num_layers (1 .. HQQ_KV_MAX_LAYERS) device pointers, read before the
+ * call returns; cache gives the format (cache.pages is not looked at).  The int32 arrays are device memory, 4-byte aligned; outputs do
+ * not overlap inputs.
+ */
+#define HQQ_KV_MAX_LAYERS 128
+typedef struct hqq_kv_layers {
+  hqq_kv_cache cache;
+  void* const* pages;
+  int num_layers;
+} hqq_kv_layers;
+
+/*
+ * After a draft has been verified: moves each sequence's accepted drafts together behind its other tokens.
+ *   num_seqs, total_q, cu_q, max_q  the drafts, as for hqq_kv_tree_plan (without cu_q total_q / num_seqs each; total_q and
+ *              max_q bound nothing but this).
+ *   page_table, table_stride, table_cols, seq_lens  as for hqq_kv_attention, the drafts included.
+ *   accepted   in  [num_seqs] rows accepted_stride apart, of up to max_accepted indices each: the accepted drafts, rising strictly
+ *              (a path from a root is).  Indices outside the draft are skipped; lists that do not rise leave the drafts' contents
+ *              undefined.
+ *   num_accepted  in  [num_seqs], limited to 0 .. max_accepted and to the drafts.
+ *   new_lens   out [num_seqs]: seq_len - T + num_accepted (not below 0; seq_len limited to the table).
+ * Draft accepted[j] goes to position seq_len - T + j.  The tables keep their pages.  No two sequences' drafts may share a page.
+ */
+typedef struct hqq_kv_accept_args {
+  hqq_kv_layers layers;
+  int64_t num_seqs, total_q;
+  const int32_t* cu_q;
+  int64_t max_q;
+  const int32_t* page_table;
+  int64_t table_stride, table_cols;
+  const int32_t* seq_lens;
+  const int32_t* accepted;
+  int64_t accepted_stride, max_accepted;
+  const int32_t* num_accepted;
+  int32_t* new_lens;
+  void* stream;
+} hqq_kv_accept_args;
+int hqq_kv_accept(const hqq_kv_accept_args* args);
+
+/*
+ * Forks sequences, as a beam search does: sequence i of num_new continues sequence parents[i] of the old ones (any order,
+ * repeated or left out).  Children share their parent's full pages.  Of the children of one parent the first keeps its partly
+ * filled page, and the pages the row lists behind it; for each other child the page's tokens are copied to page fresh[i].
+ *   parents, fresh  in  [num_new]; fresh: pages of no sequence, distinct (of a child that needs none: not used).
+ *   new_table  out [num_new] rows new_stride apart (>= table_cols), of table_cols entries; -1 behind what a child has.
+ *   new_lens   out [num_new]: the parent's length.
+ * A parent outside 0 .. num_seqs - 1 gives an empty sequence; a fresh page outside the cache is entered, nothing copied.
+ */
+typedef struct hqq_kv_fork_args {
+  hqq_kv_layers layers;
+  int64_t num_seqs;
+  const int32_t* page_table;
+  int64_t table_stride, table_cols;
+  const int32_t* seq_lens;
+  int64_t num_new;
+  const int32_t* parents;
+  const int32_t* fresh;
+  int32_t* new_table;
+  int64_t new_stride;
+  int32_t* new_lens;
+  void* stream;
+} hqq_kv_fork_args;
+int hqq_kv_fork(const hqq_kv_fork_args* args);
+
+/*
+ * Moves the pages that sequences hold together, so that the free ones are one range again: with U distinct pages held, those with
+ * numbers from U on move, in rising order, to the numbers below U that nobody holds, in rising order.
+ *   page_table, seq_lens  in  a sequence holds the pages of its first ceil(seq_len / page_size) columns (several may hold
+ *              one; entries outside the cache are nobody's).
+ *   new_table  out as for hqq_kv_fork, num_seqs rows: the new numbers, -1 for what is not held.
+ *   used       out [1]: U.  Pages U .. num_pages - 1 are free afterwards.
+ *   workspace  hqq_kv_compact_workspace_bytes(num_pages) bytes, 16-byte aligned.  num_pages at most 2^20.
+ */
+typedef struct hqq_kv_compact_args {
+  hqq_kv_layers layers;
+  int64_t num_seqs;
+  const int32_t* page_table;
+  int64_t table_stride, table_cols;
+  const int32_t* seq_lens;
+  int32_t* new_table;
+  int64_t new_stride;
+  int32_t* used;
+  void* workspace;
+  size_t workspace_bytes;
+  void* stream;
+} hqq_kv_compact_args;
+size_t hqq_kv_compact_workspace_bytes(int64_t num_pages);
+int hqq_kv_compact(const hqq_kv_compact_args* args);
+
 /* Static description of a status code. */
 const char* hqq_status_string(int status);
 

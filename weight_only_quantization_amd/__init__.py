@@ -7,7 +7,8 @@ the import of a compute function raises.
 
 Names follow the C ABI (``include/hqq.h``): ``hqq_quantize``, ``hqq_dequantize``,
 ``hqq_gemv_w4a16``, ``hqq_gemv`` (the other stored formats), the quantised key/value cache and its
-attention (``hqq_kv_*``, module ``kv_cache``), plus the size queries.
+attention (``hqq_kv_*``, module ``kv_cache``), drafted trees and moves of the cache (module ``kv_pages``), rotary
+positions (``hqq_rope``, module ``rotary``), plus the size queries.
 """
 from __future__ import annotations
 
@@ -39,7 +40,9 @@ EXPORTS = ("hqq_packed_bytes", "hqq_num_groups", "hqq_quantize_workspace_bytes",
            "hqq_dequantize", "hqq_gemv_w4a16", "hqq_gemm_workspace_bytes", "hqq_gemm_w4a16",
            "hqq_gemm_dx_workspace_bytes", "hqq_gemm_w4a16_dx", "hqq_gemm_dx", "hqq_gemv", "hqq_gemm",
            "hqq_kv_page_bytes", "hqq_kv_write", "hqq_kv_read", "hqq_kv_attention_workspace_bytes", "hqq_kv_attention",
-           "hqq_kv_attention_shared",
+           "hqq_kv_attention_shared", "hqq_kv_attention_tree", "hqq_kv_attention_tree_workspace_bytes",
+           "hqq_rope_frequencies", "hqq_rope", "hqq_kv_write_rope", "hqq_kv_tree_plan", "hqq_kv_accept", "hqq_kv_fork",
+           "hqq_kv_compact", "hqq_kv_compact_workspace_bytes",
            "hqq_release_workspaces", "hqq_status_string", "hqq_last_error")
 
 _lib = None
@@ -101,6 +104,8 @@ def load(path: str = LIB_PATH):
     lib.hqq_last_error.argtypes = []
     lib.hqq_last_error.restype = ctypes.c_char_p
     kv_cache.declare(lib)
+    rotary.declare(lib)
+    kv_pages.declare(lib)
     _lib = lib
     return lib
 
@@ -602,5 +607,11 @@ def probe_read(bufs, sink, unroll: int = 4, stream=None) -> int:
 # ------------------------------------------------------------------------------ key/value cache
 
 from . import kv_cache  # noqa: E402
-from .kv_cache import (KVCache, hqq_kv_attention, hqq_kv_attention_shared, hqq_kv_cache, hqq_kv_page_bytes,  # noqa: E402,F401
-                       hqq_kv_read, hqq_kv_write)
+from .kv_cache import (KVCache, hqq_kv_attention, hqq_kv_attention_shared, hqq_kv_attention_tree, hqq_kv_cache,  # noqa: E402,F401
+                       hqq_kv_page_bytes, hqq_kv_read, hqq_kv_write)
+
+# rotary positions; drafted trees, and moving what the cache holds
+from . import kv_pages, rotary  # noqa: E402
+from .kv_pages import (KVLayers, hqq_kv_accept, hqq_kv_compact, hqq_kv_compact_workspace_bytes, hqq_kv_fork,  # noqa: E402,F401
+                       hqq_kv_tree_plan)
+from .rotary import RopeTable, hqq_kv_write_rope, hqq_rope, hqq_rope_table  # noqa: E402,F401

@@ -25,7 +25,8 @@ FLAGS = ["-O3", "-std=c++17", "-fPIC", "--offload-arch=" + ARCH, "-ffp-contract=
          "-Wall", "-Wno-unused-function", "-I" + os.path.join(HERE, "..", "include")]
 
 SOURCES = ["hqq_api.hip", "hqq_quant.hip", "hqq_dequant.hip", "hqq_gemv.hip", "hqq_gemv_ext.hip", "hqq_gemv_dq.hip", "hqq_gemm.hip",
-           "hqq_kv_api.hip", "hqq_kv_cache.hip", "hqq_kv_stream.hip", "hqq_kv_tile.hip"]
+           "hqq_kv_api.hip", "hqq_kv_cache.hip", "hqq_kv_stream.hip", "hqq_kv_tile.hip", "hqq_kv_stream_tree.hip", "hqq_kv_tile_tree.hip",
+           "hqq_kv_pages.hip", "hqq_rope.hip", "hqq_draft_api.hip"]
 # HBM probes of known byte counts (measurement only), a library of their own
 PROBE_SOURCES = ["hqq_probe.hip"]
 
@@ -34,7 +35,8 @@ PROBE_SOURCES = ["hqq_probe.hip"]
 # accumulator input and copies accumulators between register files around most MFMAs.  The cache's
 # attention kernels the same (88 of the stream's 449 vector instructions a step were such copies).
 _VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]
-EXTRA = {"hqq_gemm.hip": _VGPR_FORM, "hqq_kv_stream.hip": _VGPR_FORM, "hqq_kv_tile.hip": _VGPR_FORM}
+EXTRA = {name: _VGPR_FORM for name in ("hqq_gemm.hip", "hqq_kv_stream.hip", "hqq_kv_tile.hip", "hqq_kv_stream_tree.hip",
+                                       "hqq_kv_tile_tree.hip")}
 
 
 def _compile(src: str) -> str:
@@ -56,7 +58,7 @@ def _link(objs, lib):
     os.replace(tmp, lib)
 
 
-def build(jobs: int = 4) -> str:
+def build(jobs: int = 8) -> str:
     os.makedirs(OBJDIR, exist_ok=True)
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         objs = list(ex.map(_compile, SOURCES + PROBE_SOURCES))
@@ -67,6 +69,6 @@ def build(jobs: int = 4) -> str:
 
 if __name__ == "__main__":
     ap = argparse.ArgumentParser()
-    ap.add_argument("--jobs", type=int, default=4)
+    ap.add_argument("--jobs", type=int, default=8)
     a = ap.parse_args()
     print(build(a.jobs))

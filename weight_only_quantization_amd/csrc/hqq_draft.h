@@ -1,0 +1,129 @@
+// Internal declarations of a drafted decode step's other operators: rotary positions, drafted trees, moving tokens and pages.
+#pragma once
+
+#include "hqq_kv.h"
+
+namespace hqq {
+namespace kv {
+
+// Rotation of the first rot channels of a head.
+struct Turn {
+  const double* freqs;  // [rot / 2] radians per position
+  const int64_t* positions;
+  int rot;
+  double c_scale, s_scale;  // magnitude, and with its sign the magnitude of the sine (backward: negative)
+};
+
+// Heads of one tensor, in and out (strides in elements).
+struct Heads {
+  const void* in;
+  void* out;
+  int64_t in_ts, in_hs, out_ts, out_hs;
+  int count;
+};
+
+struct RopeArgs {
+  Turn turn;
+  Heads q, k;
+  int64_t n;
+  int head_dim;
+};
+
+struct WriteRopeArgs {
+  WriteArgs w;
+  Turn turn;
+  Heads q;
+};
+
+constexpr int kMostRopeDim = 1024;
+// Tokens of a block.
+inline int rope_tokens(int head_dim) { return 64 / (head_dim / 16); }
+inline int write_rope_tokens(int head_dim) { return 64 / (head_dim / 8); }
+hipError_t launch_rope(const RopeArgs& a, int dtype, bool interleaved, hipStream_t st);
+hipError_t launch_write_rope(const WriteRopeArgs& a, int D, int bits, int gs, int dtype, bool interleaved, hipStream_t st);
+
+// ---- pages
+
+struct Layers {
+  uint8_t* pages[HQQ_KV_MAX_LAYERS];
+};
+
+// Sizes within a block, for kernels that move bytes whatever the format.
+struct Bytes {
+  int row;   // K codes of a token; V codes as many
+  int unit;  // V codes of a token in one of 16 places, 4 of them next to each other
+  int meta;  // words of metadata of a token (steps and floors, K and V)
+};
+
+struct Sequences {
+  const int32_t* table;
+  int64_t table_stride;
+  int table_cols;
+  const int32_t* lens;
+  int count;
+};
+
+struct TreePlanArgs {
+  const int32_t* parents;
+  Sequences seqs;
+  int page_shift;
+  const int32_t* cu_q;
+  int64_t total_q;
+  int tq, max_q;
+  uint64_t* mask;
+  int words;
+  int64_t* positions;
+  int64_t* slots;
+};
+constexpr int kMostDrafts = 4096;
+hipError_t launch_tree_plan(const TreePlanArgs& a, hipStream_t st);
+
+struct AcceptArgs {
+  Format f;  // (its pages are not used: layers has them)
+  Bytes b;
+  Layers layers;
+  int num_layers;
+  Sequences seqs;
+  const int32_t* cu_q;
+  int64_t total_q;
+  int tq, max_q;
+  const int32_t* accepted;
+  int64_t accepted_stride;
+  int most;  // accepted tokens of a sequence at most
+  const int32_t* num_accepted;
+  int32_t* new_lens;
+};
+hipError_t launch_accept(const AcceptArgs& a, hipStream_t st);
+
+struct ForkArgs {
+  Format f;
+  Bytes b;
+  Layers layers;
+  int num_layers;
+  Sequences seqs;
+  int num_new;
+  const int32_t* parents;
+  const int32_t* fresh;
+  int32_t* new_table;
+  int64_t new_stride;
+  int32_t* new_lens;
+};
+hipError_t launch_fork(const ForkArgs& a, hipStream_t st);
+
+struct CompactArgs {
+  Format f;
+  Layers layers;
+  int num_layers;
+  Sequences seqs;
+  int32_t* new_table;
+  int64_t new_stride;
+  int32_t* used;
+  int32_t* workspace;  // kCompactHead words, then sources and targets of the moves, then a page's new place
+};
+constexpr int kMostPages = 1 << 20;  // a bit each in the LDS of one block
+constexpr int kCompactHead = 4;
+inline int64_t compact_words(int64_t num_pages) { return kCompactHead + 2 * ((num_pages + 1) / 2) + num_pages; }
+hipError_t launch_compact(const CompactArgs& a, hipStream_t st);
+
+}  // namespace kv
+}  // namespace hqq

@@ -1,0 +1,273 @@
+// C ABI of rotary positions, drafted trees' plans and the cache's moves: argument checks and launches.  Every check happens before
+// anything is enqueued.
+#include <math.h>
+
+#include "hqq_kv_checks.h"
+
+namespace {
+
+using hqq::kv::Bytes;
+using hqq::kv::Heads;
+using hqq::kv::Layers;
+using hqq::kv::Sequences;
+using hqq::kv::Turn;
+
+int check_turn(const hqq_rope_form& x, const int64_t* positions, int head_dim, int backward, bool anything, Turn* t) {
+  KV_NEED(x.rot_dim > 0 && x.rot_dim <= head_dim, HQQ_ERR_INVALID_ARGUMENT, "rot_dim must be 1 .. head_dim");
+  KV_NEED(x.rot_dim % 16 == 0, HQQ_ERR_UNSUPPORTED, "rot_dim must be a multiple of 16");
+  KV_NEED(x.layout == HQQ_ROPE_HALVES || x.layout == HQQ_ROPE_INTERLEAVED, HQQ_ERR_INVALID_ARGUMENT, "unknown layout");
+  KV_NEED(isfinite(x.magnitude), HQQ_ERR_INVALID_ARGUMENT, "magnitude must be finite");
+  KV_NEED(backward == 0 || backward == 1, HQQ_ERR_INVALID_ARGUMENT, "backward must be 0 or 1");
+  if (!anything) return HQQ_OK;
+  KV_NEED(x.freqs && aligned8(x.freqs) && positions && aligned8(positions), HQQ_ERR_INVALID_ARGUMENT,
+          "freqs and positions must be 8-byte aligned pointers");
+  *t = Turn{x.freqs, positions, x.rot_dim, x.magnitude, backward ? -x.magnitude : x.magnitude};
+  return HQQ_OK;
+}
+
+int check_heads(const Heads& h) {
+  KV_NEED(h.count == 0 || (h.in && h.out && aligned16(h.in) && aligned16(h.out)), HQQ_ERR_INVALID_ARGUMENT,
+          "q, k and their outputs must be 16-byte aligned pointers");
+  KV_NEED(h.in_ts >= 0 && h.in_hs >= 0 && h.out_ts >= 0 && h.out_hs >= 0 && (h.in_ts | h.in_hs | h.out_ts | h.out_hs) % 8 == 0,
+          HQQ_ERR_INVALID_ARGUMENT, "strides must be non-negative multiples of 8 elements");
+  KV_NEED(h.in != h.out || (h.in_ts == h.out_ts && h.in_hs == h.out_hs), HQQ_ERR_INVALID_ARGUMENT,
+          "an output in the place of its input needs the same strides");
+  return HQQ_OK;
+}
+
+int check_count(int64_t n, int tokens) {
+  KV_NEED(n >= 0, HQQ_ERR_INVALID_ARGUMENT, "n out of range");
+  KV_NEED(n <= kThreads / 256 * tokens, HQQ_ERR_UNSUPPORTED, "too many tokens in a call");
+  return HQQ_OK;
+}
+
+int check_sequences(int64_t num_seqs, const int32_t* table, int64_t stride, int64_t cols, const int32_t* lens, int page_size,
+                    Sequences* s) {
+  KV_NEED(num_seqs >= 0, HQQ_ERR_INVALID_ARGUMENT, "num_seqs out of range");
+  KV_NEED(cols >= 0 && cols <= INT32_MAX / page_size, HQQ_ERR_INVALID_ARGUMENT, "table_cols out of range");
+  KV_NEED(stride >= 0, HQQ_ERR_INVALID_ARGUMENT, "table_stride must not be negative");
+  KV_NEED(num_seqs <= 65535, HQQ_ERR_UNSUPPORTED, "at most 65535 sequences in a call");
+  if (num_seqs == 0) return HQQ_OK;
+  KV_NEED(lens && aligned4(lens) && (table || cols == 0) && aligned4(table), HQQ_ERR_INVALID_ARGUMENT,
+          "seq_lens and page_table must be 4-byte aligned pointers");
+  *s = Sequences{table, stride, (int)cols, lens, (int)num_seqs};
+  return HQQ_OK;
+}
+
+int check_drafts(int64_t num_seqs, int64_t total_q, const int32_t* cu_q, int64_t max_q, int* tq) {
+  KV_NEED(total_q >= 0 && total_q <= (int64_t(1) << 30), HQQ_ERR_INVALID_ARGUMENT, "total_q out of range");
+  KV_NEED(total_q == 0 || num_seqs > 0, HQQ_ERR_INVALID_ARGUMENT, "query tokens without a sequence");
+  KV_NEED(cu_q || num_seqs == 0 || total_q % num_seqs == 0, HQQ_ERR_INVALID_ARGUMENT,
+          "without cu_q total_q must be a multiple of num_seqs");
+  KV_NEED(!cu_q || (max_q >= 0 && max_q <= total_q), HQQ_ERR_INVALID_ARGUMENT, "max_q must be 0 .. total_q");
+  KV_NEED(aligned4(cu_q), HQQ_ERR_INVALID_ARGUMENT, "cu_q must be 4-byte aligned");
+  *tq = cu_q || num_seqs == 0 ? 0 : (int)(total_q / num_seqs);
+  return HQQ_OK;
+}
+
+int check_layers(const hqq_kv_layers& x, Format* f, Bytes* b, Layers* l) {
+  const hqq_kv_cache& c = x.cache;
+  const int st = check_format(c.num_kv_heads, c.head_dim, c.nbits, c.group_size, c.page_size);
+  if (st != HQQ_OK) return st;
+  KV_NEED(x.num_layers >= 1 && x.num_layers <= HQQ_KV_MAX_LAYERS, HQQ_ERR_INVALID_ARGUMENT, "num_layers must be 1 .. 128");
+  KV_NEED(x.pages, HQQ_ERR_INVALID_ARGUMENT, "pages must not be NULL");
+  for (int i = 0; i < x.num_layers; ++i) {
+    hqq_kv_cache one = c;
+    one.pages = x.pages[i];
+    const int status = check_cache(one, f);
+    if (status != HQQ_OK) return status;
+    l->pages[i] = f->pages;
+  }
+  *b = Bytes{c.head_dim * c.nbits / 8, c.head_dim * c.nbits / 128, 2 * (c.head_dim / c.group_size)};
+  return HQQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int hqq_rope_frequencies(int rot_dim, double base, int scaling, double factor, double original_len, double fast, double slow,
+                         double* freqs, double* magnitude) {
+  KV_NEED(rot_dim > 0 && rot_dim <= hqq::kv::kMostRopeDim, HQQ_ERR_INVALID_ARGUMENT, "rot_dim must be 1 .. 1024");
+  KV_NEED(rot_dim % 16 == 0, HQQ_ERR_UNSUPPORTED, "rot_dim must be a multiple of 16");
+  KV_NEED(base > 1 && isfinite(base) && factor >= 1 && isfinite(factor), HQQ_ERR_INVALID_ARGUMENT,
+          "base must be over 1 and factor at least 1");
+  KV_NEED(scaling >= HQQ_ROPE_PLAIN && scaling <= HQQ_ROPE_BANDS, HQQ_ERR_INVALID_ARGUMENT, "unknown scaling");
+  KV_NEED(scaling != HQQ_ROPE_BANDS || (original_len >= 1 && isfinite(original_len) && slow > 0 && fast > slow && isfinite(fast)),
+          HQQ_ERR_INVALID_ARGUMENT, "bands need original_len of 1 and more and fast > slow > 0");
+  KV_NEED(freqs, HQQ_ERR_INVALID_ARGUMENT, "freqs must not be NULL");
+  const double r = rot_dim;
+  double low = 0, high = 0;
+  if (scaling == HQQ_ROPE_BASE) base *= pow(factor, r / (r - 2));
+  if (scaling == HQQ_ROPE_BANDS) {
+    const double per = r / (2 * log(base));
+    low = fmax(floor(per * log(original_len / (2 * M_PI * fast))), 0.0);
+    high = fmin(ceil(per * log(original_len / (2 * M_PI * slow))), r - 1);
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = pow(base, -2 * i / r);
+    if (scaling == HQQ_ROPE_LINEAR) f /= factor;
+    if (scaling == HQQ_ROPE_BANDS) {
+      const double ramp = fmin(fmax((i - low) / fmax(high - low, 0.001), 0.0), 1.0);
+      f = f * (1 - ramp) + f / factor * ramp;
+    }
+    freqs[i] = f;
+  }
+  if (magnitude) *magnitude = scaling == HQQ_ROPE_BANDS ? 0.1 * log(factor) + 1 : 1.0;
+  return HQQ_OK;
+}
+
+int hqq_rope(const hqq_rope_args* x) {
+  KV_NEED(x, HQQ_ERR_INVALID_ARGUMENT, "args must not be NULL");
+  KV_NEED(known_type(x->dtype), HQQ_ERR_INVALID_ARGUMENT, "dtype must be HQQ_KV_F16 or HQQ_KV_BF16");
+  KV_NEED(x->head_dim > 0, HQQ_ERR_INVALID_ARGUMENT, "head_dim must be positive");
+  KV_NEED(x->head_dim % 16 == 0 && x->head_dim <= hqq::kv::kMostRopeDim, HQQ_ERR_UNSUPPORTED,
+          "head_dim must be a multiple of 16 and at most 1024");
+  KV_NEED(x->q_heads >= 0 && x->k_heads >= 0 && x->q_heads <= 65536 && x->k_heads <= 65536, HQQ_ERR_INVALID_ARGUMENT,
+          "heads out of range");
+  int st = check_count(x->n, hqq::kv::rope_tokens(x->head_dim));
+  if (st != HQQ_OK) return st;
+  const bool anything = x->n > 0 && x->q_heads + x->k_heads > 0;
+  hqq::kv::RopeArgs a{};
+  st = check_turn(x->form, x->positions, x->head_dim, x->backward, anything, &a.turn);
+  if (st != HQQ_OK || !anything) return st;
+  a.q = Heads{x->q, x->q_out, x->q_token_stride, x->q_head_stride, x->q_out_token_stride, x->q_out_head_stride, x->q_heads};
+  a.k = Heads{x->k, x->k_out, x->k_token_stride, x->k_head_stride, x->k_out_token_stride, x->k_out_head_stride, x->k_heads};
+  a.n = x->n;
+  a.head_dim = x->head_dim;
+  for (const Heads* h : {&a.q, &a.k}) {
+    st = check_heads(*h);
+    if (st != HQQ_OK) return st;
+  }
+  return device_status(hqq::kv::launch_rope(a, x->dtype, x->form.layout == HQQ_ROPE_INTERLEAVED, static_cast<hipStream_t>(x->stream)));
+}
+
+int hqq_kv_write_rope(const hqq_kv_write_rope_args* x) {
+  KV_NEED(x, HQQ_ERR_INVALID_ARGUMENT, "args must not be NULL");
+  const hqq_kv_write_args& w = x->write;
+  hqq::kv::WriteRopeArgs a{};
+  int st = check_write(w, &a.w);
+  if (st != HQQ_OK) return st;
+  KV_NEED(x->q_heads >= 0 && x->q_heads <= 65536, HQQ_ERR_INVALID_ARGUMENT, "heads out of range");
+  st = check_count(w.n, hqq::kv::write_rope_tokens(w.cache.head_dim));
+  if (st != HQQ_OK) return st;
+  st = check_turn(x->form, x->positions, w.cache.head_dim, 0, w.n > 0, &a.turn);
+  if (st != HQQ_OK || w.n == 0) return st;
+  a.q = Heads{x->q, x->q_out, x->q_token_stride, x->q_head_stride, x->q_out_token_stride, x->q_out_head_stride, x->q_heads};
+  st = check_heads(a.q);
+  if (st != HQQ_OK) return st;
+  return device_status(hqq::kv::launch_write_rope(a, w.cache.head_dim, w.cache.nbits, w.cache.group_size, w.dtype,
+                                                  x->form.layout == HQQ_ROPE_INTERLEAVED, static_cast<hipStream_t>(w.stream)));
+}
+
+int hqq_kv_tree_plan(const hqq_kv_tree_plan_args* x) {
+  KV_NEED(x, HQQ_ERR_INVALID_ARGUMENT, "args must not be NULL");
+  const int page = x->page_size;
+  KV_NEED(page > 0, HQQ_ERR_INVALID_ARGUMENT, "page_size must be positive");
+  KV_NEED(page == 16 || page == 32 || page == 64 || page == 128 || page == 256, HQQ_ERR_UNSUPPORTED,
+          "page_size must be 16, 32, 64, 128 or 256");
+  hqq::kv::TreePlanArgs a{};
+  int st = check_sequences(x->num_seqs, x->page_table, x->table_stride, x->table_cols, x->seq_lens, page, &a.seqs);
+  if (st != HQQ_OK) return st;
+  st = check_drafts(x->num_seqs, x->total_q, x->cu_q, x->max_q, &a.tq);
+  if (st != HQQ_OK) return st;
+  KV_NEED(x->mask_words >= 1 && x->mask_words <= kMostDrafts / 64, HQQ_ERR_INVALID_ARGUMENT, "mask_words must be 1 .. 64");
+  const int64_t most = x->cu_q ? x->max_q : a.tq;
+  KV_NEED(most <= 64 * x->mask_words, HQQ_ERR_INVALID_ARGUMENT, "a sequence has more drafts than bits of its mask");
+  if (most == 0) return HQQ_OK;
+  KV_NEED(x->parents && aligned4(x->parents), HQQ_ERR_INVALID_ARGUMENT, "parents must be a 4-byte aligned pointer");
+  KV_NEED(x->mask && aligned8(x->mask) && aligned8(x->positions) && aligned8(x->slots), HQQ_ERR_INVALID_ARGUMENT,
+          "mask, positions and slots must be 8-byte aligned, mask not NULL");
+  a.parents = x->parents;
+  a.page_shift = __builtin_ctz(page);
+  a.cu_q = x->cu_q;
+  a.total_q = x->total_q;
+  a.max_q = (int)most;
+  a.mask = x->mask;
+  a.words = (int)x->mask_words;
+  a.positions = x->positions;
+  a.slots = x->slots;
+  return device_status(hqq::kv::launch_tree_plan(a, static_cast<hipStream_t>(x->stream)));
+}
+
+int hqq_kv_accept(const hqq_kv_accept_args* x) {
+  KV_NEED(x, HQQ_ERR_INVALID_ARGUMENT, "args must not be NULL");
+  hqq::kv::AcceptArgs a{};
+  int st = check_layers(x->layers, &a.f, &a.b, &a.layers);
+  if (st != HQQ_OK) return st;
+  st = check_sequences(x->num_seqs, x->page_table, x->table_stride, x->table_cols, x->seq_lens, x->layers.cache.page_size, &a.seqs);
+  if (st != HQQ_OK) return st;
+  st = check_drafts(x->num_seqs, x->total_q, x->cu_q, x->max_q, &a.tq);
+  if (st != HQQ_OK) return st;
+  KV_NEED(x->max_accepted >= 0 && x->max_accepted <= INT32_MAX && x->accepted_stride >= 0, HQQ_ERR_INVALID_ARGUMENT,
+          "max_accepted and accepted_stride must be in range");
+  if (x->num_seqs == 0) return HQQ_OK;
+  KV_NEED((x->accepted || x->max_accepted == 0) && aligned4(x->accepted) && x->num_accepted && aligned4(x->num_accepted) &&
+              x->new_lens && aligned4(x->new_lens),
+          HQQ_ERR_INVALID_ARGUMENT, "accepted, num_accepted and new_lens must be 4-byte aligned pointers");
+  a.num_layers = x->layers.num_layers;
+  a.cu_q = x->cu_q;
+  a.total_q = x->total_q;
+  a.max_q = (int)(x->cu_q ? x->max_q : a.tq);
+  a.accepted = x->accepted;
+  a.accepted_stride = x->accepted_stride;
+  // (a sequence's moves are counted in 32 bits: tokens times heads)
+  a.most = (int)(x->max_accepted < a.max_q ? x->max_accepted : a.max_q);
+  KV_NEED((int64_t)a.most * a.f.hkv <= INT32_MAX / 2, HQQ_ERR_UNSUPPORTED, "too many accepted tokens in a call");
+  a.num_accepted = x->num_accepted;
+  a.new_lens = x->new_lens;
+  return device_status(hqq::kv::launch_accept(a, static_cast<hipStream_t>(x->stream)));
+}
+
+int hqq_kv_fork(const hqq_kv_fork_args* x) {
+  KV_NEED(x, HQQ_ERR_INVALID_ARGUMENT, "args must not be NULL");
+  hqq::kv::ForkArgs a{};
+  int st = check_layers(x->layers, &a.f, &a.b, &a.layers);
+  if (st != HQQ_OK) return st;
+  st = check_sequences(x->num_seqs, x->page_table, x->table_stride, x->table_cols, x->seq_lens, x->layers.cache.page_size, &a.seqs);
+  if (st != HQQ_OK) return st;
+  KV_NEED(x->num_new >= 0 && x->new_stride >= x->table_cols, HQQ_ERR_INVALID_ARGUMENT, "num_new or new_stride out of range");
+  KV_NEED(x->num_new == 0 || x->num_seqs > 0, HQQ_ERR_INVALID_ARGUMENT, "children without a sequence");
+  KV_NEED(x->num_new <= 65535, HQQ_ERR_UNSUPPORTED, "at most 65535 sequences in a call");
+  if (x->num_new == 0) return HQQ_OK;
+  KV_NEED(x->parents && aligned4(x->parents) && x->fresh && aligned4(x->fresh) && (x->new_table || x->table_cols == 0) &&
+              aligned4(x->new_table) && x->new_lens && aligned4(x->new_lens),
+          HQQ_ERR_INVALID_ARGUMENT, "parents, fresh, new_table and new_lens must be 4-byte aligned pointers");
+  a.num_layers = x->layers.num_layers;
+  a.num_new = (int)x->num_new;
+  a.parents = x->parents;
+  a.fresh = x->fresh;
+  a.new_table = x->new_table;
+  a.new_stride = x->new_stride;
+  a.new_lens = x->new_lens;
+  return device_status(hqq::kv::launch_fork(a, static_cast<hipStream_t>(x->stream)));
+}
+
+size_t hqq_kv_compact_workspace_bytes(int64_t num_pages) {
+  return num_pages < 1 || num_pages > hqq::kv::kMostPages ? 0 : 4 * (size_t)hqq::kv::compact_words(num_pages);
+}
+
+int hqq_kv_compact(const hqq_kv_compact_args* x) {
+  KV_NEED(x, HQQ_ERR_INVALID_ARGUMENT, "args must not be NULL");
+  hqq::kv::CompactArgs a{};
+  Bytes b;
+  int st = check_layers(x->layers, &a.f, &b, &a.layers);
+  if (st != HQQ_OK) return st;
+  KV_NEED(a.f.num_pages <= hqq::kv::kMostPages, HQQ_ERR_UNSUPPORTED, "at most 2^20 pages");
+  st = check_sequences(x->num_seqs, x->page_table, x->table_stride, x->table_cols, x->seq_lens, x->layers.cache.page_size, &a.seqs);
+  if (st != HQQ_OK) return st;
+  KV_NEED(x->new_stride >= x->table_cols, HQQ_ERR_INVALID_ARGUMENT, "new_stride out of range");
+  KV_NEED((x->new_table || x->table_cols == 0 || x->num_seqs == 0) && aligned4(x->new_table) && x->used && aligned4(x->used),
+          HQQ_ERR_INVALID_ARGUMENT, "new_table and used must be 4-byte aligned pointers");
+  KV_NEED(x->workspace && x->workspace_bytes >= hqq_kv_compact_workspace_bytes(a.f.num_pages), HQQ_ERR_WORKSPACE,
+          "workspace missing or smaller than hqq_kv_compact_workspace_bytes");
+  KV_NEED(aligned16(x->workspace), HQQ_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
+  a.num_layers = x->layers.num_layers;
+  a.new_table = x->new_table;
+  a.new_stride = x->new_stride;
+  a.used = x->used;
+  a.workspace = static_cast<int32_t*>(x->workspace);
+  return device_status(hqq::kv::launch_compact(a, static_cast<hipStream_t>(x->stream)));
+}
+
+}  // extern "C"

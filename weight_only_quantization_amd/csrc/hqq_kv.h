@@ -58,6 +58,7 @@ struct KeyList {
   const int32_t* cu_q;
   int num_seqs, tq, max_q;
   int causal;
+  int tree;  // the last tq keys are seen by AttnArgs::mask
   // where the partial results of its rows begin (in rows of part_o), and their layout: the stream's
   // segments of `cap` rows, or by row
   int64_t part0;
@@ -79,6 +80,8 @@ struct AttnArgs {
   int joined;        // partial results of both lists meet in the join: no row is finished before it
   int first_list, lists;  // stream: the lists of this launch
   int blocks;             // stream: blocks that share the work of the launch; 0: a block a pair
+  const uint32_t* mask;   // drafts that a query token sees: mask_words words a token
+  int mask_words;
   void* out;
   float* lse;
   float* part_o;    // [rows][D], not divided by the sum
@@ -96,6 +99,9 @@ enum StreamMode { kShares, kSharesOnce, kWhole8, kWhole4 };
 StreamMode stream_mode(const AttnArgs& a, int nt);
 // Tiles of 256 rows of list `which`.
 hipError_t launch_kv_tile(const AttnArgs& a, int which, int D, int bits, int gs, hipStream_t st);
+// Both for calls whose own list ends in drafted tokens.
+hipError_t launch_kv_stream_tree(const AttnArgs& a, int D, int bits, int gs, int nt, hipStream_t st);
+hipError_t launch_kv_tile_tree(const AttnArgs& a, int which, int D, int bits, int gs, hipStream_t st);
 // Joins the partial results of every row; nt: of the stream's lists.
 hipError_t launch_kv_join(const AttnArgs& a, int D, int nt_own, int nt_prefix, hipStream_t st);
 
@@ -187,6 +193,13 @@ __device__ __forceinline__ Sequence sequence_of(const AttnArgs& a, const KeyList
   }
   s.len = min(min(max(s.len, 0), l.max_len), l.table_cols << a.f.page_shift);
   return s;
+}
+
+// Of a query token's mask the 32 bits from draft d on, which may lie in front of the first one: those keys are seen.
+__device__ __forceinline__ uint32_t drafts_seen(const uint32_t* row, int words, int d) {
+  const int w = d >> 5;
+  const uint32_t lo = w < 0 ? ~0u : w < words ? row[w] : 0u, hi = w + 1 < 0 ? ~0u : w + 1 < words ? row[w + 1] : 0u;
+  return __builtin_amdgcn_alignbit(hi, lo, d & 31);
 }
 
 // Page id and address of a slot; nullptr where the slot is outside the cache.

@@ -2,61 +2,12 @@
 // of key splits, the workspace.  Every check happens before anything is enqueued.
 #include <math.h>
 
-#include "hqq_internal.h"
-#include "hqq_kv.h"
+#include "hqq_kv_checks.h"
 
 namespace {
 
-using hqq::api_fail;
 using hqq::kv::AttnArgs;
-using hqq::kv::Format;
 using hqq::kv::KeyList;
-
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int device_status(hipError_t e) {
-  return e == hipSuccess ? HQQ_OK : api_fail(HQQ_ERR_DEVICE, hipGetErrorString(e));
-}
-
-#define KV_NEED(cond, status, message) \
-  do {                                 \
-    if (!(cond)) return api_fail(status, message); \
-  } while (0)
-
-int64_t block_bytes(int D, int bits, int gs, int page) { return (int64_t)page * 2 * (D * bits / 8 + 4 * (D / gs)); }
-
-int check_format(int hkv, int D, int bits, int gs, int page) {
-  KV_NEED(hkv > 0 && D > 0 && gs > 0 && page > 0, HQQ_ERR_INVALID_ARGUMENT, "cache sizes must be positive");
-  KV_NEED(bits > 0 && bits <= 8, HQQ_ERR_INVALID_ARGUMENT, "nbits must be 4 or 8");
-  KV_NEED(D == 64 || D == 128, HQQ_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
-  KV_NEED(bits == 4 || bits == 8, HQQ_ERR_UNSUPPORTED, "nbits must be 4 or 8");
-  KV_NEED((gs == 32 || gs == 64 || gs == 128) && gs <= D, HQQ_ERR_UNSUPPORTED,
-          "group_size must be 32, 64 or 128 and at most head_dim");
-  KV_NEED(page == 16 || page == 32 || page == 64 || page == 128 || page == 256, HQQ_ERR_UNSUPPORTED,
-          "page_size must be 16, 32, 64, 128 or 256");
-  KV_NEED(hkv <= 4096, HQQ_ERR_UNSUPPORTED, "at most 4096 KV heads");
-  return HQQ_OK;
-}
-
-int check_cache(const hqq_kv_cache& c, Format* f) {
-  const int st = check_format(c.num_kv_heads, c.head_dim, c.nbits, c.group_size, c.page_size);
-  if (st != HQQ_OK) return st;
-  KV_NEED(c.pages && aligned16(c.pages), HQQ_ERR_INVALID_ARGUMENT, "pages must be a 16-byte aligned pointer");
-  KV_NEED(c.num_pages >= 1 && c.num_pages <= INT32_MAX, HQQ_ERR_INVALID_ARGUMENT, "num_pages must be 1 .. 2^31-1");
-  f->pages = static_cast<uint8_t*>(c.pages);
-  f->num_pages = (uint32_t)c.num_pages;
-  f->hkv = c.num_kv_heads;
-  f->page_shift = __builtin_ctz(c.page_size);
-  f->block_bytes = block_bytes(c.head_dim, c.nbits, c.group_size, c.page_size);
-  f->page_bytes = f->block_bytes * c.num_kv_heads;
-  return HQQ_OK;
-}
-
-// A launch dimension takes fewer than 2^32 threads.
-constexpr int64_t kThreads = (int64_t(1) << 32) - 512;
-
-bool known_type(int dtype) { return dtype == HQQ_KV_F16 || dtype == HQQ_KV_BF16; }
 
 // Most keys of a list.  The kernels count keys in 32 bits and look ahead of the last one: four steps of 256 keys in
 // the stream, two tiles of 128 in the tiles, whose splits end up to 256 * 128 keys past it.
@@ -122,7 +73,7 @@ int stream_grid(const Plan& p, const hqq_kv_cache& c, int first, int lists) {
   return (int)(n > most ? most : n < 1 ? 1 : n);
 }
 
-int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
+int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p, bool tree = false) {
   Format f{};
   const hqq_kv_cache& c = x->cache;
   if (sizes_only) {
@@ -176,7 +127,8 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p) {
   own.num_seqs = (int)x->num_seqs;
   own.tq = x->num_seqs ? (int)(x->total_q / x->num_seqs) : 0;
   own.max_q = x->cu_q ? (int)x->max_q : own.tq;
-  own.causal = x->causal;
+  own.causal = tree ? 0 : x->causal;
+  own.tree = tree;
   if (x->total_q == 0 || x->num_seqs == 0 || own.max_q == 0) return HQQ_OK;
   KV_NEED(x->num_seqs <= 65535, HQQ_ERR_UNSUPPORTED, "at most 65535 sequences in a call");
   KeyList& pre = a.list[1];
@@ -257,11 +209,15 @@ hipError_t each_launch(Plan* p, const hqq_kv_cache& c, F launch) {
   return e;
 }
 
-int run_attention(const hqq_kv_attention_args* x) {
+int run_attention(const hqq_kv_attention_args* x, const hqq_kv_tree_args* tree = nullptr) {
   Plan p;
-  const int st = plan_attention(x, false, &p);
+  const int st = plan_attention(x, false, &p, tree);
   if (st != HQQ_OK) return st;
   AttnArgs& a = p.a;
+  if (tree) {
+    KV_NEED(tree->mask_words >= 1 && tree->mask_words <= kMostDrafts / 64, HQQ_ERR_INVALID_ARGUMENT, "mask_words must be 1 .. 64");
+    KV_NEED(a.list[0].max_q <= 64 * tree->mask_words, HQQ_ERR_INVALID_ARGUMENT, "a sequence has more query tokens than bits of its mask");
+  }
   if (x->total_q == 0 || a.list[0].max_q == 0) return HQQ_OK;
   const hqq_kv_cache& c = x->cache;
   KV_NEED(x->q && aligned16(x->q) && x->out && aligned16(x->out), HQQ_ERR_INVALID_ARGUMENT,
@@ -274,6 +230,11 @@ int run_attention(const hqq_kv_attention_args* x) {
   // (scalar loads drop the low address bits)
   KV_NEED(aligned4(x->seq_lens) && aligned4(x->page_table) && aligned4(x->cu_q) && aligned4(x->prefix_table) && aligned4(x->lse),
           HQQ_ERR_INVALID_ARGUMENT, "seq_lens, the page tables, cu_q and lse must be 4-byte aligned");
+  if (tree) {
+    KV_NEED(tree->mask && reinterpret_cast<uintptr_t>(tree->mask) % 8 == 0, HQQ_ERR_INVALID_ARGUMENT, "mask must be an 8-byte aligned pointer");
+    a.mask = reinterpret_cast<const uint32_t*>(tree->mask);
+    a.mask_words = 2 * (int)tree->mask_words;
+  }
   if (p.workspace) {
     KV_NEED(x->workspace && x->workspace_bytes >= p.workspace, HQQ_ERR_WORKSPACE,
             "workspace missing or smaller than hqq_kv_attention_workspace_bytes");
@@ -291,8 +252,8 @@ int run_attention(const hqq_kv_attention_args* x) {
   hipStream_t stream = static_cast<hipStream_t>(x->stream);
   const int D = c.head_dim, bits = c.nbits, gs = c.group_size;
   hipError_t e = each_launch(&p, c, [&](int i) {
-    return p.kind[i] == kTile ? hqq::kv::launch_kv_tile(a, i, D, bits, gs, stream)
-                              : hqq::kv::launch_kv_stream(a, D, bits, gs, nt_of(p.kind[i]), stream);
+    if (p.kind[i] == kTile) return (tree ? hqq::kv::launch_kv_tile_tree : hqq::kv::launch_kv_tile)(a, i, D, bits, gs, stream);
+    return (tree ? hqq::kv::launch_kv_stream_tree : hqq::kv::launch_kv_stream)(a, D, bits, gs, nt_of(p.kind[i]), stream);
   });
   if (e == hipSuccess && p.join) e = hqq::kv::launch_kv_join(a, D, nt_of(p.kind[0]), nt_of(p.kind[1]), stream);
   return device_status(e);
@@ -310,25 +271,8 @@ size_t hqq_kv_page_bytes(int num_kv_heads, int head_dim, int nbits, int group_si
 int hqq_kv_write(const hqq_kv_write_args* x) {
   KV_NEED(x, HQQ_ERR_INVALID_ARGUMENT, "args must not be NULL");
   hqq::kv::WriteArgs a{};
-  const int st = check_cache(x->cache, &a.f);
-  if (st != HQQ_OK) return st;
-  KV_NEED(known_type(x->dtype), HQQ_ERR_INVALID_ARGUMENT, "dtype must be HQQ_KV_F16 or HQQ_KV_BF16");
-  KV_NEED(x->n >= 0 && x->n <= (int64_t(1) << 30) / x->cache.num_kv_heads, HQQ_ERR_INVALID_ARGUMENT, "n out of range");
-  KV_NEED((x->n + 3) * x->cache.num_kv_heads * (x->cache.head_dim / 8) <= kThreads, HQQ_ERR_UNSUPPORTED,
-          "too many tokens in a call");
-  KV_NEED(!x->k_echo == !x->v_echo, HQQ_ERR_INVALID_ARGUMENT, "k_echo and v_echo go together");
-  if (x->n == 0) return HQQ_OK;
-  KV_NEED(x->k && x->v && x->slots, HQQ_ERR_INVALID_ARGUMENT, "k, v and slots must not be NULL");
-  KV_NEED(aligned16(x->k) && aligned16(x->v) && aligned16(x->k_echo) && aligned16(x->v_echo) &&
-              reinterpret_cast<uintptr_t>(x->slots) % 8 == 0,
-          HQQ_ERR_INVALID_ARGUMENT, "k, v and the echoes must be 16-byte aligned, slots 8-byte aligned");
-  KV_NEED(x->k_token_stride >= 0 && x->k_head_stride >= 0 && x->v_token_stride >= 0 && x->v_head_stride >= 0 &&
-              (x->k_token_stride | x->k_head_stride | x->v_token_stride | x->v_head_stride) % 8 == 0,
-          HQQ_ERR_INVALID_ARGUMENT, "strides must be non-negative multiples of 8 elements");
-  a.k = x->k, a.v = x->v, a.n = x->n;
-  a.k_ts = x->k_token_stride, a.k_hs = x->k_head_stride, a.v_ts = x->v_token_stride, a.v_hs = x->v_head_stride;
-  a.slots = x->slots;
-  a.k_echo = x->k_echo, a.v_echo = x->v_echo;
+  const int st = check_write(*x, &a);
+  if (st != HQQ_OK || x->n == 0) return st;
   return device_status(hqq::kv::launch_kv_write(a, x->cache.head_dim, x->cache.nbits, x->cache.group_size, x->dtype,
                                                 static_cast<hipStream_t>(x->stream)));
 }
@@ -367,6 +311,17 @@ int hqq_kv_attention(const hqq_kv_attention_args* x) {
 int hqq_kv_attention_shared(const hqq_kv_attention_args* x) {
   KV_NEED(x, HQQ_ERR_INVALID_ARGUMENT, "args must not be NULL");
   return run_attention(x);
+}
+
+size_t hqq_kv_attention_tree_workspace_bytes(const hqq_kv_tree_args* x) {
+  Plan p;
+  if (!x || plan_attention(&x->attention, true, &p, true) != HQQ_OK) return 0;
+  return p.workspace;
+}
+
+int hqq_kv_attention_tree(const hqq_kv_tree_args* x) {
+  KV_NEED(x, HQQ_ERR_INVALID_ARGUMENT, "args must not be NULL");
+  return run_attention(&x->attention, x);
 }
 
 int hqq_kv_attention_way(const hqq_kv_attention_args* x, int32_t way[7]) {

@@ -1,0 +1,84 @@
+// Checks that the entry points of the cache share, in front of any launch.
+#pragma once
+
+#include "hqq_internal.h"
+#include "hqq_draft.h"
+#include "hqq_kv.h"
+
+namespace {
+
+using hqq::api_fail;
+using hqq::kv::Format;
+using hqq::kv::kMostDrafts;
+
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+inline int device_status(hipError_t e) {
+  return e == hipSuccess ? HQQ_OK : api_fail(HQQ_ERR_DEVICE, hipGetErrorString(e));
+}
+
+#define KV_NEED(cond, status, message) \
+  do {                                 \
+    if (!(cond)) return api_fail(status, message); \
+  } while (0)
+
+inline int64_t block_bytes(int D, int bits, int gs, int page) { return (int64_t)page * 2 * (D * bits / 8 + 4 * (D / gs)); }
+
+inline int check_format(int hkv, int D, int bits, int gs, int page) {
+  KV_NEED(hkv > 0 && D > 0 && gs > 0 && page > 0, HQQ_ERR_INVALID_ARGUMENT, "cache sizes must be positive");
+  KV_NEED(bits > 0 && bits <= 8, HQQ_ERR_INVALID_ARGUMENT, "nbits must be 4 or 8");
+  KV_NEED(D == 64 || D == 128, HQQ_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  KV_NEED(bits == 4 || bits == 8, HQQ_ERR_UNSUPPORTED, "nbits must be 4 or 8");
+  KV_NEED((gs == 32 || gs == 64 || gs == 128) && gs <= D, HQQ_ERR_UNSUPPORTED,
+          "group_size must be 32, 64 or 128 and at most head_dim");
+  KV_NEED(page == 16 || page == 32 || page == 64 || page == 128 || page == 256, HQQ_ERR_UNSUPPORTED,
+          "page_size must be 16, 32, 64, 128 or 256");
+  KV_NEED(hkv <= 4096, HQQ_ERR_UNSUPPORTED, "at most 4096 KV heads");
+  return HQQ_OK;
+}
+
+inline int check_cache(const hqq_kv_cache& c, Format* f) {
+  const int st = check_format(c.num_kv_heads, c.head_dim, c.nbits, c.group_size, c.page_size);
+  if (st != HQQ_OK) return st;
+  KV_NEED(c.pages && aligned16(c.pages), HQQ_ERR_INVALID_ARGUMENT, "pages must be a 16-byte aligned pointer");
+  KV_NEED(c.num_pages >= 1 && c.num_pages <= INT32_MAX, HQQ_ERR_INVALID_ARGUMENT, "num_pages must be 1 .. 2^31-1");
+  f->pages = static_cast<uint8_t*>(c.pages);
+  f->num_pages = (uint32_t)c.num_pages;
+  f->hkv = c.num_kv_heads;
+  f->page_shift = __builtin_ctz(c.page_size);
+  f->block_bytes = block_bytes(c.head_dim, c.nbits, c.group_size, c.page_size);
+  f->page_bytes = f->block_bytes * c.num_kv_heads;
+  return HQQ_OK;
+}
+
+// A launch dimension takes fewer than 2^32 threads.
+constexpr int64_t kThreads = (int64_t(1) << 32) - 512;
+
+inline bool known_type(int dtype) { return dtype == HQQ_KV_F16 || dtype == HQQ_KV_BF16; }
+
+// hqq_kv_write's checks (HQQ_OK with n = 0: nothing to do).
+inline int check_write(const hqq_kv_write_args& x, hqq::kv::WriteArgs* a) {
+  const int st = check_cache(x.cache, &a->f);
+  if (st != HQQ_OK) return st;
+  KV_NEED(known_type(x.dtype), HQQ_ERR_INVALID_ARGUMENT, "dtype must be HQQ_KV_F16 or HQQ_KV_BF16");
+  KV_NEED(x.n >= 0 && x.n <= (int64_t(1) << 30) / x.cache.num_kv_heads, HQQ_ERR_INVALID_ARGUMENT, "n out of range");
+  KV_NEED((x.n + 3) * x.cache.num_kv_heads * (x.cache.head_dim / 8) <= kThreads, HQQ_ERR_UNSUPPORTED,
+          "too many tokens in a call");
+  KV_NEED(!x.k_echo == !x.v_echo, HQQ_ERR_INVALID_ARGUMENT, "k_echo and v_echo go together");
+  if (x.n == 0) return HQQ_OK;
+  KV_NEED(x.k && x.v && x.slots, HQQ_ERR_INVALID_ARGUMENT, "k, v and slots must not be NULL");
+  KV_NEED(aligned16(x.k) && aligned16(x.v) && aligned16(x.k_echo) && aligned16(x.v_echo) && aligned8(x.slots),
+          HQQ_ERR_INVALID_ARGUMENT, "k, v and the echoes must be 16-byte aligned, slots 8-byte aligned");
+  KV_NEED(x.k_token_stride >= 0 && x.k_head_stride >= 0 && x.v_token_stride >= 0 && x.v_head_stride >= 0 &&
+              (x.k_token_stride | x.k_head_stride | x.v_token_stride | x.v_head_stride) % 8 == 0,
+          HQQ_ERR_INVALID_ARGUMENT, "strides must be non-negative multiples of 8 elements");
+  a->k = x.k, a->v = x.v, a->n = x.n;
+  a->k_ts = x.k_token_stride, a->k_hs = x.k_head_stride, a->v_ts = x.v_token_stride, a->v_hs = x.v_head_stride;
+  a->slots = x.slots;
+  a->k_echo = x.k_echo, a->v_echo = x.v_echo;
+  return HQQ_OK;
+}
+
+}  // namespace

@@ -1,0 +1,381 @@
+// Drafted trees' masks and places, and moving what the cache holds: accepted drafts, forked sequences, pages of a pool with holes.
+//
+// The moves are exact copies of bytes, of all layers in one launch (the layers' addresses travel in the kernel's arguments),
+// bound by memory where there is much to move and else by the chain length -> page -> bytes -> store, three trips to memory.
+#include "hqq_draft.h"
+
+namespace hqq {
+namespace kv {
+namespace {
+
+__device__ __forceinline__ int length_of(const Sequences& s, int seq, int page_shift) {
+  return (int)min((int64_t)max(s.lens[seq], 0), (int64_t)s.table_cols << page_shift);
+}
+
+// Drafts of a sequence: their first row and number; 0 where they leave the tensor.
+struct Drafts {
+  int first, count;
+};
+template <typename Args>
+__device__ __forceinline__ Drafts drafts_of(const Args& a, int seq) {
+  Drafts d{seq * a.tq, a.tq};
+  if (a.cu_q) {
+    d.first = a.cu_q[seq];
+    d.count = a.cu_q[seq + 1] - d.first;
+    if (d.first < 0 || d.count < 0 || d.count > a.max_q || (int64_t)d.first + d.count > a.total_q) d.count = 0;
+  }
+  return d;
+}
+
+// ---- masks, positions and slots of drafted trees: a block a sequence, a thread a draft, which walks up to its root.
+// Parents come before their children, so a row's words are finished from the last one down.
+__global__ __launch_bounds__(256) void k_tree_plan(TreePlanArgs a) {
+  __shared__ int sh_parent[kMostDrafts];
+  const int seq = blockIdx.x;
+  const Drafts d = drafts_of(a, seq);
+  const int base = length_of(a.seqs, seq, a.page_shift) - d.count;  // the cache holds the drafts already
+  for (int t = threadIdx.x; t < d.count; t += blockDim.x) {
+    const int p = a.parents[d.first + t];
+    sh_parent[t] = p >= 0 && p < t ? p : -1;
+  }
+  __syncthreads();
+  for (int t = threadIdx.x; t < d.count; t += blockDim.x) {
+    uint64_t* row = a.mask + (int64_t)(d.first + t) * a.words;
+    int depth = 0, at = t;
+    for (int w = a.words - 1; w >= 0; --w) {
+      uint64_t bits = 0;
+      while (at >= 64 * w) {  // (no draft: -1)
+        bits |= uint64_t(1) << (at & 63);
+        at = sh_parent[at];
+        ++depth;
+      }
+      row[w] = bits;
+    }
+    if (a.positions) a.positions[d.first + t] = (int64_t)base + depth - 1;
+    if (a.slots) {
+      const int pos = base + t, col = pos >> a.page_shift;
+      int64_t slot = -1;
+      if (pos >= 0 && col < a.seqs.table_cols) {
+        const int id = a.seqs.table[(int64_t)seq * a.seqs.table_stride + col];
+        if (id >= 0) slot = ((int64_t)id << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+      }
+      a.slots[d.first + t] = slot;
+    }
+  }
+}
+
+// ---- accepted drafts.  What a token has in a head's block is at most 8 pieces of 16 bytes (K codes), 16 of 2, 4 or 8 (V codes)
+// and 8 of 4 (metadata): half a wave a token and head, a piece a lane; a block takes 8 of them at a time and kAhead such
+// turns before it stores the first, since a token's new place may be another one's old place.  The accepted
+// drafts rise, so nothing that a later turn reads is stored by an earlier one.
+constexpr int kAhead = 8;
+
+// Byte offset and size of piece i of token t; size 0: none.
+struct Piece {
+  int at, size;
+};
+__device__ __forceinline__ Piece piece_of(const Bytes& b, int page, int t, int i) {
+  if (i < 8) return {t * b.row + 16 * i, 16 * i < b.row ? 16 : 0};
+  if (i < 24) return {page * b.row + (((t >> 2) * 16 + i - 8) * 4 + (t & 3)) * b.unit, b.unit};
+  return {2 * page * b.row + ((i - 24) * page + t) * 4, i - 24 < b.meta ? 4 : 0};
+}
+__device__ __forceinline__ u32x4 load_piece(const uint8_t* p, int size) {
+  u32x4 v = {0, 0, 0, 0};
+  if (size == 16) {
+    v = *reinterpret_cast<const u32x4*>(p);
+  } else if (size == 8) {
+    const u32x2 w = *reinterpret_cast<const u32x2*>(p);
+    v[0] = w[0], v[1] = w[1];
+  } else if (size == 4) {
+    v[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if (size == 2) {
+    v[0] = *reinterpret_cast<const uint16_t*>(p);
+  }
+  return v;
+}
+__device__ __forceinline__ void store_piece(uint8_t* p, int size, u32x4 v) {
+  if (size == 16)
+    *reinterpret_cast<u32x4*>(p) = v;
+  else if (size == 8)
+    *reinterpret_cast<u32x2*>(p) = u32x2{v[0], v[1]};
+  else if (size == 4)
+    *reinterpret_cast<uint32_t*>(p) = v[0];
+  else if (size == 2)
+    *reinterpret_cast<uint16_t*>(p) = (uint16_t)v[0];
+}
+
+__global__ __launch_bounds__(256) void k_accept(AcceptArgs a, int heads) {
+  const int seq = blockIdx.x, layer = blockIdx.y, head0 = blockIdx.z * heads;
+  const int here = min(heads, a.f.hkv - head0);
+  const Drafts d = drafts_of(a, seq);
+  const int len = length_of(a.seqs, seq, a.f.page_shift), base = len - d.count;
+  const int count = min(min(max(a.num_accepted[seq], 0), a.most), d.count);
+  if (layer == 0 && blockIdx.z == 0 && threadIdx.x == 0) a.new_lens[seq] = max(base + count, 0);
+  const int page = 1 << a.f.page_shift, piece = threadIdx.x & 31;
+  const int32_t* chosen = a.accepted + (int64_t)seq * a.accepted_stride;
+  const int32_t* table = a.seqs.table + (int64_t)seq * a.seqs.table_stride;
+  uint8_t* pages = a.layers.pages[layer];
+  // where the piece of the token at a position is; nullptr outside the cache
+  auto place = [&](int pos, int head, int* size) -> uint8_t* {
+    if (pos < 0 || pos >= len) return nullptr;
+    const uint32_t id = (uint32_t)table[pos >> a.f.page_shift];
+    if (id >= a.f.num_pages) return nullptr;
+    const Piece x = piece_of(a.b, page, pos & (page - 1), piece);
+    *size = x.size;
+    return pages + (int64_t)id * a.f.page_bytes + head * a.f.block_bytes + x.at;
+  };
+  const int pairs = count * here;  // of a token and a head, tokens in order
+  for (int p0 = 0; p0 < pairs; p0 += 8 * kAhead) {
+    u32x4 v[kAhead];
+    uint8_t* to[kAhead];
+    int size = 0;
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      to[k] = nullptr;
+      const int p = p0 + 8 * k + (threadIdx.x >> 5);
+      if (p >= pairs) continue;
+      const int j = p / here, head = head0 + p - j * here, from = chosen[j];
+      if (from == j || from < 0 || from >= d.count) continue;
+      const uint8_t* src = place(base + from, head, &size);
+      if (!src) continue;
+      to[k] = place(base + j, head, &size);
+      if (to[k]) v[k] = load_piece(src, size);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (to[k]) store_piece(to[k], size, v[k]);
+  }
+}
+
+// ---- forks.  A child is its parent's row of the page table; of children of one parent the first keeps the partly filled page (and
+// what the row holds behind it), the others get a copy of its tokens on a page of their own.
+__global__ __launch_bounds__(256) void k_fork(ForkArgs a) {
+  const int child = blockIdx.x, layer = blockIdx.y;
+  const int parent = a.parents[child];
+  const bool there = parent >= 0 && parent < a.seqs.count;
+  int before = 0;
+  for (int i = threadIdx.x; i < child; i += 256) before |= a.parents[i] == parent;
+  const bool first = !__syncthreads_or(before);
+  const int len = there ? length_of(a.seqs, parent, a.f.page_shift) : 0;
+  const int page = 1 << a.f.page_shift, last = len >> a.f.page_shift, used = len & (page - 1);
+  const int32_t* row = a.seqs.table + (int64_t)(there ? parent : 0) * a.seqs.table_stride;
+  const int fresh = a.fresh[child];
+  if (layer == 0 && blockIdx.z == 0) {
+    int32_t* to = a.new_table + (int64_t)child * a.new_stride;
+    for (int c = threadIdx.x; c < a.seqs.table_cols; c += 256) {
+      int id = -1;
+      if (there) id = first || c < last ? row[c] : c == last && used ? fresh : -1;
+      to[c] = id;
+    }
+    if (threadIdx.x == 0) a.new_lens[child] = len;
+  }
+  if (!there || first || used == 0) return;
+  const uint32_t from = (uint32_t)row[last];
+  if (from >= a.f.num_pages || (uint32_t)fresh >= a.f.num_pages || from == (uint32_t)fresh) return;
+  // the used tokens' part of each block, 16 bytes a thread: K codes, V codes and metadata of groups of four tokens (of the last
+  // group only the tokens that are there: the rest of the page stays as it is)
+  const int quads = (used + 3) / 4, nk = used * a.b.row / 16, nv = quads * a.b.row / 4, all = nk + nv + quads * a.b.meta;
+  const uint8_t* src = a.layers.pages[layer] + (int64_t)from * a.f.page_bytes;
+  uint8_t* dst = a.layers.pages[layer] + (int64_t)fresh * a.f.page_bytes;
+  const uint32_t total = (uint32_t)all * a.f.hkv, step = gridDim.z * 256;
+  constexpr int U = 4;
+  for (uint32_t i0 = blockIdx.z * 256 + threadIdx.x; i0 < total; i0 += U * step) {
+    u32x4 v[U];
+    int64_t at[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const uint32_t i = i0 + k * step;
+      at[k] = -1;
+      if (i >= total) continue;
+      const int head = i / (uint32_t)all, x = i - head * all;
+      int off, quad = 0, unit = 4;  // of a group of four tokens: which one, bytes of a token in one place
+      if (x < nk) {
+        off = 16 * x;
+      } else if (x < nk + nv) {
+        off = 16 * (x - nk);
+        quad = off / (4 * a.b.row), unit = a.b.unit;
+        off += page * a.b.row;
+      } else {
+        const int m = x - nk - nv, r = m / quads;
+        quad = m - r * quads;
+        off = 2 * page * a.b.row + r * 4 * page + 16 * quad;
+      }
+      at[k] = head * a.f.block_bytes + off;
+      v[k] = *reinterpret_cast<const u32x4*>(src + at[k]);
+      if (x >= nk && 4 * quad + 4 > used) {
+        const u32x4 old = *reinterpret_cast<const u32x4*>(dst + at[k]);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t low = 4 * quad + ((off + 4 * w) / unit & 3) < used ? 0xffffu : 0u;
+          const uint32_t high = 4 * quad + ((off + 4 * w + 2) / unit & 3) < used ? 0xffff0000u : 0u;
+          v[k][w] = (v[k][w] & (low | high)) | (old[w] & ~(low | high));
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (at[k] >= 0) *reinterpret_cast<u32x4*>(dst + at[k]) = v[k];
+  }
+}
+
+// ---- compaction.  One block finds the pages that the tables hold (a bit each in LDS), numbers the held ones past the first
+// U = (number of held pages) and the others below it, both in rising order, and writes down who moves where.
+__device__ __forceinline__ int held_columns(const Sequences& s, int seq, int page_shift) {
+  return (length_of(s, seq, page_shift) + (1 << page_shift) - 1) >> page_shift;
+}
+
+constexpr int kPlanThreads = 1024;
+__global__ __launch_bounds__(kPlanThreads) void k_compact_plan(CompactArgs a) {
+  __shared__ uint32_t bits[kMostPages / 32];
+  __shared__ int sh_wave[kPlanThreads / 64];
+  __shared__ int sh_low;  // held pages below U
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int pages = (int)a.f.num_pages, words = (pages + 31) / 32;
+  for (int w = tid; w < words; w += kPlanThreads) bits[w] = 0;
+  __syncthreads();
+  const int cols = a.seqs.table_cols, down = cols ? kPlanThreads / cols : 0, over = cols ? kPlanThreads % cols : 0;
+  int row = cols ? tid / cols : a.seqs.count, col = cols ? tid % cols : 0;
+  while (row < a.seqs.count) {
+    constexpr int U = 4;
+    uint32_t id[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      id[k] = ~0u;
+      if (row < a.seqs.count && col < held_columns(a.seqs, row, a.f.page_shift))
+        id[k] = (uint32_t)a.seqs.table[(int64_t)row * a.seqs.table_stride + col];
+      row += down, col += over;
+      if (col >= cols) col -= cols, ++row;
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (id[k] < (uint32_t)pages) atomicOr(&bits[id[k] >> 5], 1u << (id[k] & 31));
+  }
+  __syncthreads();
+  // held pages in front of each thread's words
+  const int per = (words + kPlanThreads - 1) / kPlanThreads, w0 = min(tid * per, words), w1 = min(w0 + per, words);
+  int own = 0;
+  for (int w = w0; w < w1; ++w) own += __popc(bits[w]);
+  int before = own;
+#pragma unroll
+  for (int i = 1; i < 64; i <<= 1) {
+    const int x = __shfl_up(before, i);
+    if (lane >= i) before += x;
+  }
+  if (lane == 63) sh_wave[wave] = before;
+  before -= own;
+  __syncthreads();
+  int held = 0;
+  for (int w = 0; w < kPlanThreads / 64; ++w) {
+    if (w < wave) before += sh_wave[w];
+    held += sh_wave[w];
+  }
+  if (tid == 0 && held >> 5 >= words) sh_low = held;  // (every page, and no word has bit U)
+  if (w0 <= held >> 5 && held >> 5 < w1) {
+    int n = before;
+    for (int w = w0; w < held >> 5; ++w) n += __popc(bits[w]);
+    sh_low = n + __popc(bits[held >> 5] & ((1u << (held & 31)) - 1));
+  }
+  __syncthreads();
+  const int low = sh_low, moves = held - low;
+  int32_t* from = a.workspace + kCompactHead;
+  int32_t* to = from + (pages + 1) / 2;
+  int32_t* place = to + (pages + 1) / 2;
+  if (tid == 0) a.workspace[0] = moves, a.workspace[1] = held, a.used[0] = held;
+  int n = before;
+  for (int w = w0; w < w1; ++w) {
+    const uint32_t b = bits[w];
+    const int p0 = 32 * w;
+    // pages of the word below U and the others
+    const uint32_t below = p0 + 32 <= held ? ~0u : p0 >= held ? 0u : (1u << (held - p0)) - 1;
+    uint32_t holes = ~b & below, far = b & ~below;
+    while (holes) {
+      const int i = __builtin_ctz(holes);
+      holes &= holes - 1;
+      to[p0 + i - n - __popc(b & ((1u << i) - 1))] = p0 + i;
+    }
+    while (far) {
+      const int i = __builtin_ctz(far);
+      far &= far - 1;
+      from[n + __popc(b & ((1u << i) - 1)) - low] = p0 + i;
+    }
+    n += __popc(b);
+  }
+  __syncthreads();
+  for (int i = tid; i < moves; i += kPlanThreads) place[from[i]] = to[i];
+}
+
+// The moves: a wave takes 4 KB of a page at a time, of all layers; and the tables' new entries.
+__global__ __launch_bounds__(256) void k_compact_move(CompactArgs a) {
+  constexpr int U = 4, kPart = U * 64 * 16;
+  const int moves = a.workspace[0], held = a.workspace[1];
+  const int32_t* from = a.workspace + kCompactHead;
+  const int32_t* to = from + ((int)a.f.num_pages + 1) / 2;
+  const int32_t* place = to + ((int)a.f.num_pages + 1) / 2;
+  const int lane = threadIdx.x & 63;
+  const uint32_t waves = gridDim.x * 4, wave = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t parts = (uint32_t)((a.f.page_bytes + kPart - 1) / kPart);
+  const uint64_t total = (uint64_t)moves * a.num_layers * parts;
+  for (uint64_t i = wave; i < total; i += waves) {
+    const uint64_t x = i / parts;
+    const uint32_t part = (uint32_t)(i - x * parts);
+    const int layer = (int)(x / (uint32_t)moves), m = (int)(x - (uint64_t)layer * moves);
+    uint8_t* pages = a.layers.pages[layer];
+    const uint8_t* src = pages + (int64_t)from[m] * a.f.page_bytes;
+    uint8_t* dst = pages + (int64_t)to[m] * a.f.page_bytes;
+    const int64_t at = (int64_t)part * kPart + 16 * lane;
+    u32x4 v[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (at + 1024 * k < a.f.page_bytes) v[k] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(src + at + 1024 * k));
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (at + 1024 * k < a.f.page_bytes) __builtin_nontemporal_store(v[k], reinterpret_cast<u32x4*>(dst + at + 1024 * k));
+  }
+  const uint64_t entries = (uint64_t)a.seqs.count * a.seqs.table_cols;
+  for (uint64_t i = blockIdx.x * 256 + threadIdx.x; i < entries; i += (uint64_t)gridDim.x * 256) {
+    const int row = (int)(i / (uint32_t)a.seqs.table_cols), col = (int)(i - (uint64_t)row * a.seqs.table_cols);
+    int id = -1;
+    if (col < held_columns(a.seqs, row, a.f.page_shift)) {
+      id = a.seqs.table[(int64_t)row * a.seqs.table_stride + col];
+      if ((uint32_t)id >= a.f.num_pages)
+        id = -1;
+      else if (id >= held)
+        id = place[id];
+    }
+    a.new_table[(int64_t)row * a.new_stride + col] = id;
+  }
+}
+
+}  // namespace
+
+hipError_t launch_tree_plan(const TreePlanArgs& a, hipStream_t st) {
+  k_tree_plan<<<a.seqs.count, a.max_q > 64 ? 256 : 64, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_accept(const AcceptArgs& a, hipStream_t st) {
+  // heads of a block: eight, whose moves of up to eight tokens are one turn; fewer where that leaves CUs without a block
+  int heads = 8;
+  while (heads > 1 && (int64_t)a.seqs.count * a.num_layers * ((a.f.hkv + heads - 1) / heads) < 512) heads /= 2;
+  k_accept<<<dim3(a.seqs.count, a.num_layers, (a.f.hkv + heads - 1) / heads), 256, 0, st>>>(a, heads);
+  return hipGetLastError();
+}
+
+hipError_t launch_fork(const ForkArgs& a, hipStream_t st) {
+  // blocks of a page: 16 KB each, more where there are few
+  const int64_t parts = (a.f.page_bytes + 16383) / 16384;
+  k_fork<<<dim3(a.num_new, a.num_layers, (unsigned)(parts > 64 ? 64 : parts)), 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_compact(const CompactArgs& a, hipStream_t st) {
+  k_compact_plan<<<1, kPlanThreads, 0, st>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  k_compact_move<<<2048, 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace kv
+}  // namespace hqq

@@ -44,6 +44,11 @@ class KvAttentionArgs(ctypes.Structure):
                 ("lse", _p), ("workspace", _p), ("workspace_bytes", ctypes.c_size_t), ("stream", _p)]
 
 
+class KvTreeArgs(ctypes.Structure):
+    """hqq_kv_tree_args of include/hqq.h."""
+    _fields_ = [("attention", KvAttentionArgs), ("mask", _p), ("mask_words", _i64)]
+
+
 # The same structures as packed bytes (native alignment; a nested hqq_kv_cache ends in 4 bytes of
 # padding): a call is a few microseconds, and filling a ctypes.Structure field by field would be a
 # good part of them.
@@ -51,7 +56,9 @@ _CACHE = "Pqiiiiixxxx"
 _WRITE = struct.Struct("@" + _CACHE + "iPPqqqqqPPPP")
 _READ = struct.Struct("@" + _CACHE + "iqPPPP")
 _ATTENTION = struct.Struct("@" + _CACHE + "iPqqqiqPqPqqPqifPqPPPNP")
-assert (_WRITE.size, _READ.size, _ATTENTION.size) == tuple(map(ctypes.sizeof, (KvWriteArgs, KvReadArgs, KvAttentionArgs)))
+_TREE = struct.Struct(_ATTENTION.format + "Pq")
+assert (_WRITE.size, _READ.size, _ATTENTION.size, _TREE.size) == tuple(
+    map(ctypes.sizeof, (KvWriteArgs, KvReadArgs, KvAttentionArgs, KvTreeArgs)))
 
 _fast = {}  # entry points that take packed bytes
 
@@ -62,11 +69,16 @@ def declare(lib):
     lib.hqq_kv_page_bytes.restype = ctypes.c_size_t
     for name, args in (("hqq_kv_write", KvWriteArgs), ("hqq_kv_read", KvReadArgs),
                        ("hqq_kv_attention", KvAttentionArgs), ("hqq_kv_attention_shared", KvAttentionArgs),
-                       ("hqq_kv_attention_workspace_bytes", KvAttentionArgs)):
-        fn = getattr(lib, name)
-        fn.argtypes = [ctypes.POINTER(args)]
-        fn.restype = ctypes.c_size_t if name.endswith("bytes") else _i32
-        _fast[name] = ctypes.CFUNCTYPE(fn.restype, ctypes.c_char_p)((name, lib))
+                       ("hqq_kv_attention_workspace_bytes", KvAttentionArgs), ("hqq_kv_attention_tree", KvTreeArgs),
+                       ("hqq_kv_attention_tree_workspace_bytes", KvTreeArgs)):
+        _declare(lib, name, args)
+
+
+def _declare(lib, name, args):
+    fn = getattr(lib, name)
+    fn.argtypes = [ctypes.POINTER(args)]
+    fn.restype = ctypes.c_size_t if name.endswith("bytes") else _i32
+    _fast[name] = ctypes.CFUNCTYPE(fn.restype, ctypes.c_char_p)((name, lib))
 
 
 def _entry(name):
@@ -175,6 +187,23 @@ def _stream(stream, t):
     return _torch()._C._cuda_getCurrentRawStream(t.get_device())
 
 
+def _together(first, *others):
+    """All tensors of a call on one device (None: left out)."""
+    at = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != at:
+            raise ValueError("the tensors of a call must be on one device, got %s and %s" % (first.device, t.device))
+
+
+def _call(name, packed, near):
+    """An entry point's status, called with the device of `near` current (a launch goes to the current one)."""
+    cuda = _torch().cuda
+    if near.get_device() == cuda.current_device():
+        return _entry(name)(packed)
+    with cuda.device(near.get_device()):
+        return _entry(name)(packed)
+
+
 def _empty(stream, shape, dtype, near):
     """A new tensor on the device of `near`, on the stream the kernels run on (see _on)."""
     if stream is None:
@@ -261,7 +290,7 @@ def hqq_kv_read(cache: KVCache, slots, dtype=None, out=None, stream=None):
 
 
 def hqq_kv_attention(cache: KVCache, q, page_table, seq_lens, scale=None, cu_q=None, max_q=None, max_len=None,
-                     causal: bool = True, out=None, return_lse: bool = False, workspace=None, stream=None, _prefix=None):
+                     causal: bool = True, out=None, return_lse: bool = False, workspace=None, stream=None, _prefix=None, _mask=None):
     """Attention of query tokens q [total_q, heads, head_dim] over their sequences' cached tokens.
 
     page_table int32 [num_seqs, pages] and seq_lens int32 [num_seqs] (cached tokens, the query tokens
@@ -316,15 +345,18 @@ def hqq_kv_attention(cache: KVCache, q, page_table, seq_lens, scale=None, cu_q=N
             most if max_len is None or max_len > most else max_len, 1 if causal else 0,
             dim ** -0.5 if scale is None else scale, prefix_at, prefix_len, out.data_ptr(), 0 if lse is None else lse.data_ptr())
     at = need = 0
+    form, tail, size = _ATTENTION, (), "hqq_kv_attention_workspace_bytes"
+    if _mask is not None:
+        form, tail, entry, size = _TREE, _mask, "hqq_kv_attention_tree", "hqq_kv_attention_tree_workspace_bytes"
     if workspace is None:
-        need = _entry("hqq_kv_attention_workspace_bytes")(_ATTENTION.pack(*head, 0, 0, handle))
+        need = _entry(size)(form.pack(*head, 0, 0, handle, *tail))
         if need:
             workspace = _empty(stream, need, torch.uint8, q)
             at = workspace.data_ptr()
     else:
         _pkg._need(workspace, "workspace", torch.uint8)
         at, need = workspace.data_ptr(), workspace.numel()
-    status = _entry(entry)(_ATTENTION.pack(*head, at, need, handle))
+    status = _entry(entry)(form.pack(*head, at, need, handle, *tail))
     if status:
         _pkg._check(status)
     return out if lse is None else (out, lse)
@@ -338,3 +370,17 @@ def hqq_kv_attention_shared(cache: KVCache, q, prefix_table, prefix_len: int, pa
     (page_table, seq_lens: without the prefix).  The prefix is read once for all rows together."""
     return hqq_kv_attention(cache, q, page_table, seq_lens, scale, cu_q, max_q, max_len, causal, out, return_lse,
                             workspace, stream, (prefix_table, prefix_len))
+
+
+def hqq_kv_attention_tree(cache: KVCache, q, mask, page_table, seq_lens, scale=None, cu_q=None, max_q=None, max_len=None,
+                          prefix_table=None, prefix_len: int = 0, out=None, return_lse: bool = False, workspace=None, stream=None):
+    """hqq_kv_attention (with a prefix hqq_kv_attention_shared) for trees of drafted tokens: of its sequence's last T cached tokens,
+    T its query tokens, query token i sees those whose bits are set in mask[i] (int64 [total_q, words], bit j of word j // 64:
+    draft j; hqq_kv_tree_plan makes it), and all tokens in front of them."""
+    tokens, words = _indices(mask, "mask", _torch().int64, 2)
+    if tokens != q.shape[0]:
+        raise ValueError("mask must be [%d, words], got %s" % (q.shape[0], tuple(mask.shape)))
+    _there(mask, "mask")
+    _together(q, mask, cache.pages, page_table, seq_lens, cu_q, prefix_table, out, workspace)
+    return hqq_kv_attention(cache, q, page_table, seq_lens, scale, cu_q, max_q, max_len, False, out, return_lse, workspace, stream,
+                            (prefix_table, prefix_len) if prefix_len else None, (mask.data_ptr(), words))

@@ -1,0 +1,219 @@
+"""Binding of drafted trees and of the cache's moves (``hqq_kv_tree_plan``, ``hqq_kv_accept``, ``hqq_kv_fork``,
+``hqq_kv_compact`` of ``include/hqq.h``)."""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+import weight_only_quantization_amd as _pkg
+
+from . import kv_cache as _kv
+
+HQQ_KV_MAX_LAYERS = 128
+
+_p, _i64, _i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+
+
+class KvTreePlanArgs(ctypes.Structure):
+    """hqq_kv_tree_plan_args of include/hqq.h."""
+    _fields_ = [("parents", _p), ("total_q", _i64), ("num_seqs", _i64), ("cu_q", _p), ("max_q", _i64), ("page_table", _p),
+                ("table_stride", _i64), ("table_cols", _i64), ("seq_lens", _p), ("page_size", _i32), ("mask", _p),
+                ("mask_words", _i64), ("positions", _p), ("slots", _p), ("stream", _p)]
+
+
+class KvLayersArgs(ctypes.Structure):
+    """hqq_kv_layers of include/hqq.h."""
+    _fields_ = [("cache", _kv.KvCacheArgs), ("pages", _p), ("num_layers", _i32)]
+
+
+class KvAcceptArgs(ctypes.Structure):
+    """hqq_kv_accept_args of include/hqq.h."""
+    _fields_ = [("layers", KvLayersArgs), ("num_seqs", _i64), ("total_q", _i64), ("cu_q", _p), ("max_q", _i64), ("page_table", _p),
+                ("table_stride", _i64), ("table_cols", _i64), ("seq_lens", _p), ("accepted", _p), ("accepted_stride", _i64),
+                ("max_accepted", _i64), ("num_accepted", _p), ("new_lens", _p), ("stream", _p)]
+
+
+class KvForkArgs(ctypes.Structure):
+    """hqq_kv_fork_args of include/hqq.h."""
+    _fields_ = [("layers", KvLayersArgs), ("num_seqs", _i64), ("page_table", _p), ("table_stride", _i64), ("table_cols", _i64),
+                ("seq_lens", _p), ("num_new", _i64), ("parents", _p), ("fresh", _p), ("new_table", _p), ("new_stride", _i64),
+                ("new_lens", _p), ("stream", _p)]
+
+
+class KvCompactArgs(ctypes.Structure):
+    """hqq_kv_compact_args of include/hqq.h."""
+    _fields_ = [("layers", KvLayersArgs), ("num_seqs", _i64), ("page_table", _p), ("table_stride", _i64), ("table_cols", _i64),
+                ("seq_lens", _p), ("new_table", _p), ("new_stride", _i64), ("used", _p), ("workspace", _p),
+                ("workspace_bytes", ctypes.c_size_t), ("stream", _p)]
+
+
+# (packed bytes for speed, as in kv_cache)
+_LAYERS = _kv._CACHE + "Pixxxx"
+_PLAN = struct.Struct("@PqqPqPqqPiPqPPP")
+_ACCEPT = struct.Struct("@" + _LAYERS + "qqPqPqqPPqqPPP")
+_FORK = struct.Struct("@" + _LAYERS + "qPqqPqPPPqPP")
+_COMPACT = struct.Struct("@" + _LAYERS + "qPqqPPqPPNP")
+assert (_PLAN.size, _ACCEPT.size, _FORK.size, _COMPACT.size) == tuple(
+    map(ctypes.sizeof, (KvTreePlanArgs, KvAcceptArgs, KvForkArgs, KvCompactArgs)))
+
+
+def declare(lib):
+    """Argument types of the entry points (called when the library is loaded)."""
+    for name, args in (("hqq_kv_tree_plan", KvTreePlanArgs), ("hqq_kv_accept", KvAcceptArgs), ("hqq_kv_fork", KvForkArgs),
+                       ("hqq_kv_compact", KvCompactArgs)):
+        _kv._declare(lib, name, args)
+    lib.hqq_kv_compact_workspace_bytes.argtypes = [_i64]
+    lib.hqq_kv_compact_workspace_bytes.restype = ctypes.c_size_t
+
+
+class KVLayers:
+    """The caches of a model's layers (KVCache of one format, number of pages and device), whose sequences share their page tables:
+    what the moves take.  Made once; it keeps the caches."""
+
+    def __init__(self, caches):
+        self.caches = list(caches)
+        if not 1 <= len(self.caches) <= HQQ_KV_MAX_LAYERS:
+            raise ValueError("1 .. %d layers are wanted, got %d" % (HQQ_KV_MAX_LAYERS, len(self.caches)))
+        fields = [c.args() for c in self.caches]
+        if any(f[1:] != fields[0][1:] for f in fields):
+            raise ValueError("the layers' caches must have one format and one number of pages")
+        _kv._together(*(c.pages for c in self.caches))
+        self.page_size, self.num_pages = self.caches[0].page_size, fields[0][1]
+        self._pages = (ctypes.c_void_p * len(fields))(*(f[0] for f in fields))
+        self._args = (0, *fields[0][1:], ctypes.addressof(self._pages), len(fields))
+
+
+def _layers(layers):
+    if isinstance(layers, KVLayers):
+        return layers
+    return KVLayers([layers] if isinstance(layers, _kv.KVCache) else layers)
+
+
+def _table(page_table, seq_lens):
+    """Sequences, columns and row stride of a page table and its lengths."""
+    torch = _kv._torch()
+    lens, = _kv._indices(seq_lens, "seq_lens", torch.int32, 1)
+    seqs, cols = _kv._indices(page_table, "page_table", torch.int32, 2)
+    if lens != seqs:
+        raise ValueError("seq_lens must be [num_seqs] = [%d], got [%d]" % (seqs, lens))
+    _kv._there(seq_lens, "seq_lens")
+    row, col = page_table.stride()
+    if not page_table.is_cuda or (col != 1 and cols > 1):
+        raise ValueError("page_table must be a CUDA (HIP) tensor [num_seqs, pages], each row contiguous")
+    return seqs, cols, row
+
+
+def _drafts(cu_q, seqs, max_q, total):
+    """Pointer and bound of the drafts' ranges."""
+    if cu_q is None:
+        return 0, 0
+    if _kv._indices(cu_q, "cu_q", _kv._torch().int32, 1)[0] != seqs + 1:
+        raise ValueError("cu_q must be [num_seqs + 1]")
+    _kv._there(cu_q, "cu_q")
+    return cu_q.data_ptr(), total if max_q is None or max_q > total else max_q
+
+
+def hqq_kv_tree_plan(parents, page_table, seq_lens, page_size: int, cu_q=None, max_q=None, stream=None):
+    """What a step on drafted trees needs, from the drafts' parents (int32 [total_q]: index within the sequence, smaller than the
+    draft's own; -1 behind the cached tokens).  page_table, seq_lens (the drafts included), cu_q and max_q as for
+    hqq_kv_attention.  Returns (mask int64 [total_q, words], positions int64 [total_q], slots int64 [total_q])."""
+    torch = _kv._torch()
+    total, = _kv._indices(parents, "parents", torch.int32, 1)
+    seqs, cols, row = _table(page_table, seq_lens)
+    cu, bound = _drafts(cu_q, seqs, max_q, total)
+    _kv._there(parents, "parents")
+    most = bound if cu_q is not None else total // seqs if seqs else 0
+    words = max(1, (most + 63) // 64)
+    mask = _kv._empty(stream, (total, words), torch.int64, parents)
+    positions = _kv._empty(stream, (total,), torch.int64, parents)
+    slots = _kv._empty(stream, (total,), torch.int64, parents)
+    _kv._together(parents, page_table, seq_lens, cu_q)
+    status = _kv._call("hqq_kv_tree_plan", _PLAN.pack(
+        parents.data_ptr(), total, seqs, cu, bound, page_table.data_ptr(), row, cols, seq_lens.data_ptr(), page_size, mask.data_ptr(),
+        words, positions.data_ptr(), slots.data_ptr(), _kv._stream(stream, parents)), parents)
+    if status:
+        _pkg._check(status)
+    return mask, positions, slots
+
+
+def hqq_kv_accept(layers, page_table, seq_lens, accepted, num_accepted, tokens=None, cu_q=None, max_q=None, stream=None):
+    """Moves the accepted drafts of each sequence together, in all layers (a KVLayers, or KVCaches).
+
+    Each sequence's last `tokens` cached tokens (with cu_q those of its range, at most max_q) are drafts; accepted int32
+    [num_seqs, most] lists the accepted ones, rising, num_accepted int32 [num_seqs] how many.  Returns the new lengths int32
+    [num_seqs]."""
+    torch = _kv._torch()
+    layers = _layers(layers)
+    seqs, cols, row = _table(page_table, seq_lens)
+    rows, most = _kv._indices(accepted, "accepted", torch.int32, 2)
+    if rows != seqs or _kv._indices(num_accepted, "num_accepted", torch.int32, 1)[0] != seqs:
+        raise ValueError("accepted must be [num_seqs, most] and num_accepted [num_seqs], num_seqs = %d" % seqs)
+    if cu_q is None:
+        if tokens is None or tokens < 0:
+            raise ValueError("tokens (drafts of a sequence) or cu_q is needed")
+        cu, bound, total = 0, 0, tokens * seqs
+    else:
+        # (rows of the drafts are not read here: their number bounds cu_q alone)
+        total = (1 << 30) if max_q is None else min(1 << 30, max_q * max(seqs, 1))
+        cu, bound = _drafts(cu_q, seqs, max_q, total)
+    _kv._there(accepted, "accepted")
+    _kv._there(num_accepted, "num_accepted")
+    lens = _kv._empty(stream, (seqs,), torch.int32, seq_lens)
+    _kv._together(layers.caches[0].pages, page_table, seq_lens, accepted, num_accepted, cu_q)
+    status = _kv._call("hqq_kv_accept", _ACCEPT.pack(
+        *layers._args, seqs, total, cu, bound, page_table.data_ptr(), row, cols, seq_lens.data_ptr(), accepted.data_ptr(), most, most,
+        num_accepted.data_ptr(), lens.data_ptr(), _kv._stream(stream, seq_lens)), seq_lens)
+    if status:
+        _pkg._check(status)
+    return lens
+
+
+def hqq_kv_fork(layers, page_table, seq_lens, parents, fresh, stream=None):
+    """Sequences that continue others, as in a beam search: child i continues sequence parents[i] (int32 [num_new], device; in any
+    order, repeated or left out).  Full pages are shared; of one parent's children the first keeps its partly filled page, the others get
+    a copy on page fresh[i] (int32 [num_new]: pages of no sequence), in all layers.  Returns the children's page table and
+    lengths (int32 [num_new, columns] and [num_new])."""
+    torch = _kv._torch()
+    layers = _layers(layers)
+    seqs, cols, row = _table(page_table, seq_lens)
+    new, = _kv._indices(parents, "parents", torch.int32, 1)
+    if _kv._indices(fresh, "fresh", torch.int32, 1)[0] != new:
+        raise ValueError("fresh must be [num_new] = [%d]" % new)
+    _kv._there(parents, "parents")
+    _kv._there(fresh, "fresh")
+    table = _kv._empty(stream, (new, cols), torch.int32, page_table)
+    lens = _kv._empty(stream, (new,), torch.int32, page_table)
+    _kv._together(layers.caches[0].pages, page_table, seq_lens, parents, fresh)
+    status = _kv._call("hqq_kv_fork", _FORK.pack(
+        *layers._args, seqs, page_table.data_ptr(), row, cols, seq_lens.data_ptr(), new, parents.data_ptr(), fresh.data_ptr(),
+        table.data_ptr(), cols, lens.data_ptr(), _kv._stream(stream, seq_lens)), seq_lens)
+    if status:
+        _pkg._check(status)
+    return table, lens
+
+
+def hqq_kv_compact(layers, page_table, seq_lens, workspace=None, stream=None):
+    """Moves the pages that sequences hold (of each row the first ceil(seq_len / page_size) columns) to the numbers 0 .. used - 1, in all
+    layers.  Returns the new page table (int32, -1 for what is not held) and used (int32 [1], device): pages from there on are free.
+    `workspace`: uint8, hqq_kv_compact_workspace_bytes(num_pages) bytes."""
+    torch = _kv._torch()
+    layers = _layers(layers)
+    seqs, cols, row = _table(page_table, seq_lens)
+    table = _kv._empty(stream, (seqs, cols), torch.int32, page_table)
+    used = _kv._empty(stream, (1,), torch.int32, page_table)
+    if workspace is None:
+        workspace = _kv._empty(stream, max(_pkg.load().hqq_kv_compact_workspace_bytes(layers.num_pages), 16), torch.uint8, page_table)
+    else:
+        _pkg._need(workspace, "workspace", torch.uint8)
+    _kv._together(layers.caches[0].pages, page_table, seq_lens, workspace)
+    status = _kv._call("hqq_kv_compact", _COMPACT.pack(
+        *layers._args, seqs, page_table.data_ptr(), row, cols, seq_lens.data_ptr(), table.data_ptr(), cols, used.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _kv._stream(stream, seq_lens)), seq_lens)
+    if status:
+        _pkg._check(status)
+    return table, used
+
+
+def hqq_kv_compact_workspace_bytes(num_pages: int) -> int:
+    """Bytes of hqq_kv_compact's workspace, 0 where there are too many pages."""
+    return _pkg.load().hqq_kv_compact_workspace_bytes(num_pages)

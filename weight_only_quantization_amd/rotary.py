@@ -1,0 +1,173 @@
+"""Binding of rotary positions (``hqq_rope*`` and ``hqq_kv_write_rope`` of ``include/hqq.h``)."""
+from __future__ import annotations
+
+import ctypes
+import struct
+from dataclasses import dataclass
+
+import weight_only_quantization_amd as _pkg
+
+from . import kv_cache as _kv
+
+HQQ_ROPE_HALVES, HQQ_ROPE_INTERLEAVED = 0, 1
+SCALINGS = {"none": 0, "linear": 1, "base": 2, "bands": 3}
+
+_p, _i64, _i32, _f64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_double
+
+
+class RopeForm(ctypes.Structure):
+    """hqq_rope_form of include/hqq.h."""
+    _fields_ = [("freqs", _p), ("rot_dim", _i32), ("layout", _i32), ("magnitude", _f64)]
+
+
+class RopeArgs(ctypes.Structure):
+    """hqq_rope_args of include/hqq.h."""
+    _fields_ = [("form", RopeForm), ("dtype", _i32), ("head_dim", _i32), ("backward", _i32), ("n", _i64), ("positions", _p),
+                ("q", _p), ("q_token_stride", _i64), ("q_head_stride", _i64), ("q_heads", _i32), ("q_out", _p),
+                ("q_out_token_stride", _i64), ("q_out_head_stride", _i64), ("k", _p), ("k_token_stride", _i64),
+                ("k_head_stride", _i64), ("k_heads", _i32), ("k_out", _p), ("k_out_token_stride", _i64),
+                ("k_out_head_stride", _i64), ("stream", _p)]
+
+
+class KvWriteRopeArgs(ctypes.Structure):
+    """hqq_kv_write_rope_args of include/hqq.h."""
+    _fields_ = [("write", _kv.KvWriteArgs), ("form", RopeForm), ("positions", _p), ("q", _p), ("q_token_stride", _i64),
+                ("q_head_stride", _i64), ("q_heads", _i32), ("q_out", _p), ("q_out_token_stride", _i64),
+                ("q_out_head_stride", _i64)]
+
+
+# (packed bytes for speed, as in kv_cache)
+_FORM, _HEADS = "Piid", "PqqiPqq"
+_ROPE = struct.Struct("@" + _FORM + "iiiqP" + _HEADS + _HEADS + "P")
+_WRITE_ROPE = struct.Struct("@" + _kv._CACHE + "iPPqqqqqPPPP" + _FORM + "P" + _HEADS)
+assert (_ROPE.size, _WRITE_ROPE.size) == (ctypes.sizeof(RopeArgs), ctypes.sizeof(KvWriteRopeArgs))
+
+_NO_HEADS = (0, 0, 0, 0, 0, 0, 0)
+
+
+def declare(lib):
+    """Argument types of the entry points (called when the library is loaded)."""
+    lib.hqq_rope_frequencies.argtypes = [_i32, _f64, _i32, _f64, _f64, _f64, _f64, _p, _p]
+    lib.hqq_rope_frequencies.restype = _i32
+    for name, args in (("hqq_rope", RopeArgs), ("hqq_kv_write_rope", KvWriteRopeArgs)):
+        _kv._declare(lib, name, args)
+
+
+@dataclass
+class RopeTable:
+    """How heads are turned: `freqs`, a contiguous float64 device tensor of rot_dim / 2 radians per position; the pairs'
+    layout; the magnitude that the rotation is scaled by."""
+    freqs: "object"
+    interleaved: bool = False
+    magnitude: float = 1.0
+
+    def args(self):
+        """The fields of hqq_rope_form, checked."""
+        f = self.freqs
+        if f.dtype is not _kv._torch().float64 or f.dim() != 1:
+            raise ValueError("freqs must be a 1-D torch.float64 tensor, got %s %s" % (f.dtype, tuple(f.shape)))
+        _kv._there(f, "freqs")
+        return f.data_ptr(), 2 * f.shape[0], 1 if self.interleaved else 0, self.magnitude
+
+
+def hqq_rope_table(rot_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none", factor: float = 1.0,
+                   original_len: float = 0.0, fast: float = 32.0, slow: float = 1.0, device="cuda") -> RopeTable:
+    """Frequencies base^(-2 i / rot_dim) of rot_dim turned channels, for a context `factor` times the trained one scaled by "linear"
+    (all of them slower), "base" (the base raised) or "bands" (by how often a pair turns over original_len positions: from `fast`
+    turns on kept, up to `slow` turns slowed by the factor; it also sets the magnitude)."""
+    torch = _kv._torch()
+    if scaling not in SCALINGS:
+        raise ValueError("scaling must be one of %s, got %r" % (", ".join(SCALINGS), scaling))
+    f = torch.empty(max(rot_dim // 2, 1), dtype=torch.float64)
+    m = ctypes.c_double()
+    _pkg._check(_pkg.load().hqq_rope_frequencies(rot_dim, base, SCALINGS[scaling], factor, original_len, fast, slow, f.data_ptr(),
+                                                 ctypes.addressof(m)))
+    return RopeTable(f.to(device), interleaved, m.value)
+
+
+def _strided(t, name, n, dtype):
+    """Pointer, strides and heads of x [n, heads, dim] (channels contiguous)."""
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != n:
+        raise ValueError("%s must be [%d, heads, head_dim], got %s" % (name, n, tuple(shape)))
+    if t.dtype is not dtype:
+        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    token, head = _kv._strides(t, name, shape[1], shape[2])
+    return t.data_ptr(), token, head, shape[1]
+
+
+def _out(t, given, name, stream):
+    """The output for t: given (t's shape and type, t itself for in place) or new, its pointer and strides."""
+    if given is None:
+        given = _kv._like(stream, t)
+    elif given.shape != t.shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(t.shape), tuple(given.shape)))
+    at, token, head, _ = _strided(given, name, t.shape[0], t.dtype)
+    return given, (at, token, head)
+
+
+def hqq_rope(q, positions, rope: RopeTable, k=None, backward: bool = False, out=None, stream=None):
+    """Turns q [n, heads, head_dim] (and k, of as many tokens) by their tokens' positions (int64 [n]): fp16 or bf16, token and head
+    strides allowed, head_dim a multiple of 16.  backward: the transposed rotation, dL/dx from dL/dy.  Returns the
+    turned q, with k (q, k); `out` (q or (q, k)) takes them instead of new tensors and may be the input itself."""
+    dtype, n = q.dtype, q.shape[0]
+    code = _kv._codes.get(dtype)
+    if code is None:
+        code = _kv._dtype_code(dtype)
+    count, = _kv._indices(positions, "positions", _kv._torch().int64, 1)
+    if count != n:
+        raise ValueError("positions must be [%d], got [%d]" % (n, count))
+    at, qt, qh, heads = _strided(q, "q", n, dtype)
+    kargs = _NO_HEADS
+    if out is not None and k is not None and len(out) != 2:
+        raise ValueError("out must be (q, k)")
+    qo, to = _out(q, out if k is None or out is None else out[0], "out", stream)
+    ko = None
+    if k is not None:
+        if k.dim() != 3 or k.shape[2] != q.shape[2]:
+            raise ValueError("k must be [%d, heads, %d], got %s" % (n, q.shape[2], tuple(k.shape)))
+        kat, kt, kh, kheads = _strided(k, "k", n, dtype)
+        ko, kto = _out(k, None if out is None else out[1], "out", stream)
+        kargs = (kat, kt, kh, kheads, *kto)
+    _kv._there(positions, "positions")
+    _kv._together(q, positions, rope.freqs, qo, k, ko)
+    status = _kv._call("hqq_rope", _ROPE.pack(*rope.args(), code, q.shape[2], 1 if backward else 0, n, positions.data_ptr(), at, qt,
+                                              qh, heads, *to, *kargs, _kv._stream(stream, q)), q)
+    if status:
+        _pkg._check(status)
+    return qo if k is None else (qo, ko)
+
+
+def hqq_kv_write_rope(cache, q, k, v, positions, slots, rope: RopeTable, echo: bool = False, out=None, stream=None):
+    """hqq_rope of q and k and hqq_kv_write of the turned keys and of v, in one launch and with their bits.  Returns the turned q;
+    with `echo` (q, k, v), k and v as the values that the cache now stands for.  `out` takes q (it may be q itself)."""
+    torch = _kv._torch()
+    count, = _kv._indices(slots, "slots", torch.int64, 1)
+    dtype, n = k.dtype, k.shape[0]
+    code = _kv._codes.get(dtype)
+    if code is None:
+        code = _kv._dtype_code(dtype)
+    if v.dtype is not dtype or q.dtype is not dtype:
+        raise ValueError("q, k and v must have one dtype, got %s, %s and %s" % (q.dtype, dtype, v.dtype))
+    if v.shape[0] != n or count != n or _kv._indices(positions, "positions", torch.int64, 1)[0] != n:
+        raise ValueError("q, k, v, positions and slots must have the same number of tokens")
+    heads, dim = cache.num_kv_heads, cache.head_dim
+    kt, kh = _kv._strides(k, "k", heads, dim)
+    vt, vh = _kv._strides(v, "v", heads, dim)
+    at, qt, qh, q_heads = _strided(q, "q", n, dtype)
+    if q.shape[2] != dim:
+        raise ValueError("q must be [%d, heads, %d], got %s" % (n, dim, tuple(q.shape)))
+    qo, to = _out(q, out, "out", stream)
+    _kv._there(slots, "slots")
+    _kv._there(positions, "positions")
+    ke = ve = None
+    if echo:
+        ke = _kv._like(stream, k)
+        ve = _kv._like(stream, ke)
+    _kv._together(k, v, slots, cache.pages, q, qo, positions, rope.freqs)
+    status = _kv._call("hqq_kv_write_rope", _WRITE_ROPE.pack(
+        *cache.args(), code, k.data_ptr(), v.data_ptr(), n, kt, kh, vt, vh, slots.data_ptr(), ke.data_ptr() if echo else 0,
+        ve.data_ptr() if echo else 0, _kv._stream(stream, k), *rope.args(), positions.data_ptr(), at, qt, qh, q_heads, *to), k)
+    if status:
+        _pkg._check(status)
+    return (qo, ke, ve) if echo else qo
