@@ -36,8 +36,8 @@ struct WriteRopeArgs {
 };
 
 constexpr int kMostRopeDim = 1024;
-// Tokens of a block.
-inline int rope_tokens(int head_dim) { return 64 / (head_dim / 16); }
+// Tokens of a block: four, or as many as a table of 512 pairs takes.
+inline int rope_tokens(int head_dim) { return head_dim <= 256 ? 4 : head_dim <= 512 ? 2 : 1; }
 inline int write_rope_tokens(int head_dim) { return 64 / (head_dim / 8); }
 hipError_t launch_rope(const RopeArgs& a, int dtype, bool interleaved, hipStream_t st);
 hipError_t launch_write_rope(const WriteRopeArgs& a, int D, int bits, int gs, int dtype, bool interleaved, hipStream_t st);

@@ -104,7 +104,11 @@ __device__ __forceinline__ void store_piece(uint8_t* p, int size, u32x4 v) {
     *reinterpret_cast<uint16_t*>(p) = (uint16_t)v[0];
 }
 
+// The tokens' places are looked up first, a thread a token, so that no piece waits for a chain of its own.
+constexpr int kChosen = 256;
+
 __global__ __launch_bounds__(256) void k_accept(AcceptArgs a, int heads) {
+  __shared__ int sh_id[2][kChosen], sh_token[2][kChosen];  // from, to: page (-1: nothing to move) and token of the page
   const int seq = blockIdx.x, layer = blockIdx.y, head0 = blockIdx.z * heads;
   const int here = min(heads, a.f.hkv - head0);
   const Drafts d = drafts_of(a, seq);
@@ -115,36 +119,40 @@ __global__ __launch_bounds__(256) void k_accept(AcceptArgs a, int heads) {
   const int32_t* chosen = a.accepted + (int64_t)seq * a.accepted_stride;
   const int32_t* table = a.seqs.table + (int64_t)seq * a.seqs.table_stride;
   uint8_t* pages = a.layers.pages[layer];
-  // where the piece of the token at a position is; nullptr outside the cache
-  auto place = [&](int pos, int head, int* size) -> uint8_t* {
-    if (pos < 0 || pos >= len) return nullptr;
-    const uint32_t id = (uint32_t)table[pos >> a.f.page_shift];
-    if (id >= a.f.num_pages) return nullptr;
-    const Piece x = piece_of(a.b, page, pos & (page - 1), piece);
-    *size = x.size;
-    return pages + (int64_t)id * a.f.page_bytes + head * a.f.block_bytes + x.at;
-  };
-  const int pairs = count * here;  // of a token and a head, tokens in order
-  for (int p0 = 0; p0 < pairs; p0 += 8 * kAhead) {
-    u32x4 v[kAhead];
-    uint8_t* to[kAhead];
-    int size = 0;
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      to[k] = nullptr;
-      const int p = p0 + 8 * k + (threadIdx.x >> 5);
-      if (p >= pairs) continue;
-      const int j = p / here, head = head0 + p - j * here, from = chosen[j];
-      if (from == j || from < 0 || from >= d.count) continue;
-      const uint8_t* src = place(base + from, head, &size);
-      if (!src) continue;
-      to[k] = place(base + j, head, &size);
-      if (to[k]) v[k] = load_piece(src, size);
+  const int size = piece_of(a.b, page, 0, piece).size;
+  for (int j0 = 0; j0 < count; j0 += kChosen) {
+    if (j0) __syncthreads();
+    const int j = j0 + threadIdx.x;
+    if (j < count) {
+      const int from = chosen[j], src = base + from, dst = base + j;
+      int id = -1, to = -1;
+      if (from != j && from >= 0 && from < d.count && src >= 0 && dst >= 0 && src < len && dst < len) {
+        id = table[src >> a.f.page_shift], to = table[dst >> a.f.page_shift];
+        if ((uint32_t)id >= a.f.num_pages || (uint32_t)to >= a.f.num_pages) id = -1;
+      }
+      sh_id[0][threadIdx.x] = id, sh_id[1][threadIdx.x] = to;
+      sh_token[0][threadIdx.x] = src & (page - 1), sh_token[1][threadIdx.x] = dst & (page - 1);
     }
     __syncthreads();
+    const int pairs = min(count - j0, kChosen) * here;  // of a token and a head, tokens in order
+    for (int p0 = 0; p0 < pairs; p0 += 8 * kAhead) {
+      u32x4 v[kAhead];
+      uint8_t* to[kAhead];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-      if (to[k]) store_piece(to[k], size, v[k]);
+      for (int k = 0; k < kAhead; ++k) {
+        to[k] = nullptr;
+        const int p = p0 + 8 * k + (threadIdx.x >> 5);
+        if (p >= pairs || size == 0) continue;
+        const int j = p / here, head = head0 + p - j * here, id = sh_id[0][j];
+        if (id < 0) continue;
+        v[k] = load_piece(pages + (int64_t)id * a.f.page_bytes + head * a.f.block_bytes + piece_of(a.b, page, sh_token[0][j], piece).at, size);
+        to[k] = pages + (int64_t)sh_id[1][j] * a.f.page_bytes + head * a.f.block_bytes + piece_of(a.b, page, sh_token[1][j], piece).at;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+        if (to[k]) store_piece(to[k], size, v[k]);
+    }
   }
 }
 
@@ -179,7 +187,7 @@ __global__ __launch_bounds__(256) void k_fork(ForkArgs a) {
   const uint8_t* src = a.layers.pages[layer] + (int64_t)from * a.f.page_bytes;
   uint8_t* dst = a.layers.pages[layer] + (int64_t)fresh * a.f.page_bytes;
   const uint32_t total = (uint32_t)all * a.f.hkv, step = gridDim.z * 256;
-  constexpr int U = 4;
+  constexpr int U = 8;
   for (uint32_t i0 = blockIdx.z * 256 + threadIdx.x; i0 < total; i0 += U * step) {
     u32x4 v[U];
     int64_t at[U];
@@ -363,8 +371,8 @@ hipError_t launch_accept(const AcceptArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_fork(const ForkArgs& a, hipStream_t st) {
-  // blocks of a page: 16 KB each, more where there are few
-  const int64_t parts = (a.f.page_bytes + 16383) / 16384;
+  // blocks of a page: 64 KB each, half of which is used on average: eight loads in flight a thread
+  const int64_t parts = (a.f.page_bytes + 65535) / 65536;
   k_fork<<<dim3(a.num_new, a.num_layers, (unsigned)(parts > 64 ? 64 : parts)), 256, 0, st>>>(a);
   return hipGetLastError();
 }
