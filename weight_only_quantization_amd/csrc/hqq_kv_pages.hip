@@ -181,49 +181,50 @@ __global__ __launch_bounds__(256) void k_fork(ForkArgs a) {
   if (!there || first || used == 0) return;
   const uint32_t from = (uint32_t)row[last];
   if (from >= a.f.num_pages || (uint32_t)fresh >= a.f.num_pages || from == (uint32_t)fresh) return;
-  // the used tokens' part of each block, 16 bytes a thread: K codes, V codes and metadata of groups of four tokens (of the last
-  // group only the tokens that are there: the rest of the page stays as it is)
-  const int quads = (used + 3) / 4, nk = used * a.b.row / 16, nv = quads * a.b.row / 4, all = nk + nv + quads * a.b.meta;
+  // The used tokens' part of each block, a wave a head, 16 bytes a lane and load: K codes, V codes and metadata of groups of four
+  // tokens (of the last group only the tokens that are there: the rest of the page stays as it is).  Nine loads
+  // are in flight, which is all there is of 64 tokens of 128 channels in 4 bits.
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int quads = (used + 3) / 4, nk = used * a.b.row / 16, nv = quads * a.b.row / 4;
+  const int per_quad = a.b.row / 4, row_shift = a.f.page_shift - 2, nm = a.b.meta << row_shift;  // per_quad: V codes' loads of four tokens
   const uint8_t* src = a.layers.pages[layer] + (int64_t)from * a.f.page_bytes;
   uint8_t* dst = a.layers.pages[layer] + (int64_t)fresh * a.f.page_bytes;
-  const uint32_t total = (uint32_t)all * a.f.hkv, step = gridDim.z * 256;
-  constexpr int U = 8;
-  for (uint32_t i0 = blockIdx.z * 256 + threadIdx.x; i0 < total; i0 += U * step) {
-    u32x4 v[U];
-    int64_t at[U];
+  for (int head = blockIdx.z * 4 + wave; head < a.f.hkv; head += 4 * gridDim.z) {
+    const uint8_t* s = src + head * a.f.block_bytes;
+    uint8_t* t = dst + head * a.f.block_bytes;
+    for (int k0 = 0; 4 * k0 < nk || 4 * k0 < nv || k0 < nm; k0 += 64) {
+      u32x4 v[9];
+      int at[9];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const uint32_t i = i0 + k * step;
-      at[k] = -1;
-      if (i >= total) continue;
-      const int head = i / (uint32_t)all, x = i - head * all;
-      int off, quad = 0, unit = 4;  // of a group of four tokens: which one, bytes of a token in one place
-      if (x < nk) {
-        off = 16 * x;
-      } else if (x < nk + nv) {
-        off = 16 * (x - nk);
-        quad = off / (4 * a.b.row), unit = a.b.unit;
-        off += page * a.b.row;
-      } else {
-        const int m = x - nk - nv, r = m / quads;
-        quad = m - r * quads;
-        off = 2 * page * a.b.row + r * 4 * page + 16 * quad;
-      }
-      at[k] = head * a.f.block_bytes + off;
-      v[k] = *reinterpret_cast<const u32x4*>(src + at[k]);
-      if (x >= nk && 4 * quad + 4 > used) {
-        const u32x4 old = *reinterpret_cast<const u32x4*>(dst + at[k]);
+      for (int i = 0; i < 9; ++i) {
+        const int x = i < 8 ? 4 * k0 + 64 * (i & 3) + lane : k0 + lane;
+        int quad = 0, unit = 4;  // group of four tokens, bytes of a token in one place of it
+        at[i] = -1;
+        if (i < 4) {
+          if (x < nk) at[i] = 16 * x;
+        } else if (i < 8) {
+          quad = x / per_quad, unit = a.b.unit;
+          if (x < nv) at[i] = page * a.b.row + 16 * x;
+        } else {
+          quad = x & ((1 << row_shift) - 1);
+          if (x < nm && quad < quads) at[i] = 2 * page * a.b.row + 16 * x;
+        }
+        if (at[i] < 0) continue;
+        v[i] = *reinterpret_cast<const u32x4*>(s + at[i]);
+        if (i >= 4 && 4 * quad + 4 > used) {
+          const u32x4 old = *reinterpret_cast<const u32x4*>(t + at[i]);
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t low = 4 * quad + ((off + 4 * w) / unit & 3) < used ? 0xffffu : 0u;
-          const uint32_t high = 4 * quad + ((off + 4 * w + 2) / unit & 3) < used ? 0xffff0000u : 0u;
-          v[k][w] = (v[k][w] & (low | high)) | (old[w] & ~(low | high));
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t low = 4 * quad + ((16 * x + 4 * w) / unit & 3) < used ? 0xffffu : 0u;
+            const uint32_t high = 4 * quad + ((16 * x + 4 * w + 2) / unit & 3) < used ? 0xffff0000u : 0u;
+            v[i][w] = (v[i][w] & (low | high)) | (old[w] & ~(low | high));
+          }
         }
       }
-    }
 #pragma unroll
-    for (int k = 0; k < U; ++k)
-      if (at[k] >= 0) *reinterpret_cast<u32x4*>(dst + at[k]) = v[k];
+      for (int i = 0; i < 9; ++i)
+        if (at[i] >= 0) *reinterpret_cast<u32x4*>(t + at[i]) = v[i];
+    }
   }
 }
 
@@ -371,9 +372,8 @@ hipError_t launch_accept(const AcceptArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_fork(const ForkArgs& a, hipStream_t st) {
-  // blocks of a page: 64 KB each, half of which is used on average: eight loads in flight a thread
-  const int64_t parts = (a.f.page_bytes + 65535) / 65536;
-  k_fork<<<dim3(a.num_new, a.num_layers, (unsigned)(parts > 64 ? 64 : parts)), 256, 0, st>>>(a);
+  const int parts = (a.f.hkv + 3) / 4;
+  k_fork<<<dim3(a.num_new, a.num_layers, parts > 64 ? 64 : parts), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 

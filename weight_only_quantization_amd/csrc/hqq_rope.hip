@@ -112,8 +112,8 @@ __device__ __forceinline__ void turn_heads(const Heads& x, int64_t token, int fi
       const int h = h0 + k * step + l.lane_head;
       on[k] = l.lane_head < l.per && h < x.count;
       if (on[k]) {
-        w[k][0] = *reinterpret_cast<const u32x4*>(from + h * x.in_hs + l.at0);
-        w[k][1] = *reinterpret_cast<const u32x4*>(from + h * x.in_hs + l.at1);
+        w[k][0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + h * x.in_hs + l.at0));
+        w[k][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + h * x.in_hs + l.at1));
       }
     }
 #pragma unroll
@@ -179,12 +179,15 @@ __global__ __launch_bounds__(256) void k_write_rope(WriteRopeArgs a) {
     if (!INTER && first) cs[j].y = -cs[j].y;
   }
   const int hkv = a.w.f.hkv;
-  for (int i = blockIdx.y * 4 + wave; i < 2 * hkv; i += 4 * gridDim.y) {
+  auto load = [&](int i) {
+    const bool is_k = i < hkv;
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(is_k ? a.w.k : a.w.v);
+    p += token * (is_k ? a.w.k_ts : a.w.v_ts) + (is_k ? i : i - hkv) * (is_k ? a.w.k_hs : a.w.v_hs);
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + 8 * o));
+  };
+  auto take = [&](int i, u32x4 w) {
     const bool is_k = i < hkv;
     const int head = is_k ? i : i - hkv;
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(is_k ? a.w.k : a.w.v);
-    p += token * (is_k ? a.w.k_ts : a.w.v_ts) + head * (is_k ? a.w.k_hs : a.w.v_hs);
-    const u32x4 w = *reinterpret_cast<const u32x4*>(p + 8 * o);
     float x[8];
     floats8<BF16>(w, x);
     if (is_k) {
@@ -218,6 +221,17 @@ __global__ __launch_bounds__(256) void k_write_rope(WriteRopeArgs a) {
       }
     }
     if (a.w.k_echo && there) store_dense<BF16>(is_k ? a.w.k_echo : a.w.v_echo, (token * hkv + head) * D + 8 * o, x);
+  };
+  // (the next head's values are asked for before this one's are worked on)
+  const int step = 4 * gridDim.y;
+  int i = blockIdx.y * 4 + wave;
+  if (i >= 2 * hkv) return;
+  u32x4 w = load(i);
+  for (; i < 2 * hkv; i += step) {
+    u32x4 next = {};
+    if (i + step < 2 * hkv) next = load(i + step);
+    take(i, w);
+    w = next;
   }
 }
 
