@@ -99,14 +99,24 @@ enum StreamMode { kShares, kSharesOnce, kWhole8, kWhole4 };
 StreamMode stream_mode(const AttnArgs& a, int nt);
 // Tiles of 256 rows of list `which`.
 hipError_t launch_kv_tile(const AttnArgs& a, int which, int D, int bits, int gs, hipStream_t st);
-// Both for calls whose own list ends in drafted tokens.
+// Streams and tiles of an own list that ends in drafted tokens; the tiles take shares of the work, of 256 rows or of 128.
 hipError_t launch_kv_stream_tree(const AttnArgs& a, int D, int bits, int gs, int nt, hipStream_t st);
-hipError_t launch_kv_tile_tree(const AttnArgs& a, int which, int D, int bits, int gs, hipStream_t st);
+hipError_t launch_kv_tile_tree(const AttnArgs& a, int rows, int D, int bits, int gs, hipStream_t st);
 // Joins the partial results of every row; nt: of the stream's lists.
 hipError_t launch_kv_join(const AttnArgs& a, int D, int nt_own, int nt_prefix, hipStream_t st);
 
 constexpr int kUnitKeys = 128;  // keys of the stream's unit of work: a step of each of a block's four waves
 constexpr uint32_t kStartUnits = 3;  // units that beginning a (sequence, row tile, KV head) counts for
+
+// The shares of the work that a launch's blocks take.
+struct Share {
+  uint32_t per, more;  // units of a block; the first `more` blocks have one more
+  __device__ uint32_t begin(uint32_t i) const { return i * per + min(i, more); }
+  __device__ uint32_t block_of(uint32_t u) const {
+    const uint32_t wide = more * (per + 1);
+    return u < wide ? u / (per + 1) : more + (u - wide) / per;
+  }
+};
 
 // Softmax weights are taken 2^kLift larger than exp(score - running maximum), in the sums too: a score passes the maximum by
 // 2^5 at most, so they stay under 2^15 in fp16, which then keeps 11 bits of weights down to 2^-24 of the maximum's and holds

@@ -14,7 +14,9 @@ using hqq::kv::KeyList;
 constexpr int64_t kMostKeys = INT32_MAX - (1 << 16);
 
 // One attention call: its kernels' arguments, the row kernel of each list, the workspace.
-enum { kStream16, kStream32, kTile };  // the stream with 16 or 32 rows a block, or tiles of 256 rows
+// the stream with 16 or 32 rows a block, tiles of 256 rows; of drafted trees tiles of 128 or 256 rows in shares
+enum { kStream16, kStream32, kTile, kShare128, kShare256 };
+bool shares(int kind) { return kind == kShare128 || kind == kShare256; }
 
 struct Plan {
   AttnArgs a;
@@ -35,13 +37,15 @@ struct Plan {
 // tiles are taken where streams were the faster too: 31 (240 rows, 16379 keys) 64 and 55, 38 (1414 rows, 3399 keys) 79 and 52, but
 // 36 (5516 rows) 40 and 59.  More than 2^16 rows take tiles whatever the keys (the threshold is at 384 keys there).
 constexpr int64_t kStreamWork = int64_t(3) << 23, kStreamRows = 1 << 16;
-int row_kernel(int64_t rows, int64_t lists, int64_t keys) {
+int row_kernel(int64_t rows, int64_t lists, int64_t keys, bool tree = false) {
+  if (tree && rows > 64) return rows <= 128 ? kShare128 : kShare256;
   if (rows > 64 && (rows > kStreamRows || (keys > 0 ? keys : 1) * lists > kStreamWork / rows)) return kTile;
   return rows <= 16 || (rows + 15) / 16 * lists <= 256 ? kStream16 : kStream32;
 }
-int nt_of(int kind) { return kind == kStream16 ? 1 : 2; }
+int rows_of(int kind) { return kind == kStream16 ? 16 : kind == kStream32 ? 32 : kind == kShare128 ? 128 : 256; }
+int nt_of(int kind) { return rows_of(kind) / 16; }
 int64_t row_tiles(int64_t rows, int kind) {
-  const int64_t of = kind == kStream16 ? 16 : kind == kStream32 ? 32 : 256;
+  const int64_t of = rows_of(kind);
   return (rows + of - 1) / of;
 }
 
@@ -60,7 +64,12 @@ void split_keys(KeyList* l, int64_t blocks) {
 // Longest own keys that one block streams for a pair; longer ones are shared out over the blocks.
 constexpr int64_t kWholeKeys = 2048;
 
-// Blocks of a stream launch: what fills the GPU, but at least two units each.
+// Blocks that fill the GPU.
+int most_blocks(const hqq_kv_cache& c, int kind) {
+  return shares(kind) ? 256 : hqq::kv::stream_blocks(c.head_dim, c.group_size, nt_of(kind));
+}
+
+// Blocks of a launch of shares: what fills the GPU, but at least two units each.
 int stream_grid(const Plan& p, const hqq_kv_cache& c, int first, int lists) {
   int64_t units = 0;
   for (int i = first; i < first + lists; ++i) {
@@ -68,7 +77,7 @@ int stream_grid(const Plan& p, const hqq_kv_cache& c, int first, int lists) {
     const int64_t keys = hqq::kv::kStartUnits + (l.max_len + hqq::kv::kUnitKeys - 1) / hqq::kv::kUnitKeys;
     units += keys * l.num_seqs * p.a.f.hkv * row_tiles((int64_t)l.max_q * p.a.per, p.kind[i]);
   }
-  const int64_t most = hqq::kv::stream_blocks(c.head_dim, c.group_size, nt_of(p.kind[first]));
+  const int64_t most = most_blocks(c, p.kind[first]);
   const int64_t n = (units + 1) / 2;
   return (int)(n > most ? most : n < 1 ? 1 : n);
 }
@@ -143,21 +152,21 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p, boo
   for (int i = 0; i < (a.joined ? 2 : 1); ++i) {
     KeyList& l = a.list[i];
     const int64_t rows = (int64_t)l.max_q * a.per;
-    p->kind[i] = row_kernel(rows, (int64_t)f.hkv * l.num_seqs, l.max_len);
-    const int64_t tiles = row_tiles(rows, p->kind[i]), pairs = tiles * f.hkv * l.num_seqs;
+    p->kind[i] = row_kernel(rows, (int64_t)f.hkv * l.num_seqs, l.max_len, tree && i == 0);
+    const int64_t row_blocks = row_tiles(rows, p->kind[i]), pairs = row_blocks * f.hkv * l.num_seqs;
     // (pairs times units may pass 64 bits)
-    KV_NEED(tiles <= 65535 && pairs <= (int64_t(1) << 30) / (l.max_len / hqq::kv::kUnitKeys + hqq::kv::kStartUnits + 1),
+    KV_NEED(row_blocks <= 65535 && pairs <= (int64_t(1) << 30) / (l.max_len / hqq::kv::kUnitKeys + hqq::kv::kStartUnits + 1),
             HQQ_ERR_UNSUPPORTED, "too many query rows and keys in a call");
     if (p->kind[i] == kTile) {
       l.tiled = 1;
       split_keys(&l, pairs);
       if (l.nsplit > 1) p->join = true;
     } else {
-      const int64_t most = 16 * nt_of(p->kind[i]);
+      const int64_t most = rows_of(p->kind[i]);
       l.cap = (int)(rows < most ? rows : most);
       // (own keys and a prefix that streams alike take one launch of shares)
       const bool alone = !a.joined || row_kernel(x->total_q * a.per, f.hkv, x->prefix_len) != p->kind[0];
-      if (i == 0 && alone && l.max_len <= kWholeKeys) {
+      if (i == 0 && alone && l.max_len <= kWholeKeys && !shares(p->kind[i])) {
         l.tiled = l.nsplit = 1;
       } else {
         p->join = true;
@@ -178,7 +187,7 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p, boo
       continue;
     }
     const int64_t pairs = row_tiles(rows, p->kind[i]) * f.hkv * l.num_seqs;
-    const int64_t grid = hqq::kv::stream_blocks(c.head_dim, c.group_size, nt_of(p->kind[i]));
+    const int64_t grid = most_blocks(c, p->kind[i]);
     // (segments are counted over the pairs of both lists where one launch takes both)
     const int64_t segments = a.joined ? grid + pairs + (i ? row_tiles((int64_t)own.max_q * a.per, p->kind[0]) * f.hkv * own.num_seqs : 0)
                                       : 2 * grid;
@@ -252,8 +261,9 @@ int run_attention(const hqq_kv_attention_args* x, const hqq_kv_tree_args* tree =
   hipStream_t stream = static_cast<hipStream_t>(x->stream);
   const int D = c.head_dim, bits = c.nbits, gs = c.group_size;
   hipError_t e = each_launch(&p, c, [&](int i) {
-    if (p.kind[i] == kTile) return (tree ? hqq::kv::launch_kv_tile_tree : hqq::kv::launch_kv_tile)(a, i, D, bits, gs, stream);
-    return (tree ? hqq::kv::launch_kv_stream_tree : hqq::kv::launch_kv_stream)(a, D, bits, gs, nt_of(p.kind[i]), stream);
+    if (p.kind[i] == kTile) return hqq::kv::launch_kv_tile(a, i, D, bits, gs, stream);
+    if (shares(p.kind[i])) return hqq::kv::launch_kv_tile_tree(a, rows_of(p.kind[i]), D, bits, gs, stream);
+    return (a.list[i].tree ? hqq::kv::launch_kv_stream_tree : hqq::kv::launch_kv_stream)(a, D, bits, gs, nt_of(p.kind[i]), stream);
   });
   if (e == hipSuccess && p.join) e = hqq::kv::launch_kv_join(a, D, nt_of(p.kind[0]), nt_of(p.kind[1]), stream);
   return device_status(e);

@@ -118,15 +118,7 @@ constexpr int whole_sets(int D, int BITS, int GS, int NT) {
 // The work of a launch: units of 128 keys of every (sequence, row tile, KV head), in one order, cut into
 // equal shares, one a block.  A block walks the pieces ("segments") of its share; a pair that several
 // blocks share leaves a partial result per segment, a pair within one share is finished there.
-// Lengths live on the device, so every wave works the cut out for itself.
-struct Share {
-  uint32_t per, more;  // units of a block; the first `more` blocks have one more
-  __device__ uint32_t begin(uint32_t i) const { return i * per + min(i, more); }
-  __device__ uint32_t block_of(uint32_t u) const {
-    const uint32_t wide = more * (per + 1);
-    return u < wide ? u / (per + 1) : more + (u - wide) / per;
-  }
-};
+// Lengths live on the device, so every wave works the cut out for itself (Share, hqq_kv.h).
 
 template <int NT>
 __device__ __forceinline__ uint32_t tiles_of(const AttnArgs& a, int tq) {

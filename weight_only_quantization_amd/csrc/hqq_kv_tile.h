@@ -27,6 +27,7 @@ namespace hqq {
 namespace kv {
 namespace {
 
+
 constexpr int kWaves = 8, kRows = 32 * kWaves, kKeys = 128;
 
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -68,53 +69,34 @@ struct Raw {
   u32x4 vm;
 };
 
-// TREE: as in the stream kernel.
-template <int D, int BITS, int GS, bool TREE>
-__global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
-  const KeyList list = which ? a.list[1] : a.list[0];
+template <int D>
+using TilesK = uint8_t[2][kKeys * kRowK<D>];
+template <int D>
+using TilesV = uint8_t[2][D * kRowV];
+
+// Rows row0 .. of a pair over its keys kb .. ke - 1: all there is for the block to do.  partial: the sums are left as partial
+// result part0 + (its place by row of the call, or TREE: by row of the tile), else the output is finished.
+// TREE: the last tq keys are drafted tokens, and a row sees those of them that its mask names.  KG: 2 where the pair has up to 128
+// rows, a wave's 32 rows being two waves', one for either half of a tile's keys: no wave is without rows, and the tiles
+// are read from LDS once for the two.
+template <int D, int BITS, int GS, bool TREE, int KG>
+__device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list, const Sequence& sequence, int seq, int hk, int row0,
+                                          int kb, int ke, bool partial, int64_t part0, TilesK<D>& sh_k, TilesV<D>& sh_v,
+                                          float2 (&sh_ml)[4][64]) {
   constexpr int NG = D / GS, U = D * BITS / 128;
   constexpr int kRow = D * BITS / 8;
   constexpr int KS = D / 16, DT = D / 32;  // MFMA steps of a score, channel tiles of the output
-  __shared__ __attribute__((aligned(16))) uint8_t sh_k[2][kKeys * kRowK<D>];
-  __shared__ __attribute__((aligned(16))) uint8_t sh_v[2][D * kRowV];
-
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, h = lane >> 5;
-  // fp16 results past the largest number stay there (MODE.FP16_OVFL): a group that reaches +-65504 may stand for
-  // a little more than fp16 holds
-  __builtin_amdgcn_s_setreg(1 | 23 << 6, 1);
-
-  // Grid: KV head and sequence (x), row tile (y), key split (z).  Blocks go round the eight XCDs in order
-  // of x, so the pairs are turned by tile and split: the parts of one long sequence spread over
-  // all XCDs.  The tiles with the most keys under a causal rule start first.
-  const uint32_t pair = (blockIdx.x + blockIdx.y + blockIdx.z) % gridDim.x;
-  const int hk = pair % a.f.hkv, seq = pair / a.f.hkv, split = blockIdx.z, tile = gridDim.y - 1 - blockIdx.y;
-
-  const Sequence sequence = sequence_of<true>(a, list, seq);
   const int q0 = sequence.q0, tq = sequence.tq, len = sequence.len;
   const int rows = tq * a.per;
-  const int row0 = tile * kRows;
-  if (row0 >= rows) return;
   const int page = 1 << a.f.page_shift;
-  const int64_t total_rows = a.total_q * a.hq;
-  const int last_t = (min(row0 + kRows, rows) - 1) / a.per;
-  const int end_all = list.causal ? min(len, max(0, len - tq + last_t + 1)) : len;
-  const int kb = split * list.chunk;
-  const int ke = min(kb + list.chunk, end_all);
-  const bool partial = list.nsplit > 1 || a.joined;
-  if (kb >= end_all && partial) {  // no key of this split
-    const int row = row0 + tid;
-    if (tid < kRows && row < rows)
-      a.part_ml[list.part0 + split * total_rows + (int64_t)(q0 + row / a.per) * a.hq + hk * a.per + row % a.per] =
-          float2{kNoKey, 0.f};
-    return;
-  }
   // the wave's own rows
-  const int w_row0 = row0 + 32 * wave;
+  const int w_row0 = row0 + 32 * (KG == 2 ? wave & 3 : wave);
   const bool w_on = w_row0 < rows;
   const int w_first = w_on ? w_row0 / a.per : 0, w_last = w_on ? (min(w_row0 + 32, rows) - 1) / a.per : 0;
   const int w_end = !w_on ? 0 : list.causal ? min(ke, len - tq + w_last + 1) : ke;   // keys that some row sees
-  const int w_min = list.causal ? len - tq + w_first + 1 : TREE && list.tree ? len - tq : len;                       // keys that all rows see
+  const int w_min = list.causal ? len - tq + w_first + 1 : TREE ? len - tq : len;  // keys that all rows see
 
   // ---- queries
   h8 qf[KS];
@@ -258,7 +240,8 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
     const uint8_t* kl = kt + n * kRowK<D> + h * 16;
     const uint8_t* vl = vt + n * kRowV + h * 16;
 #pragma unroll
-    for (int sub = 0; sub < kKeys / 32; sub += 2) {
+    for (int s2 = 0; s2 < 2 / KG; ++s2) {
+      const int sub = KG == 2 ? 2 * (wave >> 2) : 2 * s2;
       const int first = key0 + 32 * sub;
       if (first >= w_end) return;
       f32x16 s[2];
@@ -277,7 +260,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           uint32_t sees = ~0u;  // the drafts among these keys that the lane's row sees
-          if (TREE && list.tree)
+          if (TREE)
             sees = drafts_seen(a.mask + (int64_t)(q0 + rt) * a.mask_words, a.mask_words, first + 32 * c - (len - tq)) >> (4 * h);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -380,13 +363,38 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
   // units 8 (a % 2) + 4 h + c whole, channel 2 d + a / 2 of each
   mref = fmaf(mref, cs, -kLift);  // what the weights are over, in units of the exponent, from here on
   l += __shfl_xor(l, 32);
+  if (KG == 2) {
+    // the second half's sums to the first: 16 bytes a lane and store, through the tiles' memory
+    float* sh_o = reinterpret_cast<float*>(sh_k[0]);
+    static_assert(sizeof(sh_k) >= 4 * 64 * DT * 16 * sizeof(float), "");
+    __syncthreads();  // the last tile has been read
+    if (wave >= 4) {
+      sh_ml[wave & 3][lane] = float2{mref, l};
+#pragma unroll
+      for (int i = 0; i < 4 * DT; ++i)
+        *reinterpret_cast<f32x4*>(sh_o + (((wave & 3) * 4 * DT + i) * 64 + lane) * 4) =
+            f32x4{o[i >> 2][4 * (i & 3)], o[i >> 2][4 * (i & 3) + 1], o[i >> 2][4 * (i & 3) + 2], o[i >> 2][4 * (i & 3) + 3]};
+    }
+    __syncthreads();
+    if (wave >= 4) return;
+    const float2 other = sh_ml[wave][lane];
+    const float mm = fmaxf(mref, other.x), f0 = exp2_(mref - mm), f1 = exp2_(other.x - mm);
+    mref = mm;
+    l = l * f0 + other.y * f1;
+#pragma unroll
+    for (int i = 0; i < 4 * DT; ++i) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(sh_o + ((wave * 4 * DT + i) * 64 + lane) * 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i >> 2][4 * (i & 3) + j] = fmaf(o[i >> 2][4 * (i & 3) + j], f0, x[j] * f1);
+    }
+  }
   // a query with an infinity or NaN gives NaN wherever it sees a key (it entered the products as 0: the fp16 mode above
   // does not hand a NaN on)
   if (l != 0.f) l += odd;
   if (!there) return;
   const int64_t at = (int64_t)(q0 + rt) * a.hq + hk * a.per + rg;
   if (partial) {
-    const int64_t part = list.part0 + split * total_rows + at;
+    const int64_t part = part0 + (TREE ? r - row0 : at);
     if (h == 0) a.part_ml[part] = float2{mref, l};
     if (l != 0.f)
 #pragma unroll
@@ -416,11 +424,50 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
   }
 }
 
-template <int D, int BITS, int GS, bool TREE>
+template <int D, int BITS, int GS>
+__global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
+  const KeyList list = which ? a.list[1] : a.list[0];
+  __shared__ __attribute__((aligned(16))) TilesK<D> sh_k;
+  __shared__ __attribute__((aligned(16))) TilesV<D> sh_v;
+
+  const int tid = threadIdx.x;
+  // fp16 results past the largest number stay there (MODE.FP16_OVFL): a group that reaches +-65504 may stand for
+  // a little more than fp16 holds
+  __builtin_amdgcn_s_setreg(1 | 23 << 6, 1);
+
+  // Grid: KV head and sequence (x), row tile (y), key split (z).  Blocks go round the eight XCDs in order
+  // of x, so the pairs are turned by tile and split: the parts of one long sequence spread over
+  // all XCDs.  The tiles with the most keys under a causal rule start first.
+  const uint32_t pair = (blockIdx.x + blockIdx.y + blockIdx.z) % gridDim.x;
+  const int hk = pair % a.f.hkv, seq = pair / a.f.hkv, split = blockIdx.z, tile = gridDim.y - 1 - blockIdx.y;
+
+  const Sequence sequence = sequence_of<true>(a, list, seq);
+  const int q0 = sequence.q0, tq = sequence.tq, len = sequence.len;
+  const int rows = tq * a.per;
+  const int row0 = tile * kRows;
+  if (row0 >= rows) return;
+  const int64_t total_rows = a.total_q * a.hq;
+  const int last_t = (min(row0 + kRows, rows) - 1) / a.per;
+  const int end_all = list.causal ? min(len, max(0, len - tq + last_t + 1)) : len;
+  const int kb = split * list.chunk;
+  const int ke = min(kb + list.chunk, end_all);
+  const bool partial = list.nsplit > 1 || a.joined;
+  if (kb >= end_all && partial) {  // no key of this split
+    const int row = row0 + tid;
+    if (tid < kRows && row < rows)
+      a.part_ml[list.part0 + split * total_rows + (int64_t)(q0 + row / a.per) * a.hq + hk * a.per + row % a.per] =
+          float2{kNoKey, 0.f};
+    return;
+  }
+  float2 none[4][64];
+  tile_pair<D, BITS, GS, false, 1>(a, list, sequence, seq, hk, row0, kb, ke, partial, list.part0 + split * total_rows, sh_k, sh_v, none);
+}
+
+template <int D, int BITS, int GS>
 hipError_t tile_t(const AttnArgs& a, int which, hipStream_t st) {
   const KeyList& l = a.list[which];
   const int tiles = (int)(((int64_t)l.max_q * a.per + kRows - 1) / kRows);
-  k_kv_tile<D, BITS, GS, TREE><<<dim3(a.f.hkv * l.num_seqs, tiles, l.nsplit), 512, 0, st>>>(a, which);
+  k_kv_tile<D, BITS, GS><<<dim3(a.f.hkv * l.num_seqs, tiles, l.nsplit), 512, 0, st>>>(a, which);
   return hipGetLastError();
 }
 

@@ -158,17 +158,21 @@ __global__ __launch_bounds__(256) void k_write_rope(WriteRopeArgs a) {
   // (lanes behind the last token go along on it, and store nothing)
   const int64_t token = there ? token0 + t : n - 1;
   const int64_t slot = a.w.slots[token];
+  const int hkv = a.w.f.hkv;
+  auto load = [&](int i) {
+    const bool is_k = i < hkv;
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(is_k ? a.w.k : a.w.v);
+    p += token * (is_k ? a.w.k_ts : a.w.v_ts) + (is_k ? i : i - hkv) * (is_k ? a.w.k_hs : a.w.v_hs);
+    return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + 8 * o));
+  };
+  const int step = 4 * gridDim.y;
+  int i = blockIdx.y * 4 + wave;
+  u32x4 w = {};
+  if (i < 2 * hkv) w = load(i);
   make_table(a.turn, token0, TOKENS, n, tab);
   __syncthreads();
   const int rot = a.turn.rot, half = rot / 2;
   {
-    const Lane l = lane_of<INTER>(D, rot, lane);
-    for (int i = wave; i < TOKENS && token0 + i < n; i += 4) {
-      double2 cs[8];
-      lane_pairs<INTER>(tab + i * half, rot, l, cs);
-      turn_heads<BF16, INTER>(a.q, token0 + i, blockIdx.y * l.per, gridDim.y * l.per, l, cs);
-    }
-  }
   const bool turned = 8 * o < rot, first = 8 * o < half;
   const int partner = t * OCT + (INTER || !turned ? o : first ? o + rot / 16 : o - rot / 16);
   // halves: own c + other s, the sine with the sign that the half's formula gives it
@@ -178,13 +182,6 @@ __global__ __launch_bounds__(256) void k_write_rope(WriteRopeArgs a) {
     cs[j] = tab[!turned ? 0 : t * half + pair_at(rot, (INTER ? 4 * o : first ? 8 * o : 8 * o - half) + j)];
     if (!INTER && first) cs[j].y = -cs[j].y;
   }
-  const int hkv = a.w.f.hkv;
-  auto load = [&](int i) {
-    const bool is_k = i < hkv;
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(is_k ? a.w.k : a.w.v);
-    p += token * (is_k ? a.w.k_ts : a.w.v_ts) + (is_k ? i : i - hkv) * (is_k ? a.w.k_hs : a.w.v_hs);
-    return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p + 8 * o));
-  };
   auto take = [&](int i, u32x4 w) {
     const bool is_k = i < hkv;
     const int head = is_k ? i : i - hkv;
@@ -222,16 +219,20 @@ __global__ __launch_bounds__(256) void k_write_rope(WriteRopeArgs a) {
     }
     if (a.w.k_echo && there) store_dense<BF16>(is_k ? a.w.k_echo : a.w.v_echo, (token * hkv + head) * D + 8 * o, x);
   };
-  // (the next head's values are asked for before this one's are worked on)
-  const int step = 4 * gridDim.y;
-  int i = blockIdx.y * 4 + wave;
-  if (i >= 2 * hkv) return;
-  u32x4 w = load(i);
   for (; i < 2 * hkv; i += step) {
     u32x4 next = {};
     if (i + step < 2 * hkv) next = load(i + step);
     take(i, w);
     w = next;
+  }
+  }
+  {
+    const Lane l = lane_of<INTER>(D, rot, lane);
+    for (int i = wave; i < TOKENS && token0 + i < n; i += 4) {
+      double2 cs[8];
+      lane_pairs<INTER>(tab + i * half, rot, l, cs);
+      turn_heads<BF16, INTER>(a.q, token0 + i, blockIdx.y * l.per, gridDim.y * l.per, l, cs);
+    }
   }
 }
 
