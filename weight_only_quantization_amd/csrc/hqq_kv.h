@@ -104,6 +104,8 @@ hipError_t launch_kv_stream_tree(const AttnArgs& a, int D, int bits, int gs, int
 hipError_t launch_kv_tile_tree(const AttnArgs& a, int rows, int D, int bits, int gs, hipStream_t st);
 // Joins the partial results of every row; nt: of the stream's lists.
 hipError_t launch_kv_join(const AttnArgs& a, int D, int nt_own, int nt_prefix, hipStream_t st);
+// The same of a call without a prefix whose own keys went in shares, of row tiles of tile_rows.
+hipError_t launch_kv_join_pairs(const AttnArgs& a, int D, int tile_rows, hipStream_t st);
 
 constexpr int kUnitKeys = 128;  // keys of the stream's unit of work: a step of each of a block's four waves
 constexpr uint32_t kStartUnits = 3;  // units that beginning a (sequence, row tile, KV head) counts for

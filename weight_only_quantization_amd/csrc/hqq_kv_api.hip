@@ -176,6 +176,8 @@ int plan_attention(const hqq_kv_attention_args* x, bool sizes_only, Plan* p, boo
   // (blocks of 512 threads per KV head and sequence; four rows a block of 256 in the join)
   KV_NEED((int64_t)f.hkv * x->num_seqs <= kThreads / 512 && (!p->join || x->total_q * a.hq <= kThreads / 64),
           HQQ_ERR_UNSUPPORTED, "too many sequences or query rows in a call");
+  KV_NEED(!tree || row_tiles((int64_t)own.max_q * a.per, p->kind[0]) * f.hkv * x->num_seqs <= kThreads / 256, HQQ_ERR_UNSUPPORTED,
+          "too many sequences or query rows in a call");
   if (!p->join) return HQQ_OK;
   // the lists' partial results, one after the other; the streams' segment lists behind them
   for (int i = 0; i < (a.joined ? 2 : 1); ++i) {
@@ -265,7 +267,9 @@ int run_attention(const hqq_kv_attention_args* x, const hqq_kv_tree_args* tree =
     if (shares(p.kind[i])) return hqq::kv::launch_kv_tile_tree(a, rows_of(p.kind[i]), D, bits, gs, stream);
     return (a.list[i].tree ? hqq::kv::launch_kv_stream_tree : hqq::kv::launch_kv_stream)(a, D, bits, gs, nt_of(p.kind[i]), stream);
   });
-  if (e == hipSuccess && p.join) e = hqq::kv::launch_kv_join(a, D, nt_of(p.kind[0]), nt_of(p.kind[1]), stream);
+  if (e == hipSuccess && p.join)
+    e = tree && !a.joined ? hqq::kv::launch_kv_join_pairs(a, D, rows_of(p.kind[0]), stream)
+                          : hqq::kv::launch_kv_join(a, D, nt_of(p.kind[0]), nt_of(p.kind[1]), stream);
   return device_status(e);
 }
 

@@ -67,6 +67,8 @@ struct Raw {
   uint32_t v[D * BITS / 128];  // a unit's codes of four tokens
   uint32_t km[NG];
   u32x4 vm;
+  bool has_k;   // whether the key is on a page of the cache
+  int tokens;   // of the four how many are there
 };
 
 template <int D>
@@ -82,7 +84,7 @@ using TilesV = uint8_t[2][D * kRowV];
 template <int D, int BITS, int GS, bool TREE, int KG>
 __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list, const Sequence& sequence, int seq, int hk, int row0,
                                           int kb, int ke, bool partial, int64_t part0, TilesK<D>& sh_k, TilesV<D>& sh_v,
-                                          float2 (&sh_ml)[4][64]) {
+                                          float2 (&sh_ml)[4][64], int (&sh_holes)[4]) {
   constexpr int NG = D / GS, U = D * BITS / 128;
   constexpr int kRow = D * BITS / 8;
   constexpr int KS = D / 16, DT = D / 32;  // MFMA steps of a score, channel tiles of the output
@@ -98,6 +100,44 @@ __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list
   const int w_end = !w_on ? 0 : list.causal ? min(ke, len - tq + w_last + 1) : ke;   // keys that some row sees
   const int w_min = list.causal ? len - tq + w_first + 1 : TREE ? len - tq : len;  // keys that all rows see
 
+  // ---- a tile's codes: a quarter of one key and one unit of four tokens a thread.  Nothing that is loaded is looked at before the
+  // tile it belongs to is unpacked (of a page's id, before the codes it leads to are asked for), a tile later, so that no load is waited for
+  // (with every load's answer tested at once a tile took three trips to memory more: 5.3 us of 128 keys for XX).
+  const int32_t* table = list.table + (int64_t)seq * list.table_stride;
+  const int last_page = max(list.table_cols - 1, 0);  // (a table without columns: any readable entry)
+  const int ik = tid >> 2, iv = (tid >> 4) * 4;
+  const uint32_t k_off = (tid & 3) * (kRow / 4);
+  const int unit = tid & 15;
+  Raw<D, BITS, NG> raw;
+  uint32_t id_k, id_v;  // pages of the next tile to load
+  auto ask_pages = [&](int key0) {
+    id_k = (uint32_t)table[min((key0 + ik) >> a.f.page_shift, last_page)];
+    id_v = (uint32_t)table[min((key0 + iv) >> a.f.page_shift, last_page)];
+  };
+  auto load = [&](int key0, int slot) {  // the codes of the tile at key0, and the page ids of the one after it
+    if (key0 >= ke) return;
+    const bool on_k = key0 + ik < ke && id_k < a.f.num_pages, on_v = key0 + iv < ke && id_v < a.f.num_pages;
+    raw.has_k = on_k;
+    raw.tokens = on_v ? len - key0 - iv : 0;
+    if (!on_k && key0 + ik < ke) sh_holes[slot] = 1;
+    {
+      const int off = (key0 + ik) & (page - 1);
+      const uint8_t* base = a.f.pages + (int64_t)(on_k ? id_k : 0) * a.f.page_bytes + hk * a.f.block_bytes;
+      load_words(base + off * kRow + k_off, raw.k);
+      const uint32_t* m = reinterpret_cast<const uint32_t*>(base + 2 * page * kRow) + off;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) raw.km[g] = m[g * page];
+    }
+    {
+      const int off = (key0 + iv) & (page - 1);
+      const uint8_t* base = a.f.pages + (int64_t)(on_v ? id_v : 0) * a.f.page_bytes + hk * a.f.block_bytes;
+      load_words(base + page * kRow + off * kRow + unit * 4 * U, raw.v);
+      raw.vm = *reinterpret_cast<const u32x4*>(base + 2 * page * kRow + 4 * (page * (NG + unit * (D / 16) / GS) + off));
+    }
+    ask_pages(key0 + kKeys);
+  };
+  ask_pages(kb);
+
   // ---- queries
   h8 qf[KS];
   float cs, odd = 0.f;  // odd: NaN where the row's query is not finite
@@ -112,8 +152,14 @@ __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
       w[i] = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(a.q) + at + 16 * i + 8 * h);
-      if (!there) w[i] = u32x4{0, 0, 0, 0};
     }
+    // the first tile's codes behind the queries
+    if (tid < 4) sh_holes[tid] = 0;
+    __syncthreads();
+    load(kb, 0);
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+      if (!there) w[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
       float x[8];
@@ -143,39 +189,7 @@ __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list
     lim = there ? (list.causal ? min(len - 1, len - tq + rt) : len - 1) : -1;
   }
 
-  // ---- unpacking: a quarter of one key and one unit of four tokens a thread
-  const int32_t* table = list.table + (int64_t)seq * list.table_stride;
-  const int ik = tid >> 2, iv = (tid >> 4) * 4;
-  const uint32_t k_off = (tid & 3) * (kRow / 4);
-  const int unit = tid & 15;
-  auto page_id = [&](int key) -> int {
-    if (key >= ke) return -1;
-    const uint32_t id = (uint32_t)table[key >> a.f.page_shift];
-    return id < a.f.num_pages ? (int)id : -1;
-  };
-  auto fetch = [&](int key0, int id_k, int id_v, Raw<D, BITS, NG>& s) {
-    {
-      const int off = (key0 + ik) & (page - 1);
-      const uint8_t* base = a.f.pages + (int64_t)max(id_k, 0) * a.f.page_bytes + hk * a.f.block_bytes;
-      load_words(base + off * kRow + k_off, s.k);
-      const uint32_t* m = reinterpret_cast<const uint32_t*>(base + 2 * page * kRow) + off;
-#pragma unroll
-      for (int g = 0; g < NG; ++g) s.km[g] = m[g * page];
-      // (keys that are not there: any finite value; their scores are masked)
-      if (id_k < 0)
-#pragma unroll
-        for (int g = 0; g < NG; ++g) s.km[g] = 0;
-    }
-    {
-      const int off = (key0 + iv) & (page - 1);
-      const uint8_t* base = a.f.pages + (int64_t)max(id_v, 0) * a.f.page_bytes + hk * a.f.block_bytes;
-      load_words(base + page * kRow + off * kRow + unit * 4 * U, s.v);
-      s.vm = *reinterpret_cast<const u32x4*>(base + 2 * page * kRow + 4 * (page * (NG + unit * (D / 16) / GS) + off));
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (id_v < 0 || key0 + iv + c >= len) s.vm[c] = 0;
-    }
-  };
+  // ---- unpacking
   uint32_t m_lo, m_hi, or1024, or64;
   asm("s_mov_b32 %0, 0x000f000f" : "=s"(m_lo));
   asm("s_mov_b32 %0, 0x00f000f0" : "=s"(m_hi));
@@ -185,7 +199,7 @@ __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list
   auto unpack = [&](Raw<D, BITS, NG>& s, uint8_t* to_k, uint8_t* to_v) {
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const uint32_t mm = s.km[i * 32 / GS];
+      const uint32_t mm = s.has_k ? s.km[i * 32 / GS] : 0u;  // (a key that is not there: any finite value; its scores are masked)
       const h2 st = as_h2(__builtin_amdgcn_perm(mm, mm, 0x01000100)), fm = as_h2(__builtin_amdgcn_perm(mm, mm, 0x03020302));
       u32x4 w;
       if (BITS == 4) {
@@ -206,7 +220,7 @@ __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list
     h2 st[2], fm[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint32_t x = s.vm[2 * i], y = s.vm[2 * i + 1];
+      const uint32_t x = 2 * i < s.tokens ? (uint32_t)s.vm[2 * i] : 0u, y = 2 * i + 1 < s.tokens ? (uint32_t)s.vm[2 * i + 1] : 0u;
       st[i] = as_h2(__builtin_amdgcn_perm(y, x, 0x05040100));
       fm[i] = as_h2(__builtin_amdgcn_perm(y, x, 0x07060302));
     }
@@ -326,36 +340,27 @@ __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list
   };
 
   if (kb < ke) {
-    Raw<D, BITS, NG> raw;
-    int id_k = page_id(kb + ik), id_v = page_id(kb + iv);
-    int bad = id_k < 0 && kb + ik < ke;
-    auto load = [&](int key0) {  // the codes of the tile at key0, and the page ids of the one after it
-      if (key0 < ke) fetch(key0, id_k, id_v, raw);
-      bad = id_k < 0 && key0 + ik < ke;
-      id_k = page_id(key0 + kKeys + ik), id_v = page_id(key0 + kKeys + iv);
-    };
-    load(kb);
-    bool holes = __syncthreads_or(bad);
     unpack(raw, sh_k[0], sh_v[0]);
-    load(kb + kKeys);
-    int buf = 0;
+    load(kb + kKeys, 1);
     // The second wave of each SIMD unpacks before its products and the first one after them, so that one's matrix
     // instructions meet the other's vector instructions.
     const bool early = wave >= kWaves / 2;
-    for (int key0 = kb; key0 < ke; key0 += kKeys) {
+    int i = 0;  // tiles so far; sh_holes[i % 4]: whether tile i has keys that are on no page
+    for (int key0 = kb; key0 < ke; key0 += kKeys, ++i) {
       const bool more = key0 + kKeys < ke;
-      const bool next_holes = __syncthreads_or(bad);  // this tile is written; the other buffer is free
+      uint8_t *next_k = sh_k[(i + 1) & 1], *next_v = sh_v[(i + 1) & 1];
+      __syncthreads();  // this tile is written; the other buffer is free
+      const bool holes = sh_holes[i & 3];
+      if (tid == 0) sh_holes[(i + 3) & 3] = 0;
       if (more && early) {
-        unpack(raw, sh_k[buf ^ 1], sh_v[buf ^ 1]);
-        load(key0 + 2 * kKeys);
+        unpack(raw, next_k, next_v);
+        load(key0 + 2 * kKeys, (i + 2) & 3);
       }
-      attend(key0, sh_k[buf], sh_v[buf], holes);
+      attend(key0, sh_k[i & 1], sh_v[i & 1], holes);
       if (more && !early) {
-        unpack(raw, sh_k[buf ^ 1], sh_v[buf ^ 1]);
-        load(key0 + 2 * kKeys);
+        unpack(raw, next_k, next_v);
+        load(key0 + 2 * kKeys, (i + 2) & 3);
       }
-      holes = next_holes;
-      buf ^= 1;
     }
   }
 
@@ -459,8 +464,9 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
           float2{kNoKey, 0.f};
     return;
   }
+  __shared__ int sh_holes[4];
   float2 none[4][64];
-  tile_pair<D, BITS, GS, false, 1>(a, list, sequence, seq, hk, row0, kb, ke, partial, list.part0 + split * total_rows, sh_k, sh_v, none);
+  tile_pair<D, BITS, GS, false, 1>(a, list, sequence, seq, hk, row0, kb, ke, partial, list.part0 + split * total_rows, sh_k, sh_v, none, sh_holes);
 }
 
 template <int D, int BITS, int GS>

@@ -23,6 +23,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile_shares(AttnArgs a) {
   __shared__ __attribute__((aligned(16))) TilesK<D> sh_k;
   __shared__ __attribute__((aligned(16))) TilesV<D> sh_v;
   __shared__ float2 sh_ml[4][64];
+  __shared__ int sh_holes[4];
   // (as in k_kv_tile)
   __builtin_amdgcn_s_setreg(1 | 23 << 6, 1);
 
@@ -91,7 +92,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile_shares(AttnArgs a) {
       list.segments[2 * at + 1] = whole && !a.joined ? 0 : (int)(share.block_of(u + units - 1) - blockIdx.x + 1);
     }
     tile_pair<D, BITS, GS, true, KG>(a, list, s, seq, hk, tile * R, kb, ke, !whole || a.joined, list.part0 + (int64_t)segment * list.cap,
-                                     sh_k, sh_v, sh_ml);
+                                     sh_k, sh_v, sh_ml, sh_holes);
     u += x1 - x0;
     if (u >= u_end) break;
     ++pair, ++pairs;
