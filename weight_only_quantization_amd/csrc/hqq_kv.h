@@ -207,11 +207,18 @@ __device__ __forceinline__ Sequence sequence_of(const AttnArgs& a, const KeyList
   return s;
 }
 
-// Of a query token's mask the 32 bits from draft d on, which may lie in front of the first one: those keys are seen.
-__device__ __forceinline__ uint32_t drafts_seen(const uint32_t* row, int words, int d) {
-  const int w = d >> 5;
-  const uint32_t lo = w < 0 ? ~0u : w < words ? row[w] : 0u, hi = w + 1 < 0 ? ~0u : w + 1 < words ? row[w + 1] : 0u;
-  return __builtin_amdgcn_alignbit(hi, lo, d & 31);
+// Of a query token's mask the 32 W bits from draft d on, which may lie in front of the first one: those keys are seen.  (All
+// words are asked for at once.)
+template <int W>
+__device__ __forceinline__ void drafts_seen(const uint32_t* row, int words, int d, uint32_t (&sees)[W]) {
+  const int w0 = d >> 5;
+  uint32_t x[W + 1];
+#pragma unroll
+  for (int i = 0; i <= W; ++i) x[i] = row[min(max(w0 + i, 0), words - 1)];
+#pragma unroll
+  for (int i = 0; i <= W; ++i) x[i] = w0 + i < 0 ? ~0u : w0 + i < words ? x[i] : 0u;
+#pragma unroll
+  for (int i = 0; i < W; ++i) sees[i] = __builtin_amdgcn_alignbit(x[i + 1], x[i], d & 31);
 }
 
 // Page id and address of a slot; nullptr where the slot is outside the cache.

@@ -417,7 +417,9 @@ __global__ __launch_bounds__(MODE == kWhole8 ? 512 : 256, MODE == kWhole8 ? 2 : 
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           const int token = min(row0 + 16 * t + n, rows - 1) / a.per;
-          sees[t] = drafts_seen(a.mask + (int64_t)(q0 + token) * a.mask_words, a.mask_words, key0 - end_min) >> (4 * h);
+          uint32_t x[1];
+          drafts_seen(a.mask + (int64_t)(q0 + token) * a.mask_words, a.mask_words, key0 - end_min, x);
+          sees[t] = x[0] >> (4 * h);
         }
       }
     }

@@ -88,7 +88,10 @@ __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list
   constexpr int NG = D / GS, U = D * BITS / 128;
   constexpr int kRow = D * BITS / 8;
   constexpr int KS = D / 16, DT = D / 32;  // MFMA steps of a score, channel tiles of the output
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int tid = threadIdx.x;
+  // (opaque, where a block takes several pairs: else what follows from it is worked out in front of them, and kept in scratch)
+  if (TREE) asm volatile("" : "+v"(tid));
+  const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int n = lane & 31, h = lane >> 5;
   const int q0 = sequence.q0, tq = sequence.tq, len = sequence.len;
   const int rows = tq * a.per;
@@ -271,16 +274,19 @@ __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list
           s[c] = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[i], s[c], 0, 0, 0);
         }
       if (holes | (first + 64 > w_min) | (first + 64 > ke)) {
+        // the drafts among these keys that the lane's row sees
+        uint32_t sees[2] = {~0u, ~0u};
+        if (TREE) {
+          drafts_seen(a.mask + (int64_t)(q0 + rt) * a.mask_words, a.mask_words, first - (len - tq), sees);
+          sees[0] >>= 4 * h, sees[1] >>= 4 * h;
+        }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t sees = ~0u;  // the drafts among these keys that the lane's row sees
-          if (TREE)
-            sees = drafts_seen(a.mask + (int64_t)(q0 + rt) * a.mask_words, a.mask_words, first + 32 * c - (len - tq)) >> (4 * h);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int key = first + 32 * c + 8 * (i >> 2) + 4 * h + (i & 3);
             bool on = key <= lim && key < ke;
-            if (TREE) on = on && (sees >> (8 * (i >> 2) + (i & 3)) & 1);
+            if (TREE) on = on && (sees[c] >> (8 * (i >> 2) + (i & 3)) & 1);
             if (holes) {
               const int id = table[min(key >> a.f.page_shift, max(list.table_cols - 1, 0))];
               on = on && (uint32_t)id < a.f.num_pages;
@@ -396,36 +402,62 @@ __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list
   // a query with an infinity or NaN gives NaN wherever it sees a key (it entered the products as 0: the fp16 mode above
   // does not hand a NaN on)
   if (l != 0.f) l += odd;
-  if (!there) return;
-  const int64_t at = (int64_t)(q0 + rt) * a.hq + hk * a.per + rg;
-  if (partial) {
-    const int64_t part = part0 + (TREE ? r - row0 : at);
-    if (h == 0) a.part_ml[part] = float2{mref, l};
-    if (l != 0.f)
+  // Rows are stored whole, 16 bytes a lane, through a part of the tiles' memory: a lane's own pieces are 8 bytes of 32 rows, and
+  // as many requests (8 us at the end of every block).
+  const int64_t at = (int64_t)(q0 + rt) * a.hq + hk * a.per + rg, part = part0 + (TREE ? r - row0 : at);
+  uint8_t* stage = (KG == 2 ? sh_v[0] : sh_k[0]) + wave * 32 * kRowK<D>;
+  static_assert(sizeof(sh_v) >= 4 * 32 * kRowK<D> && sizeof(sh_k) == 8 * 32 * kRowK<D>, "");
+  if (KG == 1) __syncthreads();  // the last tile has been read
+  if (!w_on) return;
+  const int live = min(rows - w_row0, 32);  // rows of the wave
+  uint8_t* mine = stage + n * kRowK<D>;
+  int from = lane;  // (opaque, so that the rows' places are not worked out in front of the tiles)
+  asm volatile("" : "+v"(from));
+  // rows of 2 D bytes to where(lane that holds the row)
+  auto store_rows = [&](uint8_t* to, int64_t row_at, int64_t row_bytes) {
+    constexpr int PR = D / 8;  // lanes of a row
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+    for (int i = 0; i < PR / 2; ++i) {
+      const int x = 64 * i + from, row = x / PR, c = x % PR;
+      const int64_t to_row = __shfl((long long)row_at, row);
+      if (row < live) *reinterpret_cast<u32x4*>(to + to_row * row_bytes + 16 * c) = *reinterpret_cast<const u32x4*>(stage + row * kRowK<D> + 16 * c);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
+  if (partial) {
+    if (h == 0 && there) a.part_ml[part] = float2{mref, l};
+    // half the channels at a time: those of the units 8 p ..
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+#pragma unroll
+      for (int u = 4 * p; u < 4 * p + 4; ++u) {
         const int e = (u >> 2) * 4 + (u & 3);  // 4 (a % 2) + c
-        float* to = a.part_o + part * D + (8 * (u >> 2) + 4 * h + (u & 3)) * (D / 16);
 #pragma unroll
         for (int d = 0; d < DT; d += 2)
-          *reinterpret_cast<f32x4*>(to + 2 * d) = f32x4{o[d][e], o[d][e + 8], o[d + 1][e], o[d + 1][e + 8]};
+          *reinterpret_cast<f32x4*>(mine + ((4 * h + (u & 3)) * (D / 16) + 2 * d) * 4) = f32x4{o[d][e], o[d][e + 8], o[d + 1][e], o[d + 1][e + 8]};
       }
+      store_rows(reinterpret_cast<uint8_t*>(a.part_o) + p * 2 * D, part, 4 * D);
+    }
   } else {
     const float inv = l != 0.f ? 1.0f / l : 0.f;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
       const int e = (u >> 2) * 4 + (u & 3);
-      uint16_t* to = reinterpret_cast<uint16_t*>(a.out) + at * D + (8 * (u >> 2) + 4 * h + (u & 3)) * (D / 16);
 #pragma unroll
       for (int d = 0; d < DT; d += 2) {
         const float y0 = o[d][e] * inv, y1 = o[d][e + 8] * inv, y2 = o[d + 1][e] * inv, y3 = o[d + 1][e + 8] * inv;
         u32x2 w = a.dtype == HQQ_KV_BF16 ? u32x2{pack2<true>(y0, y1), pack2<true>(y2, y3)}
                                          : u32x2{pack2<false>(y0, y1), pack2<false>(y2, y3)};
         if (l != l) w = u32x2{0x7fff7fffu, 0x7fff7fffu};
-        *reinterpret_cast<u32x2*>(to + 2 * d) = w;
+        *reinterpret_cast<u32x2*>(mine + ((8 * (u >> 2) + 4 * h + (u & 3)) * (D / 16) + 2 * d) * 2) = w;
       }
     }
-    if (a.lse && h == 0) a.lse[at] = l != 0.f ? (mref + __log2f(l)) * 0.69314718056f : -INFINITY;
+    store_rows(reinterpret_cast<uint8_t*>(a.out), at, 2 * D);
+    if (a.lse && h == 0 && there) a.lse[at] = l != 0.f ? (mref + __log2f(l)) * 0.69314718056f : -INFINITY;
   }
 }
 
