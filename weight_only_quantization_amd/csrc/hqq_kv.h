@@ -237,3 +237,5 @@ __device__ __forceinline__ uint8_t* slot_block(const Format& f, int64_t slot, in
 // the rows of a block (16, 32 or 256; 0 without the list), the stream's mode (hqq::kv::StreamMode; -1 in tiles) and the tiles' key
 // splits; then whether a join follows.  Nothing is read or launched.  Returns the call's status.
 extern "C" int hqq_kv_attention_way(const hqq_kv_attention_args* args, int32_t way[7]);
+// The same of hqq_kv_attention_tree (rows 128 or 256 with the mode of shares: tiles in shares).
+extern "C" int hqq_kv_attention_tree_way(const hqq_kv_tree_args* args, int32_t way[7]);

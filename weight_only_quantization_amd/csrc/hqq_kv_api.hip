@@ -26,6 +26,9 @@ struct Plan {
   size_t workspace;
 };
 
+// Longest own keys that one block streams for a pair; longer ones are shared out over the blocks.
+constexpr int64_t kWholeKeys = 2048;
+
 // `lists` times that many rows (KV heads times sequences) over `keys` keys.  17 rows and more take 32 a block, which
 // reads the keys for twice the rows, unless blocks of 16 are no more than the CUs: then those end sooner (16
 // sequences of 2001 keys, 5 tokens, 32 heads on 8: 19.6 us with 16 rows, 22.7 with 32; 12 tokens: 35 and 24).
@@ -36,10 +39,13 @@ struct Plan {
 // 17.5 (1180 rows on a prefix of 3706) 42 and 52, 24 (6461 rows, 925 keys) 22 and 39.  Past the threshold it goes by the sizes, and
 // tiles are taken where streams were the faster too: 31 (240 rows, 16379 keys) 64 and 55, 38 (1414 rows, 3399 keys) 79 and 52, but
 // 36 (5516 rows) 40 and 59.  More than 2^16 rows take tiles whatever the keys (the threshold is at 384 keys there).
+// Drafted trees take shares of tiles at the same threshold, up to 2048 keys, which stream without a join, at twice that.  Streamed and in
+// shares, us: 17 million pairs (4 sequences of 4096 keys, 128 rows, 8 heads) 39 and 40, 34 (the same of 8192) 58 and 50, (8 heads of 512
+// rows, 8192 keys) 58 and 48; of 2048 keys 34 (16 sequences, 128 rows) 39 and 47, 67 (32 sequences) 76 and 63, 134 (256 rows) 142 and 95.
 constexpr int64_t kStreamWork = int64_t(3) << 23, kStreamRows = 1 << 16;
 int row_kernel(int64_t rows, int64_t lists, int64_t keys, bool tree = false) {
-  if (tree && rows > 64) return rows <= 128 ? kShare128 : kShare256;
-  if (rows > 64 && (rows > kStreamRows || (keys > 0 ? keys : 1) * lists > kStreamWork / rows)) return kTile;
+  const int64_t work = tree && keys <= kWholeKeys ? 2 * kStreamWork : kStreamWork;
+  if (rows > 64 && (rows > kStreamRows || (keys > 0 ? keys : 1) * lists > work / rows)) return !tree ? kTile : rows <= 128 ? kShare128 : kShare256;
   return rows <= 16 || (rows + 15) / 16 * lists <= 256 ? kStream16 : kStream32;
 }
 int rows_of(int kind) { return kind == kStream16 ? 16 : kind == kStream32 ? 32 : kind == kShare128 ? 128 : 256; }
@@ -60,9 +66,6 @@ void split_keys(KeyList* l, int64_t blocks) {
   l->nsplit = (int)((keys + l->chunk - 1) / l->chunk);
   if (l->nsplit < 1) l->nsplit = 1;
 }
-
-// Longest own keys that one block streams for a pair; longer ones are shared out over the blocks.
-constexpr int64_t kWholeKeys = 2048;
 
 // Blocks that fill the GPU.
 int most_blocks(const hqq_kv_cache& c, int kind) {
@@ -273,6 +276,23 @@ int run_attention(const hqq_kv_attention_args* x, const hqq_kv_tree_args* tree =
   return device_status(e);
 }
 
+int way_of(const hqq_kv_attention_args* x, bool tree, int32_t way[7]) {
+  Plan p;
+  for (int i = 0; i < 7; ++i) way[i] = 0;
+  const int st = plan_attention(x, false, &p, tree);
+  if (st != HQQ_OK || x->total_q == 0 || p.a.list[0].max_q == 0) return st;
+  (void)each_launch(&p, x->cache, [&](int i) {
+    for (int l = i; l < i + (p.kind[i] == kTile ? 1 : p.a.lists); ++l) {
+      way[3 * l] = rows_of(p.kind[l]);
+      way[3 * l + 1] = p.kind[l] == kTile ? -1 : shares(p.kind[l]) ? hqq::kv::kShares : hqq::kv::stream_mode(p.a, nt_of(p.kind[l]));
+      way[3 * l + 2] = p.kind[l] == kTile ? p.a.list[l].nsplit : 1;
+    }
+    return hipSuccess;
+  });
+  way[6] = p.join;
+  return HQQ_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -338,21 +358,8 @@ int hqq_kv_attention_tree(const hqq_kv_tree_args* x) {
   return run_attention(&x->attention, x);
 }
 
-int hqq_kv_attention_way(const hqq_kv_attention_args* x, int32_t way[7]) {
-  Plan p;
-  for (int i = 0; i < 7; ++i) way[i] = 0;
-  const int st = plan_attention(x, false, &p);
-  if (st != HQQ_OK || x->total_q == 0 || p.a.list[0].max_q == 0) return st;
-  (void)each_launch(&p, x->cache, [&](int i) {
-    for (int l = i; l < i + (p.kind[i] == kTile ? 1 : p.a.lists); ++l) {
-      way[3 * l] = p.kind[l] == kTile ? 256 : 16 * nt_of(p.kind[l]);
-      way[3 * l + 1] = p.kind[l] == kTile ? -1 : hqq::kv::stream_mode(p.a, nt_of(p.kind[l]));
-      way[3 * l + 2] = p.kind[l] == kTile ? p.a.list[l].nsplit : 1;
-    }
-    return hipSuccess;
-  });
-  way[6] = p.join;
-  return HQQ_OK;
-}
+int hqq_kv_attention_way(const hqq_kv_attention_args* x, int32_t way[7]) { return way_of(x, false, way); }
+
+int hqq_kv_attention_tree_way(const hqq_kv_tree_args* x, int32_t way[7]) { return way_of(&x->attention, true, way); }
 
 }  // extern "C"
