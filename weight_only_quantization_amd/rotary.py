@@ -92,6 +92,8 @@ def _strided(t, name, n, dtype):
         raise ValueError("%s must be [%d, heads, head_dim], got %s" % (name, n, tuple(shape)))
     if t.dtype is not dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if shape[1] == 0 and t.is_cuda:   # no heads: nothing is read
+        return 0, 0, 0, 0
     token, head = _kv._strides(t, name, shape[1], shape[2])
     return t.data_ptr(), token, head, shape[1]
 
