@@ -98,7 +98,7 @@ def _table(page_table, seq_lens):
         raise ValueError("seq_lens must be [num_seqs] = [%d], got [%d]" % (seqs, lens))
     _kv._there(seq_lens, "seq_lens")
     row, col = page_table.stride()
-    if not page_table.is_cuda or (col != 1 and cols > 1):
+    if not page_table.is_cuda or (col != 1 and cols > 1 and seqs > 0):
         raise ValueError("page_table must be a CUDA (HIP) tensor [num_seqs, pages], each row contiguous")
     return seqs, cols, row
 
