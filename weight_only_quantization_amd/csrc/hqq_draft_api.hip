@@ -26,7 +26,8 @@ int check_turn(const hqq_rope_form& x, const int64_t* positions, int head_dim, i
 }
 
 int check_heads(const Heads& h) {
-  KV_NEED(h.count == 0 || (h.in && h.out && aligned16(h.in) && aligned16(h.out)), HQQ_ERR_INVALID_ARGUMENT,
+  if (h.count == 0) return HQQ_OK;
+  KV_NEED(h.in && h.out && aligned16(h.in) && aligned16(h.out), HQQ_ERR_INVALID_ARGUMENT,
           "q, k and their outputs must be 16-byte aligned pointers");
   KV_NEED(h.in_ts >= 0 && h.in_hs >= 0 && h.out_ts >= 0 && h.out_hs >= 0 && (h.in_ts | h.in_hs | h.out_ts | h.out_hs) % 8 == 0,
           HQQ_ERR_INVALID_ARGUMENT, "strides must be non-negative multiples of 8 elements");

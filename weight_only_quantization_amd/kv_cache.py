@@ -197,11 +197,11 @@ def _together(first, *others):
 
 def _call(name, packed, near):
     """An entry point's status, called with the device of `near` current (a launch goes to the current one)."""
-    cuda = _torch().cuda
-    if near.get_device() == cuda.current_device():
-        return _entry(name)(packed)
-    with cuda.device(near.get_device()):
-        return _entry(name)(packed)
+    at, torch, entry = near.get_device(), _modules["torch"], _fast.get(name) or _entry(name)
+    if at == torch._C._cuda_getDevice():
+        return entry(packed)
+    with torch.cuda.device(at):
+        return entry(packed)
 
 
 def _empty(stream, shape, dtype, near):

@@ -92,20 +92,25 @@ def _strided(t, name, n, dtype):
         raise ValueError("%s must be [%d, heads, head_dim], got %s" % (name, n, tuple(shape)))
     if t.dtype is not dtype:
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if shape[1] == 0 and t.is_cuda:   # no heads: nothing is read
+    heads = shape[1]
+    if heads == 0 and t.is_cuda:   # no heads: nothing is read
         return 0, 0, 0, 0
-    token, head = _kv._strides(t, name, shape[1], shape[2])
-    return t.data_ptr(), token, head, shape[1]
+    token, head, channel = t.stride()
+    at = t.data_ptr()
+    if not t.is_cuda or channel != 1 or token % 8 or head % 8 or at % 16:
+        _kv._strides(t, name, heads, shape[2])   # (says what is wrong)
+    return at, token, head, heads
 
 
 def _out(t, given, name, stream):
     """The output for t: given (t's shape and type, t itself for in place) or new, its pointer and strides."""
+    shape = t.shape
     if given is None:
         given = _kv._like(stream, t)
-    elif given.shape != t.shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(t.shape), tuple(given.shape)))
-    at, token, head, _ = _strided(given, name, t.shape[0], t.dtype)
-    return given, (at, token, head)
+        return given, (given.data_ptr(), shape[1] * shape[2], shape[2])
+    if given.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(given.shape)))
+    return given, _strided(given, name, shape[0], t.dtype)[:3]
 
 
 def hqq_rope(q, positions, rope: RopeTable, k=None, backward: bool = False, out=None, stream=None):
