@@ -559,8 +559,8 @@ int hqq_rope_frequencies(int rot_dim, double base, int scaling, double factor, d
  *   backward   0; 1: the transposed rotation (sine with the other sign): dL/dx from dL/dy.
  *   positions  in  int64 [n] (device, 8-byte aligned), any value within +-2^53.
  *   q, q_out   [n, q_heads, head_dim], channels contiguous; token and head strides in elements (non-negative multiples of 8;
- *              16-byte aligned pointers).  q_out may be q itself with the same strides; no other overlap, and no two heads of an output
- *              on the same memory.  k, k_out likewise.
+ *              16-byte aligned pointers).  q_out may be q itself with the same strides; no other overlap.  An output's heads lie apart: side by
+ *              side in each token, or the tokens in each head.  k, k_out likewise.
  * n = 0 does nothing.  NaN and infinities stay within their pair.
  */
 typedef struct hqq_rope_args {

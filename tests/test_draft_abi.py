@@ -118,6 +118,20 @@ def test_frequencies(lib, rot, base):  # noqa: F811
         make(scaling="bands", factor=2.0)
 
 
+@pytest.mark.parametrize("kw,fits", [
+    (dict(q_out_token_stride=0), False), (dict(q_out_head_stride=0), False), (dict(q_out_head_stride=120), False),
+    (dict(q_out_token_stride=1016), False), (dict(q_out_token_stride=128, q_out_head_stride=384), True),
+    (dict(q_out_token_stride=128, q_out_head_stride=376), False), (dict(q_out_token_stride=120, q_out_head_stride=384), False),
+    (dict(q_out_token_stride=128), False), (dict(q_heads=1, q_out_head_stride=0), True), (dict(n=1, q_out_token_stride=0), True),
+    (dict(q_heads=1, q_out_token_stride=64), False), (dict(q_heads=0, q_out_token_stride=0), True),
+    (dict(q_token_stride=0, q_head_stride=0), True), (dict(k_out_token_stride=128), False)])
+def test_outputs_apart(lib, kw, fits):  # noqa: F811
+    """Outputs whose heads share memory are refused, broadcast inputs are not (the call then stops at k, which is refused)."""
+    kw = dict(kw) if "k_out_token_stride" in kw else dict(k=FAKE + 2, **kw)
+    assert rope(lib, **kw) == BAD
+    assert ("heads of an output overlap" in hq.last_error()) == (not fits)
+
+
 # ------------------------------------------------------------------------------ trees
 
 def plan(lib, **kw):  # noqa: F811

@@ -2,6 +2,8 @@
 // anything is enqueued.
 #include <math.h>
 
+#include <utility>
+
 #include "hqq_kv_checks.h"
 
 namespace {
@@ -25,7 +27,18 @@ int check_turn(const hqq_rope_form& x, const int64_t* positions, int head_dim, i
   return HQQ_OK;
 }
 
-int check_heads(const Heads& h) {
+// Whether no two of n tokens' heads share memory: heads side by side in each token, or tokens in each head.
+bool apart(int64_t n, int64_t token_stride, int64_t heads, int64_t head_stride, int64_t channels) {
+  if (token_stride < head_stride) {
+    std::swap(n, heads);
+    std::swap(token_stride, head_stride);
+  }
+  // (of `heads` things head_stride apart, n times token_stride apart)
+  if (heads > 1 && head_stride < channels) return false;
+  return n <= 1 || (token_stride >= channels && (heads <= 1 || (token_stride - channels) / head_stride >= heads - 1));
+}
+
+int check_heads(const Heads& h, int64_t n, int channels) {
   if (h.count == 0) return HQQ_OK;
   KV_NEED(h.in && h.out && aligned16(h.in) && aligned16(h.out), HQQ_ERR_INVALID_ARGUMENT,
           "q, k and their outputs must be 16-byte aligned pointers");
@@ -33,6 +46,7 @@ int check_heads(const Heads& h) {
           HQQ_ERR_INVALID_ARGUMENT, "strides must be non-negative multiples of 8 elements");
   KV_NEED(h.in != h.out || (h.in_ts == h.out_ts && h.in_hs == h.out_hs), HQQ_ERR_INVALID_ARGUMENT,
           "an output in the place of its input needs the same strides");
+  KV_NEED(apart(n, h.out_ts, h.count, h.out_hs, channels), HQQ_ERR_INVALID_ARGUMENT, "heads of an output overlap");
   return HQQ_OK;
 }
 
@@ -137,7 +151,7 @@ int hqq_rope(const hqq_rope_args* x) {
   a.n = x->n;
   a.head_dim = x->head_dim;
   for (const Heads* h : {&a.q, &a.k}) {
-    st = check_heads(*h);
+    st = check_heads(*h, a.n, a.head_dim);
     if (st != HQQ_OK) return st;
   }
   return device_status(hqq::kv::launch_rope(a, x->dtype, x->form.layout == HQQ_ROPE_INTERLEAVED, static_cast<hipStream_t>(x->stream)));
@@ -155,7 +169,7 @@ int hqq_kv_write_rope(const hqq_kv_write_rope_args* x) {
   st = check_turn(x->form, x->positions, w.cache.head_dim, 0, w.n > 0, &a.turn);
   if (st != HQQ_OK || w.n == 0) return st;
   a.q = Heads{x->q, x->q_out, x->q_token_stride, x->q_head_stride, x->q_out_token_stride, x->q_out_head_stride, x->q_heads};
-  st = check_heads(a.q);
+  st = check_heads(a.q, w.n, w.cache.head_dim);
   if (st != HQQ_OK) return st;
   return device_status(hqq::kv::launch_write_rope(a, w.cache.head_dim, w.cache.nbits, w.cache.group_size, w.dtype,
                                                   x->form.layout == HQQ_ROPE_INTERLEAVED, static_cast<hipStream_t>(w.stream)));
