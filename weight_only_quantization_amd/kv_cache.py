@@ -356,7 +356,7 @@ def hqq_kv_attention(cache: KVCache, q, page_table, seq_lens, scale=None, cu_q=N
     else:
         _pkg._need(workspace, "workspace", torch.uint8)
         at, need = workspace.data_ptr(), workspace.numel()
-    status = _entry(entry)(form.pack(*head, at, need, handle, *tail))
+    status = _call(entry, form.pack(*head, at, need, handle, *tail), q)
     if status:
         _pkg._check(status)
     return out if lse is None else (out, lse)
@@ -376,11 +376,13 @@ def hqq_kv_attention_tree(cache: KVCache, q, mask, page_table, seq_lens, scale=N
                           prefix_table=None, prefix_len: int = 0, out=None, return_lse: bool = False, workspace=None, stream=None):
     """hqq_kv_attention (with a prefix hqq_kv_attention_shared) for trees of drafted tokens: of its sequence's last T cached tokens,
     T its query tokens, query token i sees those whose bits are set in mask[i] (int64 [total_q, words], bit j of word j // 64:
-    draft j; hqq_kv_tree_plan makes it), and all tokens in front of them."""
+    draft j; hqq_kv_tree_plan makes it), and all tokens in front of them.  max_q is at most the mask's bits (with cu_q its default)."""
     tokens, words = _indices(mask, "mask", _torch().int64, 2)
     if tokens != q.shape[0]:
         raise ValueError("mask must be [%d, words], got %s" % (q.shape[0], tuple(mask.shape)))
     _there(mask, "mask")
     _together(q, mask, cache.pages, page_table, seq_lens, cu_q, prefix_table, out, workspace)
+    if max_q is None:
+        max_q = 64 * words
     return hqq_kv_attention(cache, q, page_table, seq_lens, scale, cu_q, max_q, max_len, False, out, return_lse, workspace, stream,
                             (prefix_table, prefix_len) if prefix_len else None, (mask.data_ptr(), words))

@@ -68,12 +68,16 @@ def declare(lib):
 
 class KVLayers:
     """The caches of a model's layers (KVCache of one format, number of pages and device), whose sequences share their page tables:
-    what the moves take.  Made once; it keeps the caches."""
+    what the moves take.  Made once; it keeps the caches (whose `pages` may be replaced later, all of them)."""
 
     def __init__(self, caches):
         self.caches = list(caches)
         if not 1 <= len(self.caches) <= HQQ_KV_MAX_LAYERS:
             raise ValueError("1 .. %d layers are wanted, got %d" % (HQQ_KV_MAX_LAYERS, len(self.caches)))
+        self._check()
+
+    def _check(self):
+        self._tensors = [c.pages for c in self.caches]
         fields = [c.args() for c in self.caches]
         if any(f[1:] != fields[0][1:] for f in fields):
             raise ValueError("the layers' caches must have one format and one number of pages")
@@ -81,6 +85,14 @@ class KVLayers:
         self.page_size, self.num_pages = self.caches[0].page_size, fields[0][1]
         self._pages = (ctypes.c_void_p * len(fields))(*(f[0] for f in fields))
         self._args = (0, *fields[0][1:], ctypes.addressof(self._pages), len(fields))
+
+    def args(self):
+        """The fields of hqq_kv_layers, checked again where a cache has other pages than before."""
+        for c, t in zip(self.caches, self._tensors):
+            if c.pages is not t:
+                self._check()
+                break
+        return self._args
 
 
 def _layers(layers):
@@ -113,14 +125,17 @@ def _drafts(cu_q, seqs, max_q, total):
     return cu_q.data_ptr(), total if max_q is None or max_q > total else max_q
 
 
+_MOST_DRAFTS = 4096
+
+
 def hqq_kv_tree_plan(parents, page_table, seq_lens, page_size: int, cu_q=None, max_q=None, stream=None):
     """What a step on drafted trees needs, from the drafts' parents (int32 [total_q]: index within the sequence, smaller than the
     draft's own; -1 behind the cached tokens).  page_table, seq_lens (the drafts included), cu_q and max_q as for
-    hqq_kv_attention.  Returns (mask int64 [total_q, words], positions int64 [total_q], slots int64 [total_q])."""
+    hqq_kv_attention (4096 drafts of a sequence at most; the mask has max_q bits a row, so pass the true bound).  Returns (mask int64 [total_q, words], positions int64 [total_q], slots int64 [total_q])."""
     torch = _kv._torch()
     total, = _kv._indices(parents, "parents", torch.int32, 1)
     seqs, cols, row = _table(page_table, seq_lens)
-    cu, bound = _drafts(cu_q, seqs, max_q, total)
+    cu, bound = _drafts(cu_q, seqs, min(total, _MOST_DRAFTS) if max_q is None else max_q, total)
     _kv._there(parents, "parents")
     most = bound if cu_q is not None else total // seqs if seqs else 0
     words = max(1, (most + 63) // 64)
@@ -161,7 +176,7 @@ def hqq_kv_accept(layers, page_table, seq_lens, accepted, num_accepted, tokens=N
     lens = _kv._empty(stream, (seqs,), torch.int32, seq_lens)
     _kv._together(layers.caches[0].pages, page_table, seq_lens, accepted, num_accepted, cu_q)
     status = _kv._call("hqq_kv_accept", _ACCEPT.pack(
-        *layers._args, seqs, total, cu, bound, page_table.data_ptr(), row, cols, seq_lens.data_ptr(), accepted.data_ptr(), most, most,
+        *layers.args(), seqs, total, cu, bound, page_table.data_ptr(), row, cols, seq_lens.data_ptr(), accepted.data_ptr(), most, most,
         num_accepted.data_ptr(), lens.data_ptr(), _kv._stream(stream, seq_lens)), seq_lens)
     if status:
         _pkg._check(status)
@@ -185,7 +200,7 @@ def hqq_kv_fork(layers, page_table, seq_lens, parents, fresh, stream=None):
     lens = _kv._empty(stream, (new,), torch.int32, page_table)
     _kv._together(layers.caches[0].pages, page_table, seq_lens, parents, fresh)
     status = _kv._call("hqq_kv_fork", _FORK.pack(
-        *layers._args, seqs, page_table.data_ptr(), row, cols, seq_lens.data_ptr(), new, parents.data_ptr(), fresh.data_ptr(),
+        *layers.args(), seqs, page_table.data_ptr(), row, cols, seq_lens.data_ptr(), new, parents.data_ptr(), fresh.data_ptr(),
         table.data_ptr(), cols, lens.data_ptr(), _kv._stream(stream, seq_lens)), seq_lens)
     if status:
         _pkg._check(status)
@@ -207,7 +222,7 @@ def hqq_kv_compact(layers, page_table, seq_lens, workspace=None, stream=None):
         _pkg._need(workspace, "workspace", torch.uint8)
     _kv._together(layers.caches[0].pages, page_table, seq_lens, workspace)
     status = _kv._call("hqq_kv_compact", _COMPACT.pack(
-        *layers._args, seqs, page_table.data_ptr(), row, cols, seq_lens.data_ptr(), table.data_ptr(), cols, used.data_ptr(),
+        *layers.args(), seqs, page_table.data_ptr(), row, cols, seq_lens.data_ptr(), table.data_ptr(), cols, used.data_ptr(),
         workspace.data_ptr(), workspace.numel(), _kv._stream(stream, seq_lens)), seq_lens)
     if status:
         _pkg._check(status)
