@@ -75,6 +75,10 @@ template <int D>
 using TilesK = uint8_t[2][kKeys * kRowK<D>];
 template <int D>
 using TilesV = uint8_t[2][D * kRowV];
+template <int N>
+struct Lanes {
+  static constexpr int value = N;
+};
 
 // Rows row0 .. of a pair over its keys kb .. ke - 1: all there is for the block to do.  partial: the sums are left as partial
 // result part0 + (its place by row of the call, or TREE: by row of the tile), else the output is finished.
@@ -84,7 +88,7 @@ using TilesV = uint8_t[2][D * kRowV];
 template <int D, int BITS, int GS, bool TREE, int KG>
 __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list, const Sequence& sequence, int seq, int hk, int row0,
                                           int kb, int ke, bool partial, int64_t part0, TilesK<D>& sh_k, TilesV<D>& sh_v,
-                                          float2 (&sh_ml)[4][64], int (&sh_holes)[4]) {
+                                          float2 (&sh_ml)[8][64], int (&sh_holes)[4]) {
   constexpr int NG = D / GS, U = D * BITS / 128;
   constexpr int kRow = D * BITS / 8;
   constexpr int KS = D / 16, DT = D / 32;  // MFMA steps of a score, channel tiles of the output
@@ -105,7 +109,7 @@ __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list
 
   // ---- a tile's codes: a quarter of one key and one unit of four tokens a thread.  Nothing that is loaded is looked at before the
   // tile it belongs to is unpacked (of a page's id, before the codes it leads to are asked for), a tile later, so that no load is waited for
-  // (with every load's answer tested at once a tile took three trips to memory more: 5.3 us of 128 keys for XX).
+  // (with every load's answer tested at once a tile of 256 rows took 5.3 us for 4.5).
   const int32_t* table = list.table + (int64_t)seq * list.table_stride;
   const int last_page = max(list.table_cols - 1, 0);  // (a table without columns: any readable entry)
   const int ik = tid >> 2, iv = (tid >> 4) * 4;
@@ -150,7 +154,6 @@ __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list
   const int rt = (there ? r : 0) / a.per, rg = (there ? r : 0) % a.per;
   {
     const int64_t at = (int64_t)(q0 + rt) * a.q_ts + (int64_t)(hk * a.per + rg) * a.q_hs;
-    float top = 0.f;
     u32x4 w[KS];
 #pragma unroll
     for (int i = 0; i < KS; ++i) {
@@ -160,34 +163,41 @@ __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list
     if (tid < 4) sh_holes[tid] = 0;
     __syncthreads();
     load(kb, 0);
+    // the row's largest value, as bits without a sign (infinities and NaN are past all others)
+    u16x2 most = {0, 0};
 #pragma unroll
     for (int i = 0; i < KS; ++i)
-      if (!there) w[i] = u32x4{0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      float x[8];
-      floats8(w[i], a.dtype, x);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j])), odd = fmaf(x[j], 0.f, odd);
-    }
-    top = fmaxf(top, __shfl_xor(top, 32));
-    odd += __shfl_xor(odd, 32);
-    if (odd != odd) {
-      top = 0.f;
+      for (int j = 0; j < 4; ++j) most = __builtin_elementwise_max(most, as_u16x2(w[i][j] & 0x7fff7fffu));
+    uint32_t top = max((uint32_t)most.x, (uint32_t)most.y);
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32));
+    const bool bf16 = a.dtype == HQQ_KV_BF16;
+    if (!there) top = 0;
+    if (top >= (bf16 ? 0x7f80u : 0x7c00u)) odd = NAN, top = 0;
+    if (top == 0) {
 #pragma unroll
       for (int i = 0; i < KS; ++i) w[i] = u32x4{0, 0, 0, 0};
     }
-    // the row's largest value to [2^14, 2^15): bfloat16 rows of any size keep their bits in fp16
-    int e = 0;
-    if (top > 0.f && top < INFINITY) e = 14 - (int)((__builtin_bit_cast(uint32_t, top) >> 23) & 255) + 127;
-    e = min(e, 100);
+    // it goes to [2^14, 2^15): bfloat16 rows of any size keep their bits in fp16
+    const float f = bf16 ? __builtin_bit_cast(float, top << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)top);
+    const int e = top ? min(14 - (int)(__builtin_bit_cast(uint32_t, f) >> 23) + 127, 100) : 0;
     cs = ldexpf(a.scale_log2, -e);
+    if (bf16 || __any(e > 15)) {
+      const float up = ldexpf(1.f, e);
 #pragma unroll
-    for (int i = 0; i < KS; ++i) {
-      float x[8];
-      floats8(w[i], a.dtype, x);
+      for (int i = 0; i < KS; ++i) {
+        float x[8];
+        floats8(w[i], a.dtype, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) qf[i][j] = (_Float16)ldexpf(x[j], e);
+        for (int j = 0; j < 8; j += 2) {
+          const h2 y = __builtin_convertvector((f32x2{x[j] * up, x[j + 1] * up}), h2);
+          qf[i][j] = y.x, qf[i][j + 1] = y.y;
+        }
+      }
+    } else {
+      const _Float16 up = (_Float16)ldexpf(1.f, e);
+#pragma unroll
+      for (int i = 0; i < KS; ++i) qf[i] = __builtin_bit_cast(h8, w[i]) * up;
     }
     lim = there ? (list.causal ? min(len - 1, len - tq + rt) : len - 1) : -1;
   }
@@ -374,29 +384,36 @@ __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list
   // units 8 (a % 2) + 4 h + c whole, channel 2 d + a / 2 of each
   mref = fmaf(mref, cs, -kLift);  // what the weights are over, in units of the exponent, from here on
   l += __shfl_xor(l, 32);
+  // Half the channels at a time: those of the units 8 p .., elements 4 a + c of even and of odd a.
+  const int p0 = KG == 2 ? wave >> 2 : 0;  // the half that the wave finishes, or the first of both
   if (KG == 2) {
-    // the second half's sums to the first: 16 bytes a lane and store, through the tiles' memory
+    // the two waves of a row tile have half of its keys each, and finish half of its channels each: the other half's sums go over,
+    // 16 bytes a lane and store, through the tiles' memory
     float* sh_o = reinterpret_cast<float*>(sh_k[0]);
-    static_assert(sizeof(sh_k) >= 4 * 64 * DT * 16 * sizeof(float), "");
+    static_assert(sizeof(sh_k) >= 8 * 64 * DT * 8 * sizeof(float), "");
     __syncthreads();  // the last tile has been read
-    if (wave >= 4) {
-      sh_ml[wave & 3][lane] = float2{mref, l};
+    sh_ml[wave][lane] = float2{mref, l};
 #pragma unroll
-      for (int i = 0; i < 4 * DT; ++i)
-        *reinterpret_cast<f32x4*>(sh_o + (((wave & 3) * 4 * DT + i) * 64 + lane) * 4) =
-            f32x4{o[i >> 2][4 * (i & 3)], o[i >> 2][4 * (i & 3) + 1], o[i >> 2][4 * (i & 3) + 2], o[i >> 2][4 * (i & 3) + 3]};
+    for (int i = 0; i < 2 * DT; ++i) {
+      f32x4 x;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] = p0 ? o[i >> 1][8 * (i & 1) + c] : o[i >> 1][8 * (i & 1) + 4 + c];
+      *reinterpret_cast<f32x4*>(sh_o + ((wave * 2 * DT + i) * 64 + lane) * 4) = x;
     }
     __syncthreads();
-    if (wave >= 4) return;
-    const float2 other = sh_ml[wave][lane];
+    const float2 other = sh_ml[wave ^ 4][lane];
     const float mm = fmaxf(mref, other.x), f0 = exp2_(mref - mm), f1 = exp2_(other.x - mm);
     mref = mm;
     l = l * f0 + other.y * f1;
 #pragma unroll
-    for (int i = 0; i < 4 * DT; ++i) {
-      const f32x4 x = *reinterpret_cast<const f32x4*>(sh_o + ((wave * 4 * DT + i) * 64 + lane) * 4);
+    for (int i = 0; i < 2 * DT; ++i) {
+      const f32x4 x = *reinterpret_cast<const f32x4*>(sh_o + (((wave ^ 4) * 2 * DT + i) * 64 + lane) * 4);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) o[i >> 2][4 * (i & 3) + j] = fmaf(o[i >> 2][4 * (i & 3) + j], f0, x[j] * f1);
+      for (int c = 0; c < 4; ++c) {
+        // (kept where the half's first elements are, whichever half it is)
+        const float own = p0 ? o[i >> 1][8 * (i & 1) + 4 + c] : o[i >> 1][8 * (i & 1) + c];
+        o[i >> 1][8 * (i & 1) + c] = fmaf(own, f0, x[c] * f1);
+      }
     }
   }
   // a query with an infinity or NaN gives NaN wherever it sees a key (it entered the products as 0: the fp16 mode above
@@ -405,17 +422,17 @@ __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list
   // Rows are stored whole, 16 bytes a lane, through a part of the tiles' memory: a lane's own pieces are 8 bytes of 32 rows, and
   // as many requests (8 us at the end of every block).
   const int64_t at = (int64_t)(q0 + rt) * a.hq + hk * a.per + rg, part = part0 + (TREE ? r - row0 : at);
-  uint8_t* stage = (KG == 2 ? sh_v[0] : sh_k[0]) + wave * 32 * kRowK<D>;
-  static_assert(sizeof(sh_v) >= 4 * 32 * kRowK<D> && sizeof(sh_k) == 8 * 32 * kRowK<D>, "");
-  if (KG == 1) __syncthreads();  // the last tile has been read
+  constexpr bool kOver = KG == 1 || sizeof(sh_v) < sizeof(sh_k);  // over the keys, or what has gone from wave to wave
+  uint8_t* stage = (kOver ? sh_k[0] : sh_v[0]) + wave * 32 * kRowK<D>;
+  static_assert(sizeof(sh_k) == 8 * 32 * kRowK<D>, "");
+  if (kOver) __syncthreads();  // all of it has been read
   if (!w_on) return;
   const int live = min(rows - w_row0, 32);  // rows of the wave
-  uint8_t* mine = stage + n * kRowK<D>;
   int from = lane;  // (opaque, so that the rows' places are not worked out in front of the tiles)
   asm volatile("" : "+v"(from));
-  // rows of 2 D bytes to where(lane that holds the row)
-  auto store_rows = [&](uint8_t* to, int64_t row_at, int64_t row_bytes) {
-    constexpr int PR = D / 8;  // lanes of a row
+  // rows of `row_lanes` pieces of 16 bytes to to[place of the row by the lane that holds it]
+  auto store_rows = [&](uint8_t* to, int64_t row_at, int64_t row_bytes, auto row_lanes) {
+    constexpr int PR = decltype(row_lanes)::value, STEP = 16 * PR + 16;
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
@@ -423,41 +440,43 @@ __device__ __forceinline__ void tile_pair(const AttnArgs& a, const KeyList& list
     for (int i = 0; i < PR / 2; ++i) {
       const int x = 64 * i + from, row = x / PR, c = x % PR;
       const int64_t to_row = __shfl((long long)row_at, row);
-      if (row < live) *reinterpret_cast<u32x4*>(to + to_row * row_bytes + 16 * c) = *reinterpret_cast<const u32x4*>(stage + row * kRowK<D> + 16 * c);
+      if (row < live) *reinterpret_cast<u32x4*>(to + to_row * row_bytes + 16 * c) = *reinterpret_cast<const u32x4*>(stage + row * STEP + 16 * c);
     }
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
   };
   if (partial) {
-    if (h == 0 && there) a.part_ml[part] = float2{mref, l};
-    // half the channels at a time: those of the units 8 p ..
+    if (h == 0 && there && p0 == 0) a.part_ml[part] = float2{mref, l};
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
+    for (int p = 0; p < 2 / KG; ++p) {
 #pragma unroll
-      for (int u = 4 * p; u < 4 * p + 4; ++u) {
-        const int e = (u >> 2) * 4 + (u & 3);  // 4 (a % 2) + c
+      for (int u = 0; u < 4; ++u) {
+        const int e = 4 * p + u;
 #pragma unroll
         for (int d = 0; d < DT; d += 2)
-          *reinterpret_cast<f32x4*>(mine + ((4 * h + (u & 3)) * (D / 16) + 2 * d) * 4) = f32x4{o[d][e], o[d][e + 8], o[d + 1][e], o[d + 1][e + 8]};
+          *reinterpret_cast<f32x4*>(stage + n * kRowK<D> + ((4 * h + u) * (D / 16) + 2 * d) * 4) =
+              f32x4{o[d][e], o[d][e + 8], o[d + 1][e], o[d + 1][e + 8]};
       }
-      store_rows(reinterpret_cast<uint8_t*>(a.part_o) + p * 2 * D, part, 4 * D);
+      store_rows(reinterpret_cast<uint8_t*>(a.part_o) + (p0 + p) * 2 * D, part, 4 * D, Lanes<D / 8>());
     }
   } else {
     const float inv = l != 0.f ? 1.0f / l : 0.f;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int e = (u >> 2) * 4 + (u & 3);
+    for (int p = 0; p < 2 / KG; ++p)
 #pragma unroll
-      for (int d = 0; d < DT; d += 2) {
-        const float y0 = o[d][e] * inv, y1 = o[d][e + 8] * inv, y2 = o[d + 1][e] * inv, y3 = o[d + 1][e + 8] * inv;
-        u32x2 w = a.dtype == HQQ_KV_BF16 ? u32x2{pack2<true>(y0, y1), pack2<true>(y2, y3)}
-                                         : u32x2{pack2<false>(y0, y1), pack2<false>(y2, y3)};
-        if (l != l) w = u32x2{0x7fff7fffu, 0x7fff7fffu};
-        *reinterpret_cast<u32x2*>(mine + ((8 * (u >> 2) + 4 * h + (u & 3)) * (D / 16) + 2 * d) * 2) = w;
+      for (int u = 0; u < 4; ++u) {
+        const int e = 4 * p + u;
+#pragma unroll
+        for (int d = 0; d < DT; d += 2) {
+          const float y0 = o[d][e] * inv, y1 = o[d][e + 8] * inv, y2 = o[d + 1][e] * inv, y3 = o[d + 1][e + 8] * inv;
+          u32x2 w = a.dtype == HQQ_KV_BF16 ? u32x2{pack2<true>(y0, y1), pack2<true>(y2, y3)}
+                                           : u32x2{pack2<false>(y0, y1), pack2<false>(y2, y3)};
+          if (l != l) w = u32x2{0x7fff7fffu, 0x7fff7fffu};
+          *reinterpret_cast<u32x2*>(stage + n * (KG == 2 ? D + 16 : kRowK<D>) + ((8 * p + 4 * h + u) * (D / 16) + 2 * d) * 2) = w;
+        }
       }
-    }
-    store_rows(reinterpret_cast<uint8_t*>(a.out), at, 2 * D);
-    if (a.lse && h == 0 && there) a.lse[at] = l != 0.f ? (mref + __log2f(l)) * 0.69314718056f : -INFINITY;
+    store_rows(reinterpret_cast<uint8_t*>(a.out) + p0 * D, at, 2 * D, Lanes<D / 8 / KG>());
+    if (a.lse && h == 0 && there && p0 == 0) a.lse[at] = l != 0.f ? (mref + __log2f(l)) * 0.69314718056f : -INFINITY;
   }
 }
 
@@ -497,7 +516,7 @@ __global__ __launch_bounds__(512, 2) void k_kv_tile(AttnArgs a, int which) {
     return;
   }
   __shared__ int sh_holes[4];
-  float2 none[4][64];
+  float2 none[8][64];
   tile_pair<D, BITS, GS, false, 1>(a, list, sequence, seq, hk, row0, kb, ke, partial, list.part0 + split * total_rows, sh_k, sh_v, none, sh_holes);
 }
 
