@@ -8,6 +8,7 @@ from tests import test_gpu_kv as base
 from tests.gpu_common import say
 from tests.kv_ways import SHARES
 from tests.test_gpu_kv_ways import widen
+from tests.test_gpu_pages import Pool, compact_plain
 from tests.test_gpu_tree import args_of, expect, random_parents, run, sees_of, ways, words_of  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -163,3 +164,43 @@ def test_replaced_pages():
     caches[1].pages = caches[1].pages[:7]
     with pytest.raises(ValueError, match="one format and one number of pages"):
         hq.hqq_kv_compact(layers, t, n)
+
+
+@pytest.mark.parametrize("pages,batch,cols,layers,hkv", [(4095, 3, 900, 1, 1), (4096, 64, 128, 1, 1), (4096, 1, 8193, 1, 1), (4097, 40, 90, 1, 1), (400, 5, 60, 3, 8),
+                                                         (400, 5, 60, 24, 8)])
+def test_compact_in_one_launch_and_in_two(pages, batch, cols, layers, hkv):
+    """Around the sizes where the blocks stop planning for themselves: pages, entries of the tables, bytes that may move; captured and replayed
+    with other tables."""
+    hq, torch = base.lib()
+    say("compact", pages, batch, cols, layers)
+    f = kp.Fmt(hkv, 64, 4, 64, 16)
+    rng = np.random.default_rng(pages + cols)
+    pool = Pool(hq, torch, f, layers, pages, seed=3)
+
+    def draw():
+        table = np.full((batch, cols), -1, np.int32)
+        ids = rng.permutation(pages)[:pages // 3].astype(np.int32)
+        lens = rng.integers(0, 16 * min(cols, pages // 3 // batch) + 1, batch)
+        for b, n in enumerate(lens):
+            held = -(-int(n) // 16)
+            table[b, :held], ids = ids[:held], ids[held:]
+        return table, [int(x) for x in lens]
+
+    table, lens = draw()
+    t, n = i32(torch, table), i32(torch, lens)
+    m, used = hq.hqq_kv_compact(pool.layers, t, n)
+    want, u = compact_plain(pool, table, lens)
+    assert np.array_equal(m.cpu().numpy(), want) and used.tolist() == [u] and u > 0
+    pool.check("eager")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        m, used = hq.hqq_kv_compact(pool.layers, t, n)
+    for rep in range(3):
+        table, lens = draw()
+        t.copy_(i32(torch, table))
+        n.copy_(i32(torch, lens))
+        graph.replay()
+        torch.cuda.synchronize()
+        want, u = compact_plain(pool, table, lens)
+        assert np.array_equal(m.cpu().numpy(), want) and used.tolist() == [u]
+        pool.check("replayed")

@@ -230,22 +230,30 @@ __global__ __launch_bounds__(256) void k_fork(ForkArgs a) {
   }
 }
 
-// ---- compaction.  One block finds the pages that the tables hold (a bit each in LDS), numbers the held ones past the first
+// ---- compaction.  A block finds the pages that the tables hold (a bit each in LDS), numbers the held ones past the first
 // U = (number of held pages) and the others below it, both in rising order, and writes down who moves where.
 __device__ __forceinline__ int held_columns(const Sequences& s, int seq, int page_shift) {
   return (length_of(s, seq, page_shift) + (1 << page_shift) - 1) >> page_shift;
 }
 
-constexpr int kPlanThreads = 1024;
-__global__ __launch_bounds__(kPlanThreads) void k_compact_plan(CompactArgs a) {
-  __shared__ uint32_t bits[kMostPages / 32];
-  __shared__ int sh_wave[kPlanThreads / 64];
-  __shared__ int sh_low;  // held pages below U
+template <int THREADS, int MOST>
+struct PlanShared {
+  uint32_t bits[MOST / 32];
+  int wave[THREADS / 64];
+  int low;  // held pages below U
+};
+// from, to: of each move; place: a moved page's new number, by its old one.
+struct Moves {
+  int32_t *from, *to, *place;
+  int count, held;
+};
+template <int THREADS, int MOST>
+__device__ __forceinline__ void plan_moves(const CompactArgs& a, PlanShared<THREADS, MOST>& sh, Moves& m) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int pages = (int)a.f.num_pages, words = (pages + 31) / 32;
-  for (int w = tid; w < words; w += kPlanThreads) bits[w] = 0;
+  for (int w = tid; w < words; w += THREADS) sh.bits[w] = 0;
   __syncthreads();
-  const int cols = a.seqs.table_cols, down = cols ? kPlanThreads / cols : 0, over = cols ? kPlanThreads % cols : 0;
+  const int cols = a.seqs.table_cols, down = cols ? THREADS / cols : 0, over = cols ? THREADS % cols : 0;
   int row = cols ? tid / cols : a.seqs.count, col = cols ? tid % cols : 0;
   while (row < a.seqs.count) {
     constexpr int U = 4;
@@ -260,42 +268,39 @@ __global__ __launch_bounds__(kPlanThreads) void k_compact_plan(CompactArgs a) {
     }
 #pragma unroll
     for (int k = 0; k < U; ++k)
-      if (id[k] < (uint32_t)pages) atomicOr(&bits[id[k] >> 5], 1u << (id[k] & 31));
+      if (id[k] < (uint32_t)pages) atomicOr(&sh.bits[id[k] >> 5], 1u << (id[k] & 31));
   }
   __syncthreads();
   // held pages in front of each thread's words
-  const int per = (words + kPlanThreads - 1) / kPlanThreads, w0 = min(tid * per, words), w1 = min(w0 + per, words);
+  const int per = (words + THREADS - 1) / THREADS, w0 = min(tid * per, words), w1 = min(w0 + per, words);
   int own = 0;
-  for (int w = w0; w < w1; ++w) own += __popc(bits[w]);
+  for (int w = w0; w < w1; ++w) own += __popc(sh.bits[w]);
   int before = own;
 #pragma unroll
   for (int i = 1; i < 64; i <<= 1) {
     const int x = __shfl_up(before, i);
     if (lane >= i) before += x;
   }
-  if (lane == 63) sh_wave[wave] = before;
+  if (lane == 63) sh.wave[wave] = before;
   before -= own;
   __syncthreads();
   int held = 0;
-  for (int w = 0; w < kPlanThreads / 64; ++w) {
-    if (w < wave) before += sh_wave[w];
-    held += sh_wave[w];
+  for (int w = 0; w < THREADS / 64; ++w) {
+    if (w < wave) before += sh.wave[w];
+    held += sh.wave[w];
   }
-  if (tid == 0 && held >> 5 >= words) sh_low = held;  // (every page, and no word has bit U)
+  if (tid == 0 && held >> 5 >= words) sh.low = held;  // (every page, and no word has bit U)
   if (w0 <= held >> 5 && held >> 5 < w1) {
     int n = before;
-    for (int w = w0; w < held >> 5; ++w) n += __popc(bits[w]);
-    sh_low = n + __popc(bits[held >> 5] & ((1u << (held & 31)) - 1));
+    for (int w = w0; w < held >> 5; ++w) n += __popc(sh.bits[w]);
+    sh.low = n + __popc(sh.bits[held >> 5] & ((1u << (held & 31)) - 1));
   }
   __syncthreads();
-  const int low = sh_low, moves = held - low;
-  int32_t* from = a.workspace + kCompactHead;
-  int32_t* to = from + (pages + 1) / 2;
-  int32_t* place = to + (pages + 1) / 2;
-  if (tid == 0) a.workspace[0] = moves, a.workspace[1] = held, a.used[0] = held;
+  const int low = sh.low;
+  m.count = held - low, m.held = held;
   int n = before;
   for (int w = w0; w < w1; ++w) {
-    const uint32_t b = bits[w];
+    const uint32_t b = sh.bits[w];
     const int p0 = 32 * w;
     // pages of the word below U and the others
     const uint32_t below = p0 + 32 <= held ? ~0u : p0 >= held ? 0u : (1u << (held - p0)) - 1;
@@ -303,39 +308,33 @@ __global__ __launch_bounds__(kPlanThreads) void k_compact_plan(CompactArgs a) {
     while (holes) {
       const int i = __builtin_ctz(holes);
       holes &= holes - 1;
-      to[p0 + i - n - __popc(b & ((1u << i) - 1))] = p0 + i;
+      m.to[p0 + i - n - __popc(b & ((1u << i) - 1))] = p0 + i;
     }
     while (far) {
       const int i = __builtin_ctz(far);
       far &= far - 1;
-      from[n + __popc(b & ((1u << i) - 1)) - low] = p0 + i;
+      m.from[n + __popc(b & ((1u << i) - 1)) - low] = p0 + i;
     }
     n += __popc(b);
   }
   __syncthreads();
-  for (int i = tid; i < moves; i += kPlanThreads) place[from[i]] = to[i];
+  for (int i = tid; i < m.count; i += THREADS) m.place[m.from[i]] = m.to[i];
 }
 
-// The moves: a wave takes 1 KB of a page at a time, of all layers; and the tables' new entries.  As many blocks as there may be work for
-// (launch_compact): blocks start in order, so what is in flight at a time lies together, while waves that walk on by themselves
-// drift apart (1.38 GB moved: 466 us with 65536 blocks, 5.9 TB/s; 490 with 32768, 534 with 2048, whatever a wave has in flight).
-__global__ __launch_bounds__(256) void k_compact_move(CompactArgs a) {
+// The moves: a wave takes 1 KB of a page at a time, of all layers; and the tables' new entries.
+__device__ __forceinline__ void move_pages(const CompactArgs& a, const Moves& m) {
   constexpr int kPart = 64 * 16;
-  const int moves = a.workspace[0], held = a.workspace[1];
-  const int32_t* from = a.workspace + kCompactHead;
-  const int32_t* to = from + ((int)a.f.num_pages + 1) / 2;
-  const int32_t* place = to + ((int)a.f.num_pages + 1) / 2;
   const int lane = threadIdx.x & 63;
   const uint32_t waves = gridDim.x * 4, wave = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t parts = (uint32_t)((a.f.page_bytes + kPart - 1) / kPart);
-  const uint64_t total = (uint64_t)moves * a.num_layers * parts;
+  const uint64_t total = (uint64_t)m.count * a.num_layers * parts;
   for (uint64_t i = wave; i < total; i += waves) {
     const uint64_t x = i / parts;
     const uint32_t part = (uint32_t)(i - x * parts);
-    const int layer = (int)(x / (uint32_t)moves), m = (int)(x - (uint64_t)layer * moves);
+    const int layer = (int)(x / (uint32_t)m.count), j = (int)(x - (uint64_t)layer * m.count);
     uint8_t* pages = a.layers.pages[layer];
-    const uint8_t* src = pages + (int64_t)from[m] * a.f.page_bytes;
-    uint8_t* dst = pages + (int64_t)to[m] * a.f.page_bytes;
+    const uint8_t* src = pages + (int64_t)m.from[j] * a.f.page_bytes;
+    uint8_t* dst = pages + (int64_t)m.to[j] * a.f.page_bytes;
     const int64_t at = (int64_t)part * kPart + 16 * lane;
     if (at < a.f.page_bytes)
       __builtin_nontemporal_store(__builtin_nontemporal_load(reinterpret_cast<const u32x4*>(src + at)), reinterpret_cast<u32x4*>(dst + at));
@@ -348,11 +347,47 @@ __global__ __launch_bounds__(256) void k_compact_move(CompactArgs a) {
       id = a.seqs.table[(int64_t)row * a.seqs.table_stride + col];
       if ((uint32_t)id >= a.f.num_pages)
         id = -1;
-      else if (id >= held)
-        id = place[id];
+      else if (id >= m.held)
+        id = m.place[id];
     }
     a.new_table[(int64_t)row * a.new_stride + col] = id;
   }
+}
+
+// In general one block plans, through the workspace, and a second launch moves.  Of that as many blocks as there may be work for
+// (launch_compact): blocks start in order, so what is in flight at a time lies together, while waves that walk on by themselves
+// drift apart (1.38 GB moved: 466 us with 65536 blocks, 5.9 TB/s; 490 with 32768, 534 with 2048, whatever a wave has in flight).
+constexpr int kPlanThreads = 1024;
+__device__ __forceinline__ Moves moves_in(const CompactArgs& a) {
+  const int half = ((int)a.f.num_pages + 1) / 2;
+  int32_t* from = a.workspace + kCompactHead;
+  return {from, from + half, from + 2 * half, 0, 0};
+}
+__global__ __launch_bounds__(kPlanThreads) void k_compact_plan(CompactArgs a) {
+  __shared__ PlanShared<kPlanThreads, kMostPages> sh;
+  Moves m = moves_in(a);
+  plan_moves(a, sh, m);
+  if (threadIdx.x == 0) a.workspace[0] = m.count, a.workspace[1] = m.held, a.used[0] = m.held;
+}
+__global__ __launch_bounds__(256) void k_compact_move(CompactArgs a) {
+  Moves m = moves_in(a);
+  m.count = a.workspace[0], m.held = a.workspace[1];
+  move_pages(a, m);
+}
+
+// Few pages and up to 32 MB that may move: every block plans for itself, in LDS, and moves its part, in one launch (211 pages of
+// 72 KB, 9 sequences: 13.7 us for 18.5 in one layer, where the host's launches bind; 16.2 and 16.3 in 8 layers, 42 MB moved; 43 and 41 in 32;
+// 4000 pages in one layer, 118 MB: 35 and 31).
+constexpr int kFewPages = 4096, kFewEntries = 8192;
+constexpr int64_t kFewBlocks = 1 << 13;  // (of 4 KB each)
+__global__ __launch_bounds__(256) void k_compact_few(CompactArgs a) {
+  __shared__ PlanShared<256, kFewPages> sh;
+  __shared__ int32_t from[kFewPages / 2], to[kFewPages / 2], place[kFewPages];
+  Moves m{from, to, place, 0, 0};
+  plan_moves(a, sh, m);
+  __syncthreads();
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.used[0] = m.held;
+  move_pages(a, m);
 }
 
 }  // namespace
@@ -377,12 +412,16 @@ hipError_t launch_fork(const ForkArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_compact(const CompactArgs& a, hipStream_t st) {
-  k_compact_plan<<<1, kPlanThreads, 0, st>>>(a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
   // at most half of the pages move, and no more than the tables have entries
   const int64_t entries = (int64_t)a.seqs.count * a.seqs.table_cols, half = (a.f.num_pages + 1) / 2, moves = entries < half ? entries : half;
   const int64_t blocks = (moves * a.num_layers * ((a.f.page_bytes + 1023) / 1024) + 3) / 4;
+  if (a.f.num_pages <= kFewPages && entries <= kFewEntries && blocks <= kFewBlocks) {
+    k_compact_few<<<(unsigned)(blocks < 64 ? 64 : blocks > 512 ? 512 : blocks), 256, 0, st>>>(a);
+    return hipGetLastError();
+  }
+  k_compact_plan<<<1, kPlanThreads, 0, st>>>(a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
   k_compact_move<<<(unsigned)(blocks < 256 ? 256 : blocks > 65536 ? 65536 : blocks), 256, 0, st>>>(a);
   return hipGetLastError();
 }
