@@ -8,14 +8,14 @@ from tests import test_gpu_kv as base
 from tests.gpu_common import say
 from tests.kv_ways import SHARES
 from tests.test_gpu_kv_ways import widen
-from tests.test_gpu_pages import Pool, compact_plain
+from tests.test_gpu_pages import Pool, accept_plain, compact_plain, paths
 from tests.test_gpu_tree import args_of, expect, random_parents, run, sees_of, ways, words_of  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
 
 def i32(torch, x):
-    return torch.tensor(x, dtype=torch.int32, device="cuda")
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
 
 
 @pytest.mark.parametrize("way", ["streamed", "streams in shares", "tiles"])
@@ -204,3 +204,29 @@ def test_compact_in_one_launch_and_in_two(pages, batch, cols, layers, hkv):
         want, u = compact_plain(pool, table, lens)
         assert np.array_equal(m.cpu().numpy(), want) and used.tolist() == [u]
         pool.check("replayed")
+
+
+@pytest.mark.parametrize("d,bits,g", base.FORMATS)
+def test_accept_long_lists(d, bits, g):
+    """Accepted drafts of several windows of 256 places, from any place of a page on, among them whole runs that stay; many sequences."""
+    hq, torch = base.lib()
+    rng = np.random.default_rng(bits + g)
+    for page, hkv, layers, new, most in ((16, 5, 3, [700, 513, 260], 600), (256, 3, 2, [600, 37, 900], 900), (32, 2, 40, [9] * 70, 9)):
+        say("accept", d, bits, g, page, new[:3])
+        f = kp.Fmt(hkv, d, bits, g, page)
+        lens = [n + int(rng.integers(0, 50)) for n in new]
+        cols = max(-(-n // page) for n in lens)
+        pool = Pool(hq, torch, f, layers, cols * len(new) + 3, seed=page)
+        table = rng.permutation(cols * len(new)).reshape(len(new), cols).astype(np.int32)
+        accepted, counts = paths(rng, new, most)
+        for b, c in enumerate(counts):                                  # every other list starts with a run that stays
+            if b % 2 == 0:
+                accepted[b, :c] = np.sort(np.r_[np.arange(c // 2), c // 2 + np.sort(rng.permutation(new[b] - c // 2)[:c - c // 2])])
+        if len(set(new)) > 1:
+            kw = dict(cu_q=base.cu(torch, new), max_q=max(new))
+        else:
+            kw = dict(tokens=new[0])
+        n = hq.hqq_kv_accept(pool.layers, i32(torch, table), i32(torch, lens), i32(torch, accepted), i32(torch, counts), **kw)
+        want = accept_plain(pool, table.tolist(), lens, new, accepted.tolist(), counts)
+        assert n.tolist() == want
+        pool.check("accepted")

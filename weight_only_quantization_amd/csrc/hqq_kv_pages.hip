@@ -64,94 +64,149 @@ __global__ __launch_bounds__(256) void k_tree_plan(TreePlanArgs a) {
   }
 }
 
-// ---- accepted drafts.  What a token has in a head's block is at most 8 pieces of 16 bytes (K codes), 16 of 2, 4 or 8 (V codes)
-// and 8 of 4 (metadata): half a wave a token and head, a piece a lane; a block takes 8 of them at a time and kAhead such
-// turns before it stores the first, since a token's new place may be another one's old place.  The accepted
-// drafts rise, so nothing that a later turn reads is stored by an earlier one.
-constexpr int kAhead = 8;
+// ---- accepted drafts.  The places that they go to are taken 16 at a time, aligned, so on one page: a wave takes those of a layer and head,
+// loads all that moves there and then stores it.  The accepted drafts rise, so nothing that later places need is stored by earlier
+// ones.  Lanes lie so that few lines are touched, which is what bounds this (a 4-byte piece of a line costs as much as the line): K codes
+// 16 bytes of a token a lane; V codes one of 16 places of four tokens a lane, stored at once with what the others of the four
+// hold; metadata the tokens of one word side by side (128 drafts, 5 tokens each, 32 layers of 8 heads: 28 us, 36 with
+// half a wave a token, a piece a lane, and as many stores).
+// The tokens' places are looked up first, a thread a token, once for the layers and heads of a block.
+constexpr int kWindow = 256;
 
-// Byte offset and size of piece i of token t; size 0: none.
-struct Piece {
-  int at, size;
-};
-__device__ __forceinline__ Piece piece_of(const Bytes& b, int page, int t, int i) {
-  if (i < 8) return {t * b.row + 16 * i, 16 * i < b.row ? 16 : 0};
-  if (i < 24) return {page * b.row + (((t >> 2) * 16 + i - 8) * 4 + (t & 3)) * b.unit, b.unit};
-  return {2 * page * b.row + ((i - 24) * page + t) * 4, i - 24 < b.meta ? 4 : 0};
-}
-__device__ __forceinline__ u32x4 load_piece(const uint8_t* p, int size) {
-  u32x4 v = {0, 0, 0, 0};
-  if (size == 16) {
-    v = *reinterpret_cast<const u32x4*>(p);
-  } else if (size == 8) {
-    const u32x2 w = *reinterpret_cast<const u32x2*>(p);
-    v[0] = w[0], v[1] = w[1];
-  } else if (size == 4) {
-    v[0] = *reinterpret_cast<const uint32_t*>(p);
-  } else if (size == 2) {
-    v[0] = *reinterpret_cast<const uint16_t*>(p);
-  }
-  return v;
-}
-__device__ __forceinline__ void store_piece(uint8_t* p, int size, u32x4 v) {
-  if (size == 16)
-    *reinterpret_cast<u32x4*>(p) = v;
-  else if (size == 8)
-    *reinterpret_cast<u32x2*>(p) = u32x2{v[0], v[1]};
-  else if (size == 4)
-    *reinterpret_cast<uint32_t*>(p) = v[0];
-  else if (size == 2)
-    *reinterpret_cast<uint16_t*>(p) = (uint16_t)v[0];
+template <typename T>
+__device__ __forceinline__ T load_as(const uint8_t* p) {
+  return *reinterpret_cast<const T*>(p);
 }
 
-// The tokens' places are looked up first, a thread a token, so that no piece waits for a chain of its own.
-constexpr int kChosen = 256;
-
-__global__ __launch_bounds__(256) void k_accept(AcceptArgs a, int heads) {
-  __shared__ int sh_id[2][kChosen], sh_token[2][kChosen];  // from, to: page (-1: nothing to move) and token of the page
-  const int seq = blockIdx.x, layer = blockIdx.y, head0 = blockIdx.z * heads;
-  const int here = min(heads, a.f.hkv - head0);
+// UNIT: bytes of a token's V codes in one of 16 places; a token's K codes are as many pieces of 16 bytes.  NM: loads of metadata, of four
+// words a token each.
+template <int UNIT, int NM>
+__global__ __launch_bounds__(256) void k_accept(AcceptArgs a, int per_block) {
+  constexpr int ROW = 16 * UNIT;
+  constexpr int NK = (16 * UNIT + 63) / 64;  // loads of K codes
+  constexpr int NV = UNIT == 8 ? 2 : 1;      // 16-byte pieces (UNIT 2: one of 8) of four tokens' V codes in a place
+  __shared__ int sh_id[kWindow], sh_token[kWindow];  // where a place's token comes from: page (-1: nothing to move) and token of it
+  __shared__ int sh_to[kWindow / 16];                // page of 16 places; -1: nothing to move
+  const int seq = blockIdx.x, lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int items = a.num_layers * a.f.hkv, item0 = blockIdx.y * per_block, item1 = min(item0 + per_block, items);
   const Drafts d = drafts_of(a, seq);
   const int len = length_of(a.seqs, seq, a.f.page_shift), base = len - d.count;
-  const int count = min(min(max(a.num_accepted[seq], 0), a.most), d.count);
-  if (layer == 0 && blockIdx.z == 0 && threadIdx.x == 0) a.new_lens[seq] = max(base + count, 0);
-  const int page = 1 << a.f.page_shift, piece = threadIdx.x & 31;
+  const int count = min(min(max(a.num_accepted[seq], 0), a.most), d.count), end = base + count;
+  if (blockIdx.y == 0 && threadIdx.x == 0) a.new_lens[seq] = max(end, 0);
+  const int page = 1 << a.f.page_shift;
   const int32_t* chosen = a.accepted + (int64_t)seq * a.accepted_stride;
   const int32_t* table = a.seqs.table + (int64_t)seq * a.seqs.table_stride;
-  uint8_t* pages = a.layers.pages[layer];
-  const int size = piece_of(a.b, page, 0, piece).size;
-  for (int j0 = 0; j0 < count; j0 += kChosen) {
-    if (j0) __syncthreads();
-    const int j = j0 + threadIdx.x;
-    if (j < count) {
-      const int from = chosen[j], src = base + from, dst = base + j;
-      int id = -1, to = -1;
-      if (from != j && from >= 0 && from < d.count && src >= 0 && dst >= 0 && src < len && dst < len) {
-        id = table[src >> a.f.page_shift], to = table[dst >> a.f.page_shift];
-        if ((uint32_t)id >= a.f.num_pages || (uint32_t)to >= a.f.num_pages) id = -1;
+  const int first = max(base, 0) & ~15;
+  for (int p0 = first; p0 < end; p0 += kWindow) {
+    if (p0 != first) __syncthreads();
+    {
+      const int pos = p0 + threadIdx.x, j = pos - base;
+      int id = -1, to = -1, src = 0;
+      if (j >= 0 && j < count) {
+        const int from = chosen[j];
+        src = base + from;
+        if (from != j && from >= 0 && from < d.count && src >= 0) {
+          id = table[src >> a.f.page_shift], to = table[pos >> a.f.page_shift];
+          if ((uint32_t)id >= a.f.num_pages || (uint32_t)to >= a.f.num_pages) id = -1;
+        }
       }
-      sh_id[0][threadIdx.x] = id, sh_id[1][threadIdx.x] = to;
-      sh_token[0][threadIdx.x] = src & (page - 1), sh_token[1][threadIdx.x] = dst & (page - 1);
+      sh_id[threadIdx.x] = id, sh_token[threadIdx.x] = src & (page - 1);
+      const uint32_t moved = (uint32_t)(__ballot(id >= 0) >> (lane & 48)) & 0xffff;
+      if (moved ? (lane & 15) == __builtin_ctz(moved) : (lane & 15) == 0) sh_to[threadIdx.x >> 4] = moved ? to : -1;
     }
     __syncthreads();
-    const int pairs = min(count - j0, kChosen) * here;  // of a token and a head, tokens in order
-    for (int p0 = 0; p0 < pairs; p0 += 8 * kAhead) {
-      u32x4 v[kAhead];
-      uint8_t* to[kAhead];
+    for (int i = item0 + wave; i < item1; i += 4) {
+      const int layer = i / a.f.hkv, head = i - layer * a.f.hkv;
+      uint8_t* block = a.layers.pages[layer] + head * a.f.block_bytes;  // (of page 0)
+      for (int c = 0; c < kWindow / 16 && p0 + 16 * c < end; ++c) {
+        const int to = __builtin_amdgcn_readfirstlane(sh_to[c]);
+        if (to < 0) continue;
+        uint8_t* dst = block + (int64_t)to * a.f.page_bytes;
+        const int at = (p0 + 16 * c) & (page - 1);
+        // All loads are without a branch, and so in flight together: a lane with nothing to move reads the block's first bytes.
+        u32x4 k[NK];
+        bool on_k[NK];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        to[k] = nullptr;
-        const int p = p0 + 8 * k + (threadIdx.x >> 5);
-        if (p >= pairs || size == 0) continue;
-        const int j = p / here, head = head0 + p - j * here, id = sh_id[0][j];
-        if (id < 0) continue;
-        v[k] = load_piece(pages + (int64_t)id * a.f.page_bytes + head * a.f.block_bytes + piece_of(a.b, page, sh_token[0][j], piece).at, size);
-        to[k] = pages + (int64_t)sh_id[1][j] * a.f.page_bytes + head * a.f.block_bytes + piece_of(a.b, page, sh_token[1][j], piece).at;
+        for (int n = 0; n < NK; ++n) {
+          const int x = lane + 64 * n, t = (16 * c + x / UNIT) & (kWindow - 1), id = sh_id[t];
+          on_k[n] = x < 16 * UNIT && id >= 0;
+          k[n] = load_as<u32x4>(on_k[n] ? block + (int64_t)id * a.f.page_bytes + sh_token[t] * ROW + 16 * (x % UNIT) : dst);
+        }
+        const int quad = lane >> 4, place = lane & 15;
+        uint8_t* v_dst = dst + page * ROW + ((at / 4 + quad) * 16 + place) * 4 * UNIT;
+        uint32_t v[4][UNIT == 8 ? 2 : 1];
+        int moved = 0;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          const int t = 16 * c + 4 * quad + n, id = sh_id[t], token = sh_token[t];
+          moved |= (id >= 0) << n;
+          const uint8_t* p = block + (int64_t)id * a.f.page_bytes + page * ROW + (((token >> 2) * 16 + place) * 4 + (token & 3)) * UNIT;
+          if (id < 0) p = dst;
+          if (UNIT == 2) v[n][0] = load_as<uint16_t>(p);
+          if (UNIT == 4) v[n][0] = load_as<uint32_t>(p);
+          if (UNIT == 8) {
+            const u32x2 x = load_as<u32x2>(p);
+            v[n][0] = x[0], v[n][UNIT == 8 ? 1 : 0] = x[1];
+          }
+        }
+        uint32_t old[UNIT];  // what the four tokens' place holds now, where some of them stay
+        const uint8_t* v_old = moved && moved != 15 ? v_dst : dst;
+        if (UNIT == 2) {
+          const u32x2 x = load_as<u32x2>(v_old);
+          old[0] = x[0], old[1] = x[1];
+        } else {
+#pragma unroll
+          for (int n = 0; n < NV; ++n) {
+            const u32x4 x = load_as<u32x4>(v_old + 16 * n);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) old[(4 * n + e) % UNIT] = x[e];
+          }
+        }
+        uint32_t m[NM];
+        bool on_m[NM];
+#pragma unroll
+        for (int n = 0; n < NM; ++n) {
+          const int x = lane + 64 * n, t = 16 * c + (x & 15), word = x >> 4, id = sh_id[t];
+          on_m[n] = word < a.b.meta && id >= 0;
+          m[n] = load_as<uint32_t>(on_m[n] ? block + (int64_t)id * a.f.page_bytes + 2 * page * ROW + (word * page + sh_token[t]) * 4 : dst);
+        }
+        // (the wave's loads before its stores)
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int n = 0; n < NK; ++n)
+          if (on_k[n]) *reinterpret_cast<u32x4*>(dst + at * ROW + 16 * (lane + 64 * n)) = k[n];
+        if (moved) {
+          if (UNIT == 2) {
+            u32x2 x;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t low = moved >> (2 * e) & 1 ? v[2 * e][0] : old[e] & 0xffffu;
+              const uint32_t high = moved >> (2 * e + 1) & 1 ? v[2 * e + 1][0] << 16 : old[e] & 0xffff0000u;
+              x[e] = low | high;
+            }
+            *reinterpret_cast<u32x2*>(v_dst) = x;
+          } else {
+#pragma unroll
+            for (int n = 0; n < NV; ++n) {
+              u32x4 x;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int w = 4 * n + e, token = 4 * w / UNIT;  // word of the place, and its token
+                x[e] = moved >> token & 1 ? v[token & 3][UNIT == 8 ? w & 1 : 0] : old[w % UNIT];
+              }
+              *reinterpret_cast<u32x4*>(v_dst + 16 * n) = x;
+            }
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NM; ++n) {
+          const int x = lane + 64 * n;
+          if (on_m[n]) *reinterpret_cast<uint32_t*>(dst + 2 * page * ROW + ((x >> 4) * page + at + (x & 15)) * 4) = m[n];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
       }
-      __syncthreads();
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (to[k]) store_piece(to[k], size, v[k]);
     }
   }
 }
@@ -398,10 +453,15 @@ hipError_t launch_tree_plan(const TreePlanArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_accept(const AcceptArgs& a, hipStream_t st) {
-  // heads of a block: eight, whose moves of up to eight tokens are one turn; fewer where that leaves CUs without a block
-  int heads = 8;
-  while (heads > 1 && (int64_t)a.seqs.count * a.num_layers * ((a.f.hkv + heads - 1) / heads) < 512) heads /= 2;
-  k_accept<<<dim3(a.seqs.count, a.num_layers, (a.f.hkv + heads - 1) / heads), 256, 0, st>>>(a, heads);
+  // layers and heads of a block: a wave each, or as many more as leave 4096 blocks (with 2048 32 us for 28, with 8192 the same)
+  const int items = a.num_layers * a.f.hkv;
+  int per = 4;
+  while (per < items && ((int64_t)a.seqs.count * ((items + 2 * per - 1) / (2 * per)) >= 4096 || (items + per - 1) / per > 65535)) per *= 2;
+  const dim3 grid(a.seqs.count, (items + per - 1) / per);
+#define X(u, nm) \
+  if (a.b.unit == u && (a.b.meta > 4) == (nm > 1)) k_accept<u, nm><<<grid, 256, 0, st>>>(a, per);
+  X(2, 1) X(4, 1) X(4, 2) X(8, 1) X(8, 2)
+#undef X
   return hipGetLastError();
 }
 
