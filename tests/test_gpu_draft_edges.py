@@ -230,3 +230,26 @@ def test_accept_long_lists(d, bits, g):
         want = accept_plain(pool, table.tolist(), lens, new, accepted.tolist(), counts)
         assert n.tolist() == want
         pool.check("accepted")
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_outputs_past_the_caches(inter):
+    """Outputs of 32 MiB and of one token more, which are stored past the caches: the bits of the same tokens in smaller calls; in place too."""
+    hq, torch = base.lib()
+    rng = np.random.default_rng(12)
+    t = hq.hqq_rope_table(64, interleaved=inter)
+    full = 1 << 12                                                       # tokens of 32 heads of 128 channels in 32 MiB
+    for n, dtype in ((full, torch.float16), (full + 1, torch.float16), (full + 77, torch.bfloat16)):
+        say("past the caches", inter, n)
+        pos = torch.from_numpy(rng.integers(0, 1 << 20, n)).cuda()
+        q = torch.randn(n, 32, 128, device="cuda").to(dtype)
+        k, v = torch.randn(n, 2, 128, device="cuda").to(dtype), torch.randn(n, 2, 128, device="cuda").to(dtype)
+        parts = torch.cat([hq.hqq_rope(q[i:i + 1000], pos[i:i + 1000], t) for i in range(0, n, 1000)])
+        assert torch.equal(hq.hqq_rope(q, pos, t), parts)
+        cache, other = hq.hqq_kv_cache(-(-n // 64), 2, 128), hq.hqq_kv_cache(-(-n // 64), 2, 128)
+        cache.pages.zero_(), other.pages.zero_()
+        slots = torch.arange(n, device="cuda")
+        assert torch.equal(hq.hqq_kv_write_rope(cache, q, k, v, pos, slots, t), parts)
+        hq.hqq_kv_write(other, hq.hqq_rope(k, pos, t), v, slots)
+        assert torch.equal(cache.pages, other.pages)
+        assert hq.hqq_rope(q, pos, t, out=q) is q and torch.equal(q, parts)

@@ -20,6 +20,7 @@ struct Heads {
   void* out;
   int64_t in_ts, in_hs, out_ts, out_hs;
   int count;
+  bool past;  // stores past the caches
 };
 
 struct RopeArgs {

@@ -50,6 +50,9 @@ int check_heads(const Heads& h, int64_t n, int channels) {
   return HQQ_OK;
 }
 
+// Outputs that the L2 caches (8 of 4 MB) do not hold until the next kernel reads them are stored past them.
+bool past_caches(int64_t n, int64_t heads, int64_t channels) { return n * heads * channels * 2 > (int64_t(32) << 20); }
+
 int check_count(int64_t n, int tokens) {
   KV_NEED(n >= 0, HQQ_ERR_INVALID_ARGUMENT, "n out of range");
   KV_NEED(n <= kThreads / 256 * tokens, HQQ_ERR_UNSUPPORTED, "too many tokens in a call");
@@ -146,8 +149,9 @@ int hqq_rope(const hqq_rope_args* x) {
   hqq::kv::RopeArgs a{};
   st = check_turn(x->form, x->positions, x->head_dim, x->backward, anything, &a.turn);
   if (st != HQQ_OK || !anything) return st;
-  a.q = Heads{x->q, x->q_out, x->q_token_stride, x->q_head_stride, x->q_out_token_stride, x->q_out_head_stride, x->q_heads};
-  a.k = Heads{x->k, x->k_out, x->k_token_stride, x->k_head_stride, x->k_out_token_stride, x->k_out_head_stride, x->k_heads};
+  a.q = Heads{x->q, x->q_out, x->q_token_stride, x->q_head_stride, x->q_out_token_stride, x->q_out_head_stride, x->q_heads, false};
+  a.k = Heads{x->k, x->k_out, x->k_token_stride, x->k_head_stride, x->k_out_token_stride, x->k_out_head_stride, x->k_heads, false};
+  a.q.past = a.k.past = past_caches(x->n, x->q_heads + x->k_heads, x->head_dim);
   a.n = x->n;
   a.head_dim = x->head_dim;
   for (const Heads* h : {&a.q, &a.k}) {
@@ -168,7 +172,8 @@ int hqq_kv_write_rope(const hqq_kv_write_rope_args* x) {
   if (st != HQQ_OK) return st;
   st = check_turn(x->form, x->positions, w.cache.head_dim, 0, w.n > 0, &a.turn);
   if (st != HQQ_OK || w.n == 0) return st;
-  a.q = Heads{x->q, x->q_out, x->q_token_stride, x->q_head_stride, x->q_out_token_stride, x->q_out_head_stride, x->q_heads};
+  a.q = Heads{x->q, x->q_out, x->q_token_stride, x->q_head_stride, x->q_out_token_stride, x->q_out_head_stride, x->q_heads, false};
+  a.q.past = past_caches(w.n, x->q_heads, w.cache.head_dim);
   st = check_heads(a.q, w.n, w.cache.head_dim);
   if (st != HQQ_OK) return st;
   return device_status(hqq::kv::launch_write_rope(a, w.cache.head_dim, w.cache.nbits, w.cache.group_size, w.dtype,
