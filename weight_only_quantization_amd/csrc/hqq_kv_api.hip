@@ -32,7 +32,7 @@ constexpr int64_t kWholeKeys = 2048;
 // `lists` times that many rows (KV heads times sequences) over `keys` keys.  17 rows and more take 32 a block, which
 // reads the keys for twice the rows, unless blocks of 16 are no more than the CUs: then those end sooner (16
 // sequences of 2001 keys, 5 tokens, 32 heads on 8: 19.6 us with 16 rows, 22.7 with 32; 12 tokens: 35 and 24).
-// More than 64 rows take tiles where there is work enough: a block of tiles takes 10 us to begin and end and 5 us
+// More than 64 rows take tiles where there is work enough: a block of tiles takes about 8 us to begin and end and 4.5 us
 // per 128 keys, while streams spread few keys over more and shorter blocks.  Time of the call streamed and in tiles by the
 // millions of pairs of a row and a key, over all KV heads and sequences: 0.36 (298 rows, 306 keys) 13 and 24 us, 3.0 (1290
 // rows) 14 and 28, 6.9 (1856 rows) 13 and 27, 12.5 (2160 rows, 721 keys) 19 and 34, 12.6 (70 rows, 5623 keys, 32 heads) 29 and 28,

@@ -10,15 +10,20 @@
 // (1024 + c) - 1024 is exact, fma(c, s, m) rounds once.
 // Softmax as in the stream kernel: one pass, fp32, the maximum raised only when a score passes it by 2^5.
 //
-// 2048 tokens on 8192 keys, 32 heads on 8, 4 bits: 240 Gflop in 280-298 us among such calls, by the card (303 in a trace), 0.81-0.86 Pflop/s; a
-// library product of two 8192 x 8192 fp16 matrices reaches 1.18.  Keys, values and weights in fp16 cost 6.9e-4 of the output (2-norm)
+// 2048 tokens on 8192 keys, 32 heads on 8, 4 bits: 240 Gflop in 270-287 us among such calls, by the card (304 in a trace), 0.84-0.89 Pflop/s; a
+// library product of two 8192 x 8192 fp16 matrices reaches 1.18-1.32.  Keys, values and weights in fp16 cost 6.9e-4 of the output (2-norm)
 // with the fp16 output's own 2.1e-4.  Per 32 x 32 scores a wave needs 512 cycles of
 // the matrix unit and about 600 of the vector unit (16 exponentials take 256); with K and V from LDS and
 // their unpacking it takes about 1500 of its SIMD, without either 920: the two waves of a SIMD overlap only in part.
+// Of a tile of 128 keys and 256 rows a wave's products and weights take 3.55 us of 4.5, unpacking 0.6, loads 0.24, the barrier 0.3; the
+// counters have the matrix unit busy for 43 % of the time and the vector unit for 56 %.
 // Padded rows against swizzled ones (an address a read less) 330 -> 312 us, the tile's two halves
-// unrolled and each half's values multiplied while the next half's weights are worked out -> 285-310.  Tried without
-// gain: operands read from LDS a phase ahead, 64 rows a wave with one wave a SIMD (480 us), wave
-// priorities around the products, a prescribed alternation of matrix and vector instructions.
+// unrolled and each half's values multiplied while the next half's weights are worked out -> 285-310, nothing loaded looked at
+// before its tile is unpacked 286 -> 272.  Tried without
+// gain: operands read from LDS a phase ahead or 2 to 6 reads ahead (259 against 263, 272 against 277 us: within the runs' spread), 64 rows
+// a wave with one wave a SIMD (480 us), wave priorities around the products, a prescribed alternation of matrix and vector
+// instructions, one half's weights between the other half's products (274-288 against 266), blocks of four waves on tiles of 64 keys. Two waves that alternate
+// such instructions by themselves take 619-678 ns a turn against 499 for the matrix part alone: little overlaps.
 #pragma once
 
 #include "hqq_kv.h"

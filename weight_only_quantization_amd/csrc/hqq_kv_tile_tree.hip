@@ -3,6 +3,10 @@
 // The batch's lengths differ, and a draft has few tiles of rows, so fixed key splits would leave the longest sequence's
 // blocks to run alone: the tiles of all (sequence, row tile, KV head) are cut into equal shares, one a block, as the stream's
 // units are (hqq_kv_stream.h), and pairs that several blocks share leave partial results for the join.
+//
+// 16 sequences of 200-4096 keys, 16-32 drafts, 32 heads on 8, 8 bits: 44 us, and 6 for the join; a block has 1.4 pieces, each of 7.5 us
+// beside 2.6 us a tile, and 2.2 us go by before it knows its first.  8 sequences of 9000-16384 keys, 64 drafts, 64 heads on 8, 4 bits:
+// 213 Gflop in 240-250 us between the calls of a row (0.87 Pflop/s, as the prompts' tiles), and 12 for the join.
 #include "hqq_kv_tile.h"
 
 namespace hqq {

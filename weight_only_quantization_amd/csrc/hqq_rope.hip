@@ -6,7 +6,10 @@
 // that is rounded like the separate calls' (and like a reference's) takes the same code where it lies next to a border.
 //
 // Both kernels move bytes; the cosines and sines of a block's tokens are worked out once, a pair or two a thread, and serve
-// all heads that the block's waves walk over.
+// all heads that the block's waves walk over.  16411 tokens of 64 heads of 128 channels (538 MB): 95 us, 5.7 TB/s, where a large copy has
+// 5.8-6.1; 64 bits cost nothing there (105 and 107 us at an earlier step).  16387 prompt tokens of 64 query heads on 8 into a cache of
+// 8 bits with their echo (707 MB): 129 us, 5.5 TB/s.  A step of 64 tokens of 40 heads takes 4.3 us, the chain position -> angle ->
+// pair -> store, and the host's call three times that.
 #include "hqq_draft.h"
 #include "hqq_kv_quant.h"
 
@@ -100,7 +103,8 @@ __device__ __forceinline__ void turn_runs(const Lane& l, const double2 (&cs)[8],
 }
 
 // Heads first + lane_head, then every `step` further, two steps' loads in flight.  Loads past the caches (16411 tokens, 538 MB into
-// ever new outputs: 103 us for 108), and stores where there is much (Heads::past: 95 for 103).
+// ever new outputs: 103 us for 108), and stores where there is much (Heads::past: 95 for 103; calls that reuse one output, half of
+// which the last cache then holds, lose by it: 94 for 85).
 template <bool BF16, bool INTER, bool PAST>
 __device__ __forceinline__ void turn_heads_to(const Heads& x, int64_t token, int first, int step, const Lane& l, const double2 (&cs)[8]) {
   const uint16_t* from = reinterpret_cast<const uint16_t*>(x.in) + token * x.in_ts;
