@@ -8,7 +8,7 @@
 // Both kernels move bytes; the cosines and sines of a block's tokens are worked out once, a pair or two a thread, and serve
 // all heads that the block's waves walk over.  16411 tokens of 64 heads of 128 channels (538 MB): 95 us, 5.7 TB/s, where a large copy has
 // 5.8-6.1; 64 bits cost nothing there (105 and 107 us at an earlier step).  16387 prompt tokens of 64 query heads on 8 into a cache of
-// 8 bits with their echo (707 MB): 129 us, 5.5 TB/s.  A step of 64 tokens of 40 heads takes 4.3 us, the chain position -> angle ->
+// 8 bits with their echo (707 MB): 126 us, 5.6 TB/s.  A step of 64 tokens of 40 heads takes 4.3 us, the chain position -> angle ->
 // pair -> store, and the host's call three times that.
 #include "hqq_draft.h"
 #include "hqq_kv_quant.h"
@@ -45,118 +45,143 @@ __device__ __forceinline__ void turn_pair(float& a, float& b, double2 cs) {
   b = (float)fma(x, cs.y, y * cs.x);
 }
 
-// How a wave takes the heads of a token: a lane owns two runs of 8 channels of a head (at0, at1) that make whole pairs, `per` heads
-// side by side are a wave's step, and `lane_head` is the lane's among them (per where the lane has none).  So a wave walks through a
-// token's heads as they lie in memory.
+// A lane's part of a head, 8 channels, `per` heads side by side in a wave: what a wave loads and stores at a time lies together.
+// Halves: the other channels of its pairs are another lane's.
 struct Lane {
-  int at0, at1, per, lane_head;
-  bool t0, t1;  // whether the runs are turned (else copied)
+  int at, per, head;    // first channel; heads of a wave's step; the lane's among them (per: none)
+  bool turned, first;   // whether the channels are turned (else copied); whether they are in the first half of what is
+  int partner;          // lane that has the other half
 };
 template <bool INTER>
 __device__ __forceinline__ Lane lane_of(int head_dim, int rot, int lane) {
-  const int units = head_dim / 16, u = lane % units;
+  const int pieces = head_dim / 8, u = lane % pieces;
   Lane l;
-  l.per = 64 / units;
-  l.lane_head = lane / units;
-  if (INTER) {
-    l.at0 = 8 * u, l.at1 = 8 * (u + units);
-    l.t0 = l.at0 < rot, l.t1 = l.at1 < rot;
-  } else {
-    l.t0 = l.t1 = 16 * u < rot;
-    l.at0 = l.t0 ? 8 * u : 16 * u, l.at1 = l.t0 ? rot / 2 + 8 * u : 16 * u + 8;
-  }
+  l.at = 8 * u, l.per = 64 / pieces, l.head = lane / pieces;
+  l.turned = l.at < rot, l.first = l.at < rot / 2;
+  l.partner = INTER || !l.turned ? lane : l.first ? lane + rot / 16 : lane - rot / 16;
   return l;
 }
-// The lane's pairs of a token, whose table this is: of run 0 (halves: of both runs), and of run 1.
+// The cosines and sines of the lane's channels, from a token's table.  Halves: a channel is own c + other s, the sine with the sign that
+// the half's formula gives it.
 template <bool INTER>
-__device__ __forceinline__ void lane_pairs(const double2* tab, int rot, const Lane& l, double2 (&cs)[8]) {
+__device__ __forceinline__ void lane_pairs(const double2* tab, int rot, const Lane& l, double2 (&cs)[INTER ? 4 : 8]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const bool on = INTER && j >= 4 ? l.t1 : l.t0;
-    const int i = !INTER ? l.at0 + j : j < 4 ? l.at0 / 2 + j : l.at1 / 2 + j - 4;
-    cs[j] = tab[on ? pair_at(rot, i) : 0];
+  for (int j = 0; j < (INTER ? 4 : 8); ++j) {
+    const int i = (INTER ? l.at / 2 : l.first ? l.at : l.at - rot / 2) + j;
+    cs[j] = tab[l.turned ? pair_at(rot, i) : 0];
+    if (!INTER && l.first) cs[j].y = -cs[j].y;
   }
 }
-
+// The lane's channels turned, as they lie (all lanes of the wave take part).
 template <bool BF16, bool INTER>
-__device__ __forceinline__ void turn_runs(const Lane& l, const double2 (&cs)[8], u32x4& w0, u32x4& w1) {
-  float x[8], y[8];
-  floats8<BF16>(w0, x);
-  floats8<BF16>(w1, y);
+__device__ __forceinline__ u32x4 turned_of(const Lane& l, const double2 (&cs)[INTER ? 4 : 8], u32x4 w) {
+  float x[8];
+  floats8<BF16>(w, x);
   if (INTER) {
-    if (l.t0) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) turn_pair(x[2 * j], x[2 * j + 1], cs[j]);
-      w0 = pack8<BF16>(x);
-    }
-    if (l.t1) {
+    for (int j = 0; j < 4; ++j) turn_pair(x[2 * j], x[2 * j + 1], cs[j]);
+  } else {
+    u32x4 v;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) turn_pair(y[2 * j], y[2 * j + 1], cs[4 + j]);
-      w1 = pack8<BF16>(y);
-    }
-  } else if (l.t0) {
+    for (int j = 0; j < 4; ++j) v[j] = __shfl((int)w[j], l.partner);
+    float y[8];
+    floats8<BF16>(v, y);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) turn_pair(x[j], y[j], cs[j]);
-    w0 = pack8<BF16>(x);
-    w1 = pack8<BF16>(y);
+    for (int j = 0; j < 8; ++j) x[j] = (float)fma((double)y[j], cs[j].y, (double)x[j] * cs[j].x);
   }
+  const u32x4 r = pack8<BF16>(x);
+  return l.turned ? r : w;
 }
 
-// Heads first + lane_head, then every `step` further, two steps' loads in flight.  Loads past the caches (16411 tokens, 538 MB into
+// Heads first + head, then every `step` further, four steps' loads in flight (16000 tokens of 128 heads of 64 channels: 95 us, 114 with a lane's
+// channels in two places, whose stores then were half lines; 32 heads of 256, 64 of them turned: 93 and 130; of 80 channels, whose steps of six heads end
+// inside a line: 117-134 and 176-189).  Loads past the caches (16411 tokens, 538 MB into
 // ever new outputs: 103 us for 108), and stores where there is much (Heads::past: 95 for 103; calls that reuse one output, half of
 // which the last cache then holds, lose by it: 94 for 85).
 template <bool BF16, bool INTER, bool PAST>
-__device__ __forceinline__ void turn_heads_to(const Heads& x, int64_t token, int first, int step, const Lane& l, const double2 (&cs)[8]) {
-  const uint16_t* from = reinterpret_cast<const uint16_t*>(x.in) + token * x.in_ts;
-  uint16_t* to = reinterpret_cast<uint16_t*>(x.out) + token * x.out_ts;
-  for (int h0 = first; h0 < x.count; h0 += 2 * step) {
-    u32x4 w[2][2];
-    bool on[2];
+__device__ __forceinline__ void turn_heads_to(const Heads& x, int64_t token, int first, int step, const Lane& l,
+                                              const double2 (&cs)[INTER ? 4 : 8]) {
+  constexpr int U = 4;
+  const uint16_t* from = reinterpret_cast<const uint16_t*>(x.in) + token * x.in_ts + l.at;
+  uint16_t* to = reinterpret_cast<uint16_t*>(x.out) + token * x.out_ts + l.at;
+  auto load = [&](int h) {
+    u32x4 w = {0, 0, 0, 0};
+    if (l.head < l.per && h < x.count) w = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + h * x.in_hs));
+    return w;
+  };
+  u32x4 w[U];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int h = h0 + k * step + l.lane_head;
-      on[k] = l.lane_head < l.per && h < x.count;
-      if (on[k]) {
-        w[k][0] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + h * x.in_hs + l.at0));
-        w[k][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(from + h * x.in_hs + l.at1));
-      }
-    }
+  for (int k = 0; k < U; ++k) w[k] = load(first + k * step + l.head);
+  for (int h0 = first; h0 < x.count; h0 += U * step) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      if (!on[k]) continue;
-      const int h = h0 + k * step + l.lane_head;
-      turn_runs<BF16, INTER>(l, cs, w[k][0], w[k][1]);
-      u32x4 *to0 = reinterpret_cast<u32x4*>(to + h * x.out_hs + l.at0), *to1 = reinterpret_cast<u32x4*>(to + h * x.out_hs + l.at1);
-      if (PAST) {
-        __builtin_nontemporal_store(w[k][0], to0);
-        __builtin_nontemporal_store(w[k][1], to1);
-      } else {
-        *to0 = w[k][0];
-        *to1 = w[k][1];
-      }
+    for (int k = 0; k < U; ++k) {
+      if (h0 + k * step >= x.count) break;
+      const int h = h0 + k * step + l.head;
+      const u32x4 r = turned_of<BF16, INTER>(l, cs, w[k]);
+      w[k] = load(h + U * step);
+      if (l.head >= l.per || h >= x.count) continue;
+      if (PAST)
+        __builtin_nontemporal_store(r, reinterpret_cast<u32x4*>(to + h * x.out_hs));
+      else
+        *reinterpret_cast<u32x4*>(to + h * x.out_hs) = r;
     }
   }
 }
-
 template <bool BF16, bool INTER>
-__device__ __forceinline__ void turn_heads(const Heads& x, int64_t token, int first, int step, const Lane& l, const double2 (&cs)[8]) {
+__device__ __forceinline__ void turn_heads(const Heads& x, int64_t token, int first, int step, const Lane& l, const double2 (&cs)[INTER ? 4 : 8]) {
   if (x.past)
     turn_heads_to<BF16, INTER, true>(x, token, first, step, l, cs);
   else
     turn_heads_to<BF16, INTER, false>(x, token, first, step, l, cs);
 }
 
-// A wave a token, or every fourth of the block's.
+// Heads of more than 512 channels: a wave a head, whose lanes take pairs that are in two places, 8 channels each.
 template <bool BF16, bool INTER>
+__device__ __forceinline__ void turn_wide(const Heads& x, int64_t token, int first, int step, int head_dim, int rot, const double2* tab) {
+  const int u = threadIdx.x & 63, units = head_dim / 16;
+  const int at0 = INTER ? 8 * u : 16 * u < rot ? 8 * u : 16 * u, at1 = INTER ? 8 * (u + units) : 16 * u < rot ? rot / 2 + 8 * u : 16 * u + 8;
+  for (int h = first; h < x.count; h += step) {
+    if (u >= units) continue;
+    const uint16_t* from = reinterpret_cast<const uint16_t*>(x.in) + token * x.in_ts + h * x.in_hs;
+    uint16_t* to = reinterpret_cast<uint16_t*>(x.out) + token * x.out_ts + h * x.out_hs;
+    const u32x4 w0 = *reinterpret_cast<const u32x4*>(from + at0), w1 = *reinterpret_cast<const u32x4*>(from + at1);
+    float a[8], b[8];
+    floats8<BF16>(w0, a);
+    floats8<BF16>(w1, b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (INTER) {
+        const int at = j < 4 ? at0 + 2 * j : at1 + 2 * j - 8;
+        if (at < rot) turn_pair(j < 4 ? a[2 * j] : b[2 * j - 8], j < 4 ? a[2 * j + 1] : b[2 * j - 7], tab[pair_at(rot, at / 2)]);
+      } else if (16 * u < rot) {
+        turn_pair(a[j], b[j], tab[pair_at(rot, at0 + j)]);
+      }
+    }
+    // (what is copied is copied as it lies, NaN's bits too)
+    const bool t0 = at0 < rot, t1 = INTER ? at1 < rot : t0;
+    *reinterpret_cast<u32x4*>(to + at0) = t0 ? pack8<BF16>(a) : w0;
+    *reinterpret_cast<u32x4*>(to + at1) = t1 ? pack8<BF16>(b) : w1;
+  }
+}
+
+// A wave a token, or every fourth of the block's.
+template <bool BF16, bool INTER, bool WIDE>
 __global__ __launch_bounds__(256) void k_rope(RopeArgs a, int tokens) {
   __shared__ double2 tab[kTab];
   const int64_t token0 = (int64_t)blockIdx.x * tokens;
   make_table(a.turn, token0, tokens, a.n, tab);
   __syncthreads();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (WIDE) {
+    // (a token a block: its heads to the four waves)
+    const int first = blockIdx.y * 4 + wave, step = gridDim.y * 4;
+    turn_wide<BF16, INTER>(a.q, token0, first, step, a.head_dim, a.turn.rot, tab);
+    turn_wide<BF16, INTER>(a.k, token0, first, step, a.head_dim, a.turn.rot, tab);
+    return;
+  }
   const Lane l = lane_of<INTER>(a.head_dim, a.turn.rot, threadIdx.x & 63);
   for (int t = wave; t < tokens && token0 + t < a.n; t += 4) {
-    double2 cs[8];
+    double2 cs[INTER ? 4 : 8];
     lane_pairs<INTER>(tab + t * (a.turn.rot / 2), a.turn.rot, l, cs);
     turn_heads<BF16, INTER>(a.q, token0 + t, blockIdx.y * l.per, gridDim.y * l.per, l, cs);
     turn_heads<BF16, INTER>(a.k, token0 + t, blockIdx.y * l.per, gridDim.y * l.per, l, cs);
@@ -191,37 +216,16 @@ __global__ __launch_bounds__(256) void k_write_rope(WriteRopeArgs a) {
   make_table(a.turn, token0, TOKENS, n, tab);
   __syncthreads();
   const int rot = a.turn.rot, half = rot / 2;
+  const Lane l = lane_of<INTER>(D, rot, lane);  // (its heads are tokens here)
   {
-  const bool turned = 8 * o < rot, first = 8 * o < half;
-  const int partner = t * OCT + (INTER || !turned ? o : first ? o + rot / 16 : o - rot / 16);
-  // halves: own c + other s, the sine with the sign that the half's formula gives it
   double2 cs[INTER ? 4 : 8];
-#pragma unroll
-  for (int j = 0; j < (INTER ? 4 : 8); ++j) {
-    cs[j] = tab[!turned ? 0 : t * half + pair_at(rot, (INTER ? 4 * o : first ? 8 * o : 8 * o - half) + j)];
-    if (!INTER && first) cs[j].y = -cs[j].y;
-  }
+  lane_pairs<INTER>(tab + t * half, rot, l, cs);
   auto take = [&](int i, u32x4 w) {
     const bool is_k = i < hkv;
     const int head = is_k ? i : i - hkv;
+    if (is_k) w = turned_of<BF16, INTER>(l, cs, w);
     float x[8];
     floats8<BF16>(w, x);
-    if (is_k) {
-      if (INTER) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) turn_pair(x[2 * j], x[2 * j + 1], cs[j]);
-      } else {
-        u32x4 v;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = __shfl((int)w[j], partner);
-        float y[8];
-        floats8<BF16>(v, y);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = (float)fma((double)y[j], cs[j].y, (double)x[j] * cs[j].x);
-      }
-      const u32x4 r = pack8<BF16>(x);
-      floats8<BF16>(turned ? r : w, x);
-    }
     int c[8], at;
     const uint32_t m = quantise<BITS, GS>(x, c);
     uint8_t* block = there ? slot_block(a.w.f, slot, head, &at) : nullptr;
@@ -245,13 +249,10 @@ __global__ __launch_bounds__(256) void k_write_rope(WriteRopeArgs a) {
     w = next;
   }
   }
-  {
-    const Lane l = lane_of<INTER>(D, rot, lane);
-    for (int i = wave; i < TOKENS && token0 + i < n; i += 4) {
-      double2 cs[8];
-      lane_pairs<INTER>(tab + i * half, rot, l, cs);
-      turn_heads<BF16, INTER>(a.q, token0 + i, blockIdx.y * l.per, gridDim.y * l.per, l, cs);
-    }
+  for (int i = wave; i < TOKENS && token0 + i < n; i += 4) {
+    double2 cs[INTER ? 4 : 8];
+    lane_pairs<INTER>(tab + i * half, rot, l, cs);
+    turn_heads<BF16, INTER>(a.q, token0 + i, blockIdx.y * l.per, gridDim.y * l.per, l, cs);
   }
 }
 
@@ -265,7 +266,7 @@ dim3 rope_grid(int64_t n, int tokens, int most) {
 
 template <int D, int BITS, int GS>
 hipError_t write_rope_t(const WriteRopeArgs& a, int dtype, bool inter, hipStream_t st) {
-  const int per = 64 / (D / 16), q = (a.q.count + per - 1) / per, kv = (2 * a.w.f.hkv + 3) / 4;
+  const int per = 64 / (D / 8), q = (a.q.count + per - 1) / per, kv = (2 * a.w.f.hkv + 3) / 4;
   const dim3 grid = rope_grid(a.w.n, write_rope_tokens(D), q > kv ? q : kv);
   if (dtype == HQQ_KV_BF16) {
     inter ? k_write_rope<D, BITS, GS, true, true><<<grid, 256, 0, st>>>(a)
@@ -279,14 +280,19 @@ hipError_t write_rope_t(const WriteRopeArgs& a, int dtype, bool inter, hipStream
 
 }  // namespace
 
-hipError_t launch_rope(const RopeArgs& a, int dtype, bool inter, hipStream_t st) {
-  const int tokens = rope_tokens(a.head_dim), per = 64 / (a.head_dim / 16);
+template <bool WIDE>
+static hipError_t rope_t(const RopeArgs& a, int dtype, bool inter, int per, hipStream_t st) {
+  const int tokens = rope_tokens(a.head_dim);
   const dim3 grid = rope_grid(a.n, tokens, ((a.q.count > a.k.count ? a.q.count : a.k.count) + per - 1) / per);
   if (dtype == HQQ_KV_BF16)
-    inter ? k_rope<true, true><<<grid, 256, 0, st>>>(a, tokens) : k_rope<true, false><<<grid, 256, 0, st>>>(a, tokens);
+    inter ? k_rope<true, true, WIDE><<<grid, 256, 0, st>>>(a, tokens) : k_rope<true, false, WIDE><<<grid, 256, 0, st>>>(a, tokens);
   else
-    inter ? k_rope<false, true><<<grid, 256, 0, st>>>(a, tokens) : k_rope<false, false><<<grid, 256, 0, st>>>(a, tokens);
+    inter ? k_rope<false, true, WIDE><<<grid, 256, 0, st>>>(a, tokens) : k_rope<false, false, WIDE><<<grid, 256, 0, st>>>(a, tokens);
   return hipGetLastError();
+}
+
+hipError_t launch_rope(const RopeArgs& a, int dtype, bool inter, hipStream_t st) {
+  return a.head_dim > 512 ? rope_t<true>(a, dtype, inter, 4, st) : rope_t<false>(a, dtype, inter, 64 / (a.head_dim / 8), st);
 }
 
 hipError_t launch_write_rope(const WriteRopeArgs& a, int D, int bits, int gs, int dtype, bool inter, hipStream_t st) {
