@@ -6,9 +6,9 @@
 // that is rounded like the separate calls' (and like a reference's) takes the same code where it lies next to a border.
 //
 // Both kernels move bytes; the cosines and sines of a block's tokens are worked out once, a pair or two a thread, and serve
-// all heads that the block's waves walk over.  16411 tokens of 64 heads of 128 channels (538 MB): 95 us, 5.7 TB/s, where a large copy has
+// all heads that the block's waves walk over.  16411 tokens of 64 heads of 128 channels (538 MB): 94 us, 5.7 TB/s, where a large copy has
 // 5.8-6.1; 64 bits cost nothing there (105 and 107 us at an earlier step).  16387 prompt tokens of 64 query heads on 8 into a cache of
-// 8 bits with their echo (707 MB): 126 us, 5.6 TB/s.  A step of 64 tokens of 40 heads takes 4.3 us, the chain position -> angle ->
+// 8 bits with their echo (707 MB): 124-126 us, 5.7 TB/s.  A step of 64 tokens of 40 heads takes 4.3 us, the chain position -> angle ->
 // pair -> store, and the host's call three times that.
 #include "hqq_draft.h"
 #include "hqq_kv_quant.h"
